@@ -8,6 +8,7 @@
 
 #include "adam_math.h"
 #include "gs_internal.h"
+#include "matrix.h"
 #include "profile.h"
 
 namespace {
@@ -145,6 +146,54 @@ PreWs carve_pre(void* ws, int64_t n) {
 // while the depth order is computed.
 int32_t finish_preprocess(gs_proj* out, int n, float znear, const PreWs& w, uint32_t* total_pairs, hipStream_t s);
 
+// ---- matrices of the network operators
+
+constexpr int64_t kMaxCols = int64_t(1) << 20;
+inline bool width_ok(int64_t c) { return c >= 1 && c <= kMaxCols; }
+
+constexpr int kF32 = 1 << GS_MAT_F32, kBF16 = 1 << GS_MAT_BF16, kMX8 = 1 << GS_MAT_MX8;
+
+// A matrix argument's own fields; types: the accepted ones (bits kF32 | kBF16 | kMX8).
+int32_t check_matrix(const gs_matrix* m, const char* name, int types) {
+  if (!m) return fail(GS_ERR_INVALID_ARG, "%s is null", name);
+  if (m->rows < 0 || m->rows >= (int64_t(1) << 31)) return fail(GS_ERR_INVALID_ARG, "%s: rows out of range", name);
+  if (m->cols < 1) return fail(GS_ERR_INVALID_ARG, "%s: cols must be positive", name);
+  if (m->cols > kMaxCols) return fail(GS_ERR_UNSUPPORTED, "%s: more than 2^20 columns", name);
+  if (m->type < GS_MAT_F32 || m->type > GS_MAT_MX8) return fail(GS_ERR_INVALID_ARG, "%s: unknown type", name);
+  if (!((types >> m->type) & 1)) return fail(GS_ERR_UNSUPPORTED, "%s: this type is not taken here", name);
+  if (m->ld < m->cols || m->ld > (int64_t(1) << 31)) return fail(GS_ERR_INVALID_ARG, "%s: ld out of range", name);
+  if (m->rows == 0) return GS_OK;
+  if (!m->data) return fail(GS_ERR_INVALID_ARG, "%s: data is null", name);
+  const uintptr_t unit = m->type == GS_MAT_F32 ? 4 : m->type == GS_MAT_BF16 ? 2 : 1;
+  if (reinterpret_cast<uintptr_t>(m->data) % unit) return fail(GS_ERR_INVALID_ARG, "%s: data is misaligned", name);
+  if (m->type == GS_MAT_MX8) {
+    if (!m->scales) return fail(GS_ERR_INVALID_ARG, "%s: scales is null", name);
+    if (m->scales_ld < (m->cols + 31) / 32 || m->scales_ld > (int64_t(1) << 31))
+      return fail(GS_ERR_INVALID_ARG, "%s: scales_ld out of range", name);
+  }
+  return GS_OK;
+}
+
+int32_t check_shape(const gs_matrix* m, const char* name, int types, int64_t rows, int64_t cols) {
+  const int32_t st = check_matrix(m, name, types);
+  if (st != GS_OK) return st;
+  if (m->rows != rows || m->cols != cols)
+    return fail(GS_ERR_INVALID_ARG, "%s is %lld x %lld, expected %lld x %lld", name, (long long)m->rows,
+                (long long)m->cols, (long long)rows, (long long)cols);
+  return GS_OK;
+}
+
+// Whether an output starts where another matrix does (the sharing a check on the host can
+// see without knowing the allocations).
+bool same_data(const gs_matrix* a, const gs_matrix* b) { return a && b && a->data && a->data == b->data; }
+
+// An output that may be the input itself has to have its type and ld.
+int32_t check_in_place(const gs_matrix* out, const gs_matrix* in, const char* name) {
+  if (same_data(out, in) && (out->type != in->type || out->ld != in->ld))
+    return fail(GS_ERR_INVALID_ARG, "%s in place of an input needs its type and ld", name);
+  return GS_OK;
+}
+
 // Pinned host word the pair count is copied into, and the event that marks the copy,
 // one per device and host thread, created on first use and kept for the process.
 struct HostSlot {
@@ -204,6 +253,8 @@ size_t gs_workspace_bytes(int32_t which_call, int64_t n, uint32_t pairs, int32_t
     case GS_WS_LOSS_CHARBONNIER: return (W > 0 && H > 0) ? gsk::charbonnier_ws_bytes(H, W) : 0;
     case GS_WS_CAMERA_GRAD: return gsk::camera_grad_ws_bytes(n < 0 ? 0 : n);
     case GS_WS_RELOCATE: return gsk::relocate_ws_bytes(n < 0 ? 0 : n);
+    case GS_WS_RMSNORM_BWD: return n >= 0 && width_ok(W) ? gsk::rmsnorm_bwd_ws_bytes(n, W) : 0;
+    case GS_WS_LINEAR_BWD: return n >= 0 && width_ok(W) && width_ok(H) ? gsk::linear_bwd_ws_bytes(n, W, H) : 0;
     default: return 0;
   }
 }
@@ -696,6 +747,131 @@ int32_t gs_loss_charbonnier(const float* img, const float* target, int32_t H, in
   const hipError_t e = gsk::launch_charbonnier(img, target, H, W, delta, exposure, loss_out, dL_dimg, dL_dexposure,
                                                ws, as_stream(stream));
   if (e != hipSuccess) return hip_fail(e, "loss_charbonnier");
+  return GS_OK;
+}
+
+int32_t gs_mx8_pack(const gs_matrix* x, const gs_matrix* q, void* stream) {
+  g_err[0] = 0;
+  int32_t st;
+  if ((st = check_matrix(x, "x", kF32 | kBF16)) != GS_OK) return st;
+  if ((st = check_shape(q, "q", kMX8, x->rows, x->cols)) != GS_OK) return st;
+  if (same_data(x, q)) return fail(GS_ERR_INVALID_ARG, "the output is one of the inputs");
+  if (x->rows == 0) return GS_OK;
+  const hipError_t e = gsk::launch_mx8_pack(gsk::mat_arg(x), gsk::mat_arg(q), x->rows, int(x->cols), as_stream(stream));
+  if (e != hipSuccess) return hip_fail(e, "mx8_pack");
+  return GS_OK;
+}
+
+int32_t gs_mx8_unpack(const gs_matrix* q, const gs_matrix* x, void* stream) {
+  g_err[0] = 0;
+  int32_t st;
+  if ((st = check_matrix(q, "q", kMX8)) != GS_OK) return st;
+  if ((st = check_shape(x, "x", kF32 | kBF16, q->rows, q->cols)) != GS_OK) return st;
+  if (same_data(x, q)) return fail(GS_ERR_INVALID_ARG, "the output is one of the inputs");
+  if (q->rows == 0) return GS_OK;
+  const hipError_t e =
+      gsk::launch_mx8_unpack(gsk::mat_arg(q), gsk::mat_arg(x), q->rows, int(q->cols), as_stream(stream));
+  if (e != hipSuccess) return hip_fail(e, "mx8_unpack");
+  return GS_OK;
+}
+
+int32_t gs_rmsnorm_fwd(const gs_matrix* x, const gs_matrix* residual, const float* weight, float eps,
+                       const gs_matrix* h, const gs_matrix* ckpt, const gs_matrix* y, float* rstd, void* stream) {
+  g_err[0] = 0;
+  int32_t st;
+  if ((st = check_matrix(x, "x", kF32 | kBF16)) != GS_OK) return st;
+  const int64_t rows = x->rows, cols = x->cols;
+  if (residual && (st = check_shape(residual, "residual", kF32 | kBF16, rows, cols)) != GS_OK) return st;
+  if (h && (st = check_shape(h, "h", kF32 | kBF16, rows, cols)) != GS_OK) return st;
+  if (ckpt && (st = check_shape(ckpt, "ckpt", kMX8, rows, cols)) != GS_OK) return st;
+  if ((st = check_shape(y, "y", kF32 | kBF16 | kMX8, rows, cols)) != GS_OK) return st;
+  if (!weight) return fail(GS_ERR_INVALID_ARG, "weight is null");
+  if (!(eps > 0.0f) || !std::isfinite(eps)) return fail(GS_ERR_INVALID_ARG, "eps must be positive");
+  if ((st = check_in_place(h, x, "h")) != GS_OK || (st = check_in_place(h, residual, "h")) != GS_OK) return st;
+  if (same_data(y, x) || same_data(y, residual) || same_data(y, h) || same_data(y, ckpt) || same_data(ckpt, x) ||
+      same_data(ckpt, residual) || same_data(ckpt, h))
+    return fail(GS_ERR_INVALID_ARG, "an output is one of the inputs or another output");
+  if (rows == 0) return GS_OK;
+  const hipError_t e = gsk::launch_rmsnorm_fwd(gsk::mat_arg(x), gsk::mat_arg(residual), weight, eps, gsk::mat_arg(h),
+                                               gsk::mat_arg(ckpt), gsk::mat_arg(y), rstd, rows, int(cols),
+                                               as_stream(stream));
+  if (e != hipSuccess) return hip_fail(e, "rmsnorm_fwd");
+  return GS_OK;
+}
+
+int32_t gs_rmsnorm_bwd(const gs_matrix* dy, const gs_matrix* h, const float* weight, const float* rstd,
+                       const gs_matrix* dres, const gs_matrix* dh, float* dweight, void* ws, size_t ws_bytes,
+                       void* stream) {
+  g_err[0] = 0;
+  int32_t st;
+  if ((st = check_matrix(dy, "dy", kF32 | kBF16)) != GS_OK) return st;
+  const int64_t rows = dy->rows, cols = dy->cols;
+  if ((st = check_shape(h, "h", kF32 | kBF16 | kMX8, rows, cols)) != GS_OK) return st;
+  if (dres && (st = check_shape(dres, "dres", kF32 | kBF16, rows, cols)) != GS_OK) return st;
+  if ((st = check_shape(dh, "dh", kF32 | kBF16, rows, cols)) != GS_OK) return st;
+  if (!weight || (rows > 0 && !rstd)) return fail(GS_ERR_INVALID_ARG, "weight or rstd is null");
+  if ((st = check_in_place(dh, dres, "dh")) != GS_OK) return st;
+  if (same_data(dh, dy) || same_data(dh, h)) return fail(GS_ERR_INVALID_ARG, "the output is one of the inputs");
+  const size_t need = gsk::rmsnorm_bwd_ws_bytes(rows, int(cols));
+  if (!ws || ws_bytes < need) return fail(GS_ERR_CAPACITY, "rmsnorm_bwd workspace needs %zu bytes", need);
+  if (rows == 0 && !dweight) return GS_OK;
+  const hipError_t e = gsk::launch_rmsnorm_bwd(gsk::mat_arg(dy), gsk::mat_arg(h), weight, rstd, gsk::mat_arg(dres),
+                                               gsk::mat_arg(dh), dweight, rows, int(cols), ws, as_stream(stream));
+  if (e != hipSuccess) return hip_fail(e, "rmsnorm_bwd");
+  return GS_OK;
+}
+
+int32_t gs_linear_fwd(const gs_matrix* x, const gs_matrix* w, const float* bias, int32_t act,
+                      const gs_matrix* residual, const gs_matrix* z, const gs_matrix* y, void* stream) {
+  g_err[0] = 0;
+  int32_t st;
+  if ((st = check_matrix(x, "x", kBF16 | kMX8)) != GS_OK) return st;
+  if ((st = check_matrix(w, "w", kBF16)) != GS_OK) return st;
+  const int64_t rows = x->rows, in = x->cols, out = w->rows;
+  if ((st = check_shape(w, "w", kBF16, out, in)) != GS_OK) return st;
+  if (!width_ok(out)) return fail(GS_ERR_INVALID_ARG, "w: rows must be 1..2^20");
+  if (act < GS_ACT_NONE || act > GS_ACT_GELU) return fail(GS_ERR_INVALID_ARG, "unknown activation");
+  if (residual && (st = check_shape(residual, "residual", kF32 | kBF16, rows, out)) != GS_OK) return st;
+  if (z && (st = check_shape(z, "z", kF32 | kBF16 | kMX8, rows, out)) != GS_OK) return st;
+  if ((st = check_shape(y, "y", kF32 | kBF16, rows, out)) != GS_OK) return st;
+  if ((st = check_in_place(y, residual, "y")) != GS_OK) return st;
+  if (same_data(y, x) || same_data(y, w) || same_data(y, z) || same_data(z, x) || same_data(z, w) ||
+      same_data(z, residual))
+    return fail(GS_ERR_INVALID_ARG, "an output is one of the inputs or another output");
+  if (rows == 0) return GS_OK;
+  const hipError_t e = gsk::launch_linear_fwd(gsk::mat_arg(x), gsk::mat_arg(w), bias, act, gsk::mat_arg(residual),
+                                              gsk::mat_arg(z), gsk::mat_arg(y), rows, int(in), int(out),
+                                              as_stream(stream));
+  if (e != hipSuccess) return hip_fail(e, "linear_fwd");
+  return GS_OK;
+}
+
+int32_t gs_linear_bwd(const gs_matrix* dy, const gs_matrix* z, int32_t act, const gs_matrix* x, const gs_matrix* w,
+                      const gs_matrix* dx, const gs_matrix* dw, float* dbias, void* ws, size_t ws_bytes,
+                      void* stream) {
+  g_err[0] = 0;
+  int32_t st;
+  if ((st = check_matrix(x, "x", kBF16 | kMX8)) != GS_OK) return st;
+  if ((st = check_matrix(w, "w", kBF16)) != GS_OK) return st;
+  const int64_t rows = x->rows, in = x->cols, out = w->rows;
+  if ((st = check_shape(w, "w", kBF16, out, in)) != GS_OK) return st;
+  if (!width_ok(out)) return fail(GS_ERR_INVALID_ARG, "w: rows must be 1..2^20");
+  if (act < GS_ACT_NONE || act > GS_ACT_GELU) return fail(GS_ERR_INVALID_ARG, "unknown activation");
+  if ((st = check_shape(dy, "dy", kF32 | kBF16, rows, out)) != GS_OK) return st;
+  if (act != GS_ACT_NONE && !z) return fail(GS_ERR_INVALID_ARG, "z is null");
+  if (z && (st = check_shape(z, "z", kF32 | kBF16 | kMX8, rows, out)) != GS_OK) return st;
+  if (dx && (st = check_shape(dx, "dx", kF32 | kBF16, rows, in)) != GS_OK) return st;
+  if (dw && (st = check_shape(dw, "dw", kF32 | kBF16, out, in)) != GS_OK) return st;
+  for (const gs_matrix* o : {dx, dw})
+    for (const gs_matrix* i : {dy, z, x, w})
+      if (same_data(o, i)) return fail(GS_ERR_INVALID_ARG, "an output is one of the inputs");
+  if (same_data(dx, dw)) return fail(GS_ERR_INVALID_ARG, "an output is another output");
+  const size_t need = gsk::linear_bwd_ws_bytes(rows, int(in), int(out));
+  if (!ws || ws_bytes < need) return fail(GS_ERR_CAPACITY, "linear_bwd workspace needs %zu bytes", need);
+  const hipError_t e = gsk::launch_linear_bwd(gsk::mat_arg(dy), gsk::mat_arg(z), act, gsk::mat_arg(x),
+                                              gsk::mat_arg(w), gsk::mat_arg(dx), gsk::mat_arg(dw), dbias, rows,
+                                              int(in), int(out), ws, as_stream(stream));
+  if (e != hipSuccess) return hip_fail(e, "linear_bwd");
   return GS_OK;
 }
 

@@ -1,0 +1,378 @@
+// gs_linear_fwd and gs_linear_bwd: y = act(x W^T + b) + r and its gradients.  With
+// z = x W^T + b and dz = dy act'(z):  dx = dz W,  dW = dz^T x,  db = sum of the rows of dz.
+//
+// Every product runs on the matrix cores (16x16x32, bfloat16 operands, float32 sums):
+// bfloat16 and MX8 operands are exact there, float32 ones (and dz) are rounded to bfloat16.
+#include "matrix.h"
+#include "profile.h"
+
+namespace gsk {
+namespace {
+
+constexpr int kThreads = 256;
+
+// ------------------------------------------------------------- epilogue of the forward
+
+struct Epilogue {
+  const float* bias;   // nullable
+  int act;
+  MatArg r, z, y;      // residual and kept pre-activation nullable
+};
+
+// 16 columns of a row to memory; for MX8 the lanes 16 apart hold the two halves of a
+// 32-column block (all lanes active).  n: columns of the 16 that exist (<= 0: none).
+__device__ inline void store16(const MatArg& m, int64_t row, int col, const float v[16], int n) {
+  if (m.type == GS_MAT_MX8) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t u = i < n ? finite_magnitude(v[i]) : 0u;
+      top = u > top ? u : top;
+    }
+    top = max_across16(top);
+    const uint32_t byte = mx8_scale_byte(top);
+    const float inv = mx8_inverse(byte);
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = mx8_encode4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], inv);
+    char* p = m.p + row * m.ld + col;
+    if (n >= 16) {
+      __builtin_memcpy(p, &w, 16);
+    } else if (n > 0) {
+      store_bytes8(p, w[0], w[1], n);
+      if (n > 8) store_bytes8(p + 8, w[2], w[3], n - 8);
+    }
+    if (n > 0 && (col & 31) == 0) m.s[row * m.lds + (col >> 5)] = uint8_t(byte);
+    return;
+  }
+  if (n > 0) store8(m, row, col, v, n);
+  if (n > 8) store8(m, row, col + 8, v + 8, n - 8);
+}
+
+// v: x W^T for 16 columns of a row.
+__device__ inline void finish16(const Epilogue& e, int64_t row, int col, float v[16], int n) {
+  if (e.bias) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] += i < n ? e.bias[col + i] : 0.0f;
+  }
+  if (e.z.p) store16(e.z, row, col, v, n);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = activate(v[i], e.act);
+  if (e.r.p) {
+    float r[16];
+    raw8_to_float(load_raw8(e.r, row, col, n), e.r.type, r);
+    raw8_to_float(load_raw8(e.r, row, col + 8, n - 8), e.r.type, r + 8);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] += r[i];
+  }
+  store16(e.y, row, col, v, n);
+}
+
+// ------------------------------------------------- tiled product, contraction contiguous
+
+// out(q, p) = sum_k Q(q, k) P(p, k) on tiles of 64 WP columns p by 16 QT WQ rows q, a wave
+// taking 64 columns by 16 QT rows.  Both operands' tiles of 64 k are staged through
+// registers (converting to bfloat16) into LDS; the 16-byte pieces of a 128-byte row are
+// permuted by the row's number so that the 16 rows a fragment read covers fall into
+// different banks.  P's rows are stored so that a lane's four result tiles are 16
+// consecutive columns of one output row: wide stores, and half an MX8 block.
+template <int WP, int WQ, int QT>
+__global__ void __launch_bounds__(WP* WQ * 64) gemm_nt_kernel(MatArg P, MatArg Q, int64_t np, int64_t nq, int nk,
+                                                               Epilogue e) {
+  constexpr int kT = WP * WQ * 64, BP = 64 * WP, BQ = 16 * QT * WQ, kLoads = (BP + BQ) * 8 / kT;
+  __shared__ __align__(16) uint8_t lds[(BP + BQ) * 128];
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, wp = wave % WP, wq = wave / WP;
+  const int64_t p0 = int64_t(blockIdx.y) * BP, q0 = int64_t(blockIdx.x) * BQ;
+  f32x4 acc[QT][4];
+#pragma unroll
+  for (int i = 0; i < QT; ++i)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
+  for (int k0 = 0; k0 < nk; k0 += 64) {
+    Raw8 raw[kLoads];
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const int i = u * kT + threadIdx.x, row = i / 8, k = k0 + i % 8 * 8;
+      if (row < BP)
+        raw[u] = load_raw8(P, p0 + row, k, p0 + row < np ? nk - k : 0);
+      else
+        raw[u] = load_raw8(Q, q0 + row - BP, k, q0 + row - BP < nq ? nk - k : 0);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const int i = u * kT + threadIdx.x;
+      int row = i / 8;
+      const int type = row < BP ? P.type : Q.type;
+      if (row < BP) row = (row & ~63) | ((row & 12) << 2) | ((row & 48) >> 2) | (row & 3);
+      *reinterpret_cast<u32x4*>(lds + row * 128 + ((i % 8) ^ ((row >> 1) & 7)) * 16) = raw8_to_bf16(raw[u], type);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      const int piece = kk * 4 + lane / 16;
+      bf16x8 pf[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int row = wp * 64 + t * 16 + lane % 16;
+        pf[t] = *reinterpret_cast<const bf16x8*>(lds + row * 128 + (piece ^ ((row >> 1) & 7)) * 16);
+      }
+#pragma unroll
+      for (int i = 0; i < QT; ++i) {
+        const int row = BP + (wq * QT + i) * 16 + lane % 16;
+        const bf16x8 qf = *reinterpret_cast<const bf16x8*>(lds + row * 128 + (piece ^ ((row >> 1) & 7)) * 16);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[t], qf, acc[i][t], 0, 0, 0);
+      }
+    }
+  }
+  const int64_t col = p0 + wp * 64 + lane / 16 * 16;
+#pragma unroll
+  for (int i = 0; i < QT; ++i) {
+    const int64_t row = q0 + (wq * QT + i) * 16 + lane % 16;
+    float v[16];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[4 * t + j] = acc[i][t][j];
+    finish16(e, row, int(col), v, row < nq ? int(np - col < 16 ? np - col : 16) : 0);
+  }
+}
+
+// ------------------------------------------------- tiled product, contraction over rows
+
+// out(q, p) = sum_m Q(m, q) P(m, p) for m in the block's slice of the rows: the weight's
+// gradient (Q = dz, P = x).  Tiles of 64 rows are kept in LDS as they are in memory (plus
+// 32 bytes a row, so that eight rows fall into different banks) and read transposed
+// (ds_read_b64_tr_b16: four rows of 16 columns, a column's four values to a lane).
+template <int WP, int WQ, int QT>
+__global__ void __launch_bounds__(WP* WQ * 64) gemm_tn_kernel(MatArg P, MatArg Q, int np, int nq, int64_t rows,
+                                                               int64_t per_slice, float* part, MatArg out) {
+  constexpr int kT = WP * WQ * 64, BP = 64 * WP, BQ = 16 * QT * WQ, BM = 64;
+  constexpr int kPitchP = BP * 2 + 32, kPitchQ = BQ * 2 + 32, kLoads = BM * (BP + BQ) / 8 / kT;
+  __shared__ __align__(16) uint8_t lds[BM * (kPitchP + kPitchQ)];
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, wp = wave % WP, wq = wave / WP;
+  const int p0 = blockIdx.x * BP, q0 = blockIdx.y * BQ;
+  const int64_t first = int64_t(blockIdx.z) * per_slice;
+  const int64_t last = first + per_slice < rows ? first + per_slice : rows;
+  f32x4 acc[QT][4];
+#pragma unroll
+  for (int i = 0; i < QT; ++i)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
+  for (int64_t m0 = first; m0 < last; m0 += BM) {
+    Raw8 raw[kLoads];
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const int i = u * kT + threadIdx.x, m = i / ((BP + BQ) / 8), c = i % ((BP + BQ) / 8) * 8;
+      const bool in = m0 + m < last;
+      if (c < BP)
+        raw[u] = load_raw8(P, m0 + m, p0 + c, in ? np - p0 - c : 0);
+      else
+        raw[u] = load_raw8(Q, m0 + m, q0 + c - BP, in ? nq - q0 - (c - BP) : 0);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const int i = u * kT + threadIdx.x, m = i / ((BP + BQ) / 8), c = i % ((BP + BQ) / 8) * 8;
+      if (c < BP)
+        *reinterpret_cast<u32x4*>(lds + m * kPitchP + c * 2) = raw8_to_bf16(raw[u], P.type);
+      else
+        *reinterpret_cast<u32x4*>(lds + BM * kPitchP + m * kPitchQ + (c - BP) * 2) = raw8_to_bf16(raw[u], Q.type);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int kk = 0; kk < BM / 32; ++kk) {
+      const int m = kk * 32 + lane / 16 * 8 + lane % 16 / 4, c = lane % 4 * 4;
+      bf16x8 pf[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        pf[t] = read_transposed(lds + m * kPitchP + (wp * 64 + t * 16 + c) * 2, kPitchP);
+#pragma unroll
+      for (int i = 0; i < QT; ++i) {
+        const bf16x8 qf =
+            read_transposed(lds + BM * kPitchP + m * kPitchQ + ((wq * QT + i) * 16 + c) * 2, kPitchQ);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[t], qf, acc[i][t], 0, 0, 0);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < QT; ++i) {
+    const int q = q0 + (wq * QT + i) * 16 + lane % 16;
+    if (q >= nq) continue;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int p = p0 + wp * 64 + t * 16 + lane / 16 * 4;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (p + j >= np) continue;
+        if (part) {
+          part[(int64_t(blockIdx.z) * nq + q) * np + p + j] = acc[i][t][j];
+        } else if (out.type == GS_MAT_F32) {
+          reinterpret_cast<float*>(out.p)[int64_t(q) * out.ld + p + j] = acc[i][t][j];
+        } else {
+          reinterpret_cast<uint16_t*>(out.p)[int64_t(q) * out.ld + p + j] = uint16_t(pack_bf16(acc[i][t][j], 0.0f));
+        }
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------- dz, db and W^T
+
+// dz = dy act'(z) to bfloat16 (unless dz is absent) and part[slice] = the column sums of dz
+// before its rounding.  lanes (a power of two in [4, 64]) take 8 columns each of a row.
+__global__ void __launch_bounds__(kThreads) dz_kernel(MatArg dy, MatArg z, int act, MatArg dz, float* part,
+                                                       int64_t rows, int cols, int64_t per_slice, int lanes) {
+  const int lane = threadIdx.x & (lanes - 1), slot = threadIdx.x / lanes, per = kThreads / lanes;
+  const int col = int(blockIdx.y) * lanes * 8 + lane * 8, n = cols - col;
+  const int64_t first = int64_t(blockIdx.x) * per_slice;
+  const int64_t last = first + per_slice < rows ? first + per_slice : rows;
+  float acc[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+  for (int64_t row = first + slot; row < last; row += per) {
+    float v[8];
+    const Raw8 a = load_raw8(dy, row, col, n);
+    if (act != GS_ACT_NONE) {
+      const Raw8 b = load_raw8(z, row, col, n);
+      float t[8];
+      raw8_to_float(a, dy.type, v);
+      raw8_to_float(b, z.type, t);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= act_slope(t[i], act);
+    } else {
+      raw8_to_float(a, dy.type, v);
+    }
+    if (dz.p && n > 0) store_bf16x8(dz.p + (row * dz.ld + col) * 2, v, n);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] += v[i];
+  }
+  if (!part) return;
+  __shared__ float sums[kThreads * 8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sums[threadIdx.x * 8 + i] = acc[i];
+  __syncthreads();
+  for (int j = threadIdx.x; j < lanes * 8; j += kThreads) {
+    float t = 0.0f;
+    for (int k = 0; k < per; ++k) t += sums[k * lanes * 8 + j];
+    const int c = int(blockIdx.y) * lanes * 8 + j;
+    if (c < cols) part[int64_t(blockIdx.x) * cols + c] = t;
+  }
+}
+
+// wt[k][n] = w[n][k], tiles of 64 x 64.
+__global__ void __launch_bounds__(kThreads) transpose_kernel(MatArg w, MatArg wt, int n, int k) {
+  __shared__ uint16_t tile[64][66];
+  const int k0 = blockIdx.x * 64, n0 = blockIdx.y * 64;
+  for (int i = threadIdx.x; i < 4096; i += kThreads) {
+    const int r = i / 64, c = i % 64;
+    if (n0 + r < n && k0 + c < k)
+      tile[r][c] = reinterpret_cast<const uint16_t*>(w.p)[int64_t(n0 + r) * w.ld + k0 + c];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 4096; i += kThreads) {
+    const int r = i / 64, c = i % 64;
+    if (k0 + r < k && n0 + c < n)
+      reinterpret_cast<uint16_t*>(wt.p)[int64_t(k0 + r) * wt.ld + n0 + c] = tile[c][r];
+  }
+}
+
+inline size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
+inline int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
+
+// How the backward's row loops are split: slices of the rows whose partial sums are joined
+// in order.
+int dz_slices(int64_t rows) { return int(min64(rows < 64 ? 1 : rows / 64, 1024)); }
+
+int dw_slices(int64_t rows, int k, int n) {
+  const int64_t tiles = int64_t(div_up(k, 64)) * div_up(n, 64);
+  const int64_t want = tiles >= 512 ? 1 : 512 / tiles;
+  return int(min64(want, rows < 256 ? 1 : rows / 256));
+}
+
+struct BwdWs {
+  char *dz, *wt;
+  float *db, *dw;
+  int64_t dz_ld, wt_ld;
+  size_t bytes;
+};
+
+BwdWs carve_bwd(void* ws, int64_t rows, int k, int n) {
+  BwdWs w;
+  char* p = static_cast<char*>(ws);
+  size_t at = 0;
+  w.dz_ld = w.wt_ld = (n + 7) & ~7;
+  w.dz = p + at;
+  at += align256(size_t(rows) * w.dz_ld * 2);
+  w.wt = p + at;
+  at += align256(size_t(k) * w.wt_ld * 2);
+  w.db = reinterpret_cast<float*>(p + at);
+  at += align256(size_t(dz_slices(rows)) * n * 4);
+  w.dw = reinterpret_cast<float*>(p + at);
+  at += align256(size_t(dw_slices(rows, k, n)) * n * k * 4);
+  w.bytes = at;
+  return w;
+}
+
+}  // namespace
+
+hipError_t launch_linear_fwd(const MatArg& x, const MatArg& w, const float* bias, int act, const MatArg& r,
+                             const MatArg& z, const MatArg& y, int64_t rows, int k, int n, hipStream_t s) {
+  const Epilogue e{bias, act, r, z, y};
+  GSK_PROF("linear_fwd", s);
+  gemm_nt_kernel<1, 4, 1><<<dim3(div_up(rows, 64), div_up(n, 64)), kThreads, 0, s>>>(w, x, n, rows, k, e);
+  return hipGetLastError();
+}
+
+size_t linear_bwd_ws_bytes(int64_t rows, int k, int n) { return carve_bwd(nullptr, rows, k, n).bytes; }
+
+hipError_t launch_linear_bwd(const MatArg& dy, const MatArg& z, int act, const MatArg& x, const MatArg& w,
+                             const MatArg& dx, const MatArg& dw, float* dbias, int64_t rows, int k, int n, void* ws,
+                             hipStream_t s) {
+  const BwdWs b = carve_bwd(ws, rows, k, n);
+  const bool own_dz = act != GS_ACT_NONE && (dx.p || dw.p);
+  const MatArg dz = own_dz ? MatArg{b.dz, nullptr, b.dz_ld, 0, GS_MAT_BF16} : dy;
+  const MatArg none{nullptr, nullptr, 0, 0, GS_MAT_F32};
+  hipError_t e;
+  if (own_dz || dbias) {
+    int lanes = 4;
+    while (lanes < 64 && lanes * 8 < n) lanes *= 2;
+    const int slices = dz_slices(rows);
+    const int64_t per = (rows + slices - 1) / slices;
+    {
+      GSK_PROF("linear_dz", s);
+      dz_kernel<<<dim3(slices, div_up(n, lanes * 8)), kThreads, 0, s>>>(dy, z, act, own_dz ? dz : none,
+                                                                        dbias ? b.db : nullptr, rows, n, per, lanes);
+    }
+    if (dbias) {
+      const MatArg out{reinterpret_cast<char*>(dbias), nullptr, n, 0, GS_MAT_F32};
+      if ((e = launch_sum_parts(b.db, slices, n, n, out, s)) != hipSuccess) return e;
+    }
+  }
+  if (dx.p && rows > 0) {
+    const MatArg wt{b.wt, nullptr, b.wt_ld, 0, GS_MAT_BF16};
+    {
+      GSK_PROF("linear_wt", s);
+      transpose_kernel<<<dim3(div_up(k, 64), div_up(n, 64)), kThreads, 0, s>>>(w, wt, n, k);
+    }
+    const Epilogue out{nullptr, GS_ACT_NONE, none, none, dx};
+    GSK_PROF("linear_dx", s);
+    gemm_nt_kernel<1, 4, 1><<<dim3(div_up(rows, 64), div_up(k, 64)), kThreads, 0, s>>>(wt, dz, k, rows, n, out);
+  }
+  if (dw.p) {
+    const int slices = dw_slices(rows, k, n);
+    const int64_t per = ((rows + slices - 1) / slices + 63) / 64 * 64;
+    float* part = slices > 1 ? b.dw : nullptr;
+    {
+      GSK_PROF("linear_dw", s);
+      gemm_tn_kernel<1, 4, 1><<<dim3(div_up(k, 64), div_up(n, 64), slices), kThreads, 0, s>>>(x, dz, k, n, rows, per,
+                                                                                              part, dw);
+    }
+    if (part && (e = launch_sum_parts(part, slices, int64_t(n) * k, k, dw, s)) != hipSuccess) return e;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace gsk

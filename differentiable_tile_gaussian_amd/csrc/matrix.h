@@ -1,0 +1,322 @@
+// Row-major matrices of the network operators on the device: 8-column chunks loaded from
+// float32, bfloat16 or MX8 storage, and the MX8 encoding.
+//
+// MX8 (the microscaling format with e4m3 elements): the 32-column block b of a row holds
+// v = q 2^(scale byte - 127), with the smallest scale exponent >= -126 for which the
+// block's largest finite magnitude is at most 448 2^e (448 is e4m3's largest value).  A
+// power-of-two scale makes the decoded value exact in bfloat16 (4 significant bits), so
+// the matrix products read the decoded values without another rounding.
+#pragma once
+
+#include "gs_internal.h"
+
+namespace gsk {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// A matrix argument of a kernel (gs_matrix without its sizes).  p == nullptr: absent.
+struct MatArg {
+  char* p;
+  uint8_t* s;
+  int64_t ld, lds;
+  int32_t type;
+};
+
+inline MatArg mat_arg(const gs_matrix* m) {
+  if (!m) return MatArg{nullptr, nullptr, 0, 0, GS_MAT_F32};
+  return MatArg{static_cast<char*>(m->data), m->scales, m->ld, m->scales_ld, m->type};
+}
+
+// 8 columns as loaded: float32 uses both halves, bfloat16 lo, MX8 the first two words of lo
+// and the scale byte.
+struct Raw8 {
+  u32x4 lo, hi;
+  uint32_t scale;
+};
+
+// Columns col .. col + 7 of a row, of which the first n exist (n >= 8: all; the others
+// read as zero).  col is a multiple of 8.  The addresses need only the element's own
+// alignment: the copies compile to wide loads in the unaligned access mode, which is the
+// amdhsa default.
+__device__ inline Raw8 load_raw8(const MatArg& m, int64_t row, int col, int n) {
+  Raw8 r;
+  r.lo = u32x4{0, 0, 0, 0};
+  r.hi = u32x4{0, 0, 0, 0};
+  r.scale = 0;
+  if (m.type == GS_MAT_BF16) {
+    const char* p = m.p + (row * m.ld + col) * 2;
+    if (n >= 8) {
+      __builtin_memcpy(&r.lo, __builtin_assume_aligned(p, 2), 16);
+    } else {
+      const uint16_t* e = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) r.lo[i / 2] |= uint32_t(e[i]) << (16 * (i & 1));
+    }
+  } else if (m.type == GS_MAT_F32) {
+    const char* p = m.p + (row * m.ld + col) * 4;
+    if (n >= 8) {
+      __builtin_memcpy(&r.lo, __builtin_assume_aligned(p, 4), 16);
+      __builtin_memcpy(&r.hi, __builtin_assume_aligned(p + 16, 4), 16);
+    } else {
+      const uint32_t* e = reinterpret_cast<const uint32_t*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i < n) r.lo[i] = e[i];
+        if (i + 4 < n) r.hi[i] = e[i + 4];
+      }
+    }
+  } else {
+    const char* p = m.p + row * m.ld + col;
+    if (n > 0) r.scale = m.s[row * m.lds + (col >> 5)];
+    if (n >= 8) {
+      u32x2 v;
+      __builtin_memcpy(&v, p, 8);
+      r.lo[0] = v[0];
+      r.lo[1] = v[1];
+    } else {
+      const uint8_t* e = reinterpret_cast<const uint8_t*>(p);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) r.lo[i / 4] |= uint32_t(e[i]) << (8 * (i & 3));
+    }
+  }
+  return r;
+}
+
+__device__ inline float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ inline float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// A scale byte as the float whose exponent the scaled conversions read (2^-127 for byte
+// 0, NaN for byte 255).
+__device__ inline float mx8_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+__device__ inline void raw8_to_float(const Raw8& r, int type, float v[8]) {
+  if (type == GS_MAT_BF16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf16_lo(r.lo[i]);
+      v[2 * i + 1] = bf16_hi(r.lo[i]);
+    }
+  } else if (type == GS_MAT_F32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = __uint_as_float(r.lo[i]);
+      v[4 + i] = __uint_as_float(r.hi[i]);
+    }
+  } else {
+    const float s = mx8_scale(r.scale);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(r.lo[i], s, false);
+      const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(r.lo[i], s, true);
+      v[4 * i] = a[0];
+      v[4 * i + 1] = a[1];
+      v[4 * i + 2] = b[0];
+      v[4 * i + 3] = b[1];
+    }
+  }
+}
+
+// Four e4m3 values as bfloat16, exactly.
+__device__ inline u32x2 mx8_to_bf16x4(uint32_t w, float scale) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, true);
+  return u32x2{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b)};
+}
+
+// Two floats rounded to bfloat16 (nearest even).
+__device__ inline uint32_t pack_bf16(float a, float b) {
+  const bf16x2 v{(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+// The chunk as bfloat16 operands of a matrix product: float32 rounds, the others are exact.
+__device__ inline u32x4 raw8_to_bf16(const Raw8& r, int type) {
+  if (type == GS_MAT_BF16) return r.lo;
+  if (type == GS_MAT_F32) {
+    u32x4 o;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      o[i] = pack_bf16(__uint_as_float(r.lo[2 * i]), __uint_as_float(r.lo[2 * i + 1]));
+      o[2 + i] = pack_bf16(__uint_as_float(r.hi[2 * i]), __uint_as_float(r.hi[2 * i + 1]));
+    }
+    return o;
+  }
+  const float s = mx8_scale(r.scale);
+  const u32x2 a = mx8_to_bf16x4(r.lo[0], s), b = mx8_to_bf16x4(r.lo[1], s);
+  return u32x4{a[0], a[1], b[0], b[1]};
+}
+
+// ---- encoding
+
+// Bits of |v|, zero for infinities and NaN: a block's scale goes by its finite values.
+__device__ inline uint32_t finite_magnitude(float v) {
+  const uint32_t u = __float_as_uint(v) & 0x7fffffffu;
+  return u < 0x7f800000u ? u : 0u;
+}
+
+// The scale byte for a block whose largest finite magnitude has these bits: the exponent
+// field of the smallest 2^e with magnitude <= 1.75 2^(e + 8) (the addition carries into
+// the exponent exactly when the mantissa is above 1.75's).
+__device__ inline uint32_t mx8_scale_byte(uint32_t top) {
+  const int e = int((top + 0x1fffffu) >> 23) - 8;
+  return uint32_t(e < 1 ? 1 : e);
+}
+
+// 1 / scale, exactly (scale bytes from mx8_scale_byte are at most 247).
+__device__ inline float mx8_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+
+// Four values of a block to e4m3 (nearest even; infinities and NaN become NaN).
+__device__ inline uint32_t mx8_encode4(float a, float b, float c, float d, float inv) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, 0, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(c * inv, d * inv, w, true);
+  return uint32_t(w);
+}
+
+// The larger of x and the same value of the lane 16 or 32 away.
+__device__ inline uint32_t max_across16(uint32_t x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  return r[0] > r[1] ? r[0] : r[1];
+}
+
+// ---- stores of 8 (or the first n) columns
+
+__device__ inline void store_f32x8(float* p, const float v[8], int n) {
+  if (n >= 8) {
+    const f32x4 a{v[0], v[1], v[2], v[3]}, b{v[4], v[5], v[6], v[7]};
+    __builtin_memcpy(__builtin_assume_aligned(p, 4), &a, 16);
+    __builtin_memcpy(__builtin_assume_aligned(p + 4, 4), &b, 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = v[i];
+  }
+}
+
+__device__ inline void store_bf16x8(char* p, const float v[8], int n) {
+  const u32x4 w{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+  if (n >= 8) {
+    __builtin_memcpy(__builtin_assume_aligned(p, 2), &w, 16);
+  } else {
+    uint16_t* e = reinterpret_cast<uint16_t*>(p);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) e[i] = uint16_t(w[i / 2] >> (16 * (i & 1)));
+  }
+}
+
+__device__ inline void store_bytes8(char* p, uint32_t a, uint32_t b, int n) {
+  if (n >= 8) {
+    const u32x2 w{a, b};
+    __builtin_memcpy(p, &w, 8);
+  } else {
+    uint8_t* e = reinterpret_cast<uint8_t*>(p);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) e[i] = uint8_t((i < 4 ? a : b) >> (8 * (i & 3)));
+  }
+}
+
+// float32 or bfloat16 (the other types are the callers').
+__device__ inline void store8(const MatArg& m, int64_t row, int col, const float v[8], int n) {
+  if (m.type == GS_MAT_F32)
+    store_f32x8(reinterpret_cast<float*>(m.p) + row * m.ld + col, v, n);
+  else
+    store_bf16x8(m.p + (row * m.ld + col) * 2, v, n);
+}
+
+// The largest magnitude over the four neighbouring lanes that hold a 32-column block.
+__device__ inline uint32_t max_over_quad(uint32_t x) {
+  uint32_t y = uint32_t(__builtin_amdgcn_mov_dpp(int(x), 0xb1, 0xf, 0xf, true));  // lanes 1 0 3 2
+  x = x > y ? x : y;
+  y = uint32_t(__builtin_amdgcn_mov_dpp(int(x), 0x4e, 0xf, 0xf, true));           // lanes 2 3 0 1
+  return x > y ? x : y;
+}
+
+// A chunk of 8 columns to MX8, where four neighbouring lanes (all active) hold the four
+// chunks of one block; values of absent columns are zero.
+__device__ inline void store_mx8_quad(const MatArg& m, int64_t row, int col, const float v[8], int n) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t u = finite_magnitude(v[i]);
+    top = u > top ? u : top;
+  }
+  top = max_over_quad(top);
+  const uint32_t byte = mx8_scale_byte(top);
+  const float inv = mx8_inverse(byte);
+  const uint32_t a = mx8_encode4(v[0], v[1], v[2], v[3], inv), b = mx8_encode4(v[4], v[5], v[6], v[7], inv);
+  if (n > 0) {
+    store_bytes8(m.p + row * m.ld + col, a, b, n);
+    if ((col & 31) == 0) m.s[row * m.lds + (col >> 5)] = uint8_t(byte);
+  }
+}
+
+// ---- activations (GS_ACT_*)
+
+__device__ inline float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
+
+constexpr float kGelu = 1.5957691216057308f;   // 2 sqrt(2 / pi)
+
+__device__ inline float activate(float z, int act) {
+  if (act == GS_ACT_RELU) return z < 0.0f ? 0.0f : z;   // NaN passes
+  if (act == GS_ACT_SILU) return z * sigmoid(z);
+  if (act == GS_ACT_GELU) return z * sigmoid(kGelu * z * (1.0f + 0.044715f * z * z));
+  return z;
+}
+
+// act'(z).  With g the sigmoid of u, the slope is g + z u' g (1 - g); where g (1 - g)
+// underflows the second term's limit is zero, whatever z is.
+__device__ inline float act_slope(float z, int act) {
+  if (act == GS_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+  if (act == GS_ACT_SILU) {
+    const float g = sigmoid(z), t = g * (1.0f - g);
+    return t == 0.0f ? g : g + z * t;
+  }
+  if (act == GS_ACT_GELU) {
+    const float g = sigmoid(kGelu * z * (1.0f + 0.044715f * z * z)), t = g * (1.0f - g);
+    return t == 0.0f ? g : g + z * t * kGelu * (1.0f + 0.134145f * z * z);
+  }
+  return 1.0f;
+}
+
+// An operand of a 16x16x32 product whose contraction runs down the rows of an LDS tile: lane
+// l names the row l % 16 / 4 and the four columns (l % 4) * 4 of its eight rows (8 (l / 16)
+// on), and receives column l % 16 of those eight rows.
+__device__ inline bf16x8 read_transposed(const uint8_t* p, int pitch) {
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) s16x4* Lds;
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p));
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p + 4 * pitch));
+  const short __attribute__((ext_vector_type(8))) v{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  return __builtin_bit_cast(bf16x8, v);
+}
+
+// ---- partial sums: out[c] = sum over parts of part[p * count + c], in the order of the
+// parts' index groups (a fixed order); out float32 or bfloat16.
+hipError_t launch_sum_parts(const float* part, int parts, int64_t count, int cols, const MatArg& out, hipStream_t s);
+
+// ---- mx8.hip, rmsnorm.hip, linear.hip: the calls' launches (arguments checked by the caller)
+hipError_t launch_mx8_pack(const MatArg& x, const MatArg& q, int64_t rows, int cols, hipStream_t s);
+hipError_t launch_mx8_unpack(const MatArg& q, const MatArg& x, int64_t rows, int cols, hipStream_t s);
+hipError_t launch_rmsnorm_fwd(const MatArg& x, const MatArg& r, const float* w, float eps, const MatArg& h,
+                              const MatArg& ckpt, const MatArg& y, float* rstd, int64_t rows, int cols,
+                              hipStream_t s);
+size_t rmsnorm_bwd_ws_bytes(int64_t rows, int cols);
+hipError_t launch_rmsnorm_bwd(const MatArg& dy, const MatArg& h, const float* w, const float* rstd,
+                              const MatArg& dres, const MatArg& dh, float* dweight, int64_t rows, int cols, void* ws,
+                              hipStream_t s);
+hipError_t launch_linear_fwd(const MatArg& x, const MatArg& w, const float* bias, int act, const MatArg& r,
+                             const MatArg& z, const MatArg& y, int64_t rows, int k, int n, hipStream_t s);
+size_t linear_bwd_ws_bytes(int64_t rows, int k, int n);
+hipError_t launch_linear_bwd(const MatArg& dy, const MatArg& z, int act, const MatArg& x, const MatArg& w,
+                             const MatArg& dx, const MatArg& dw, float* dbias, int64_t rows, int k, int n, void* ws,
+                             hipStream_t s);
+
+}  // namespace gsk

@@ -1,0 +1,86 @@
+// gs_mx8_pack and gs_mx8_unpack: a matrix to and from MX8 (matrix.h has the format).
+//
+// Both are streams bounded by HBM: pack reads 2 or 4 bytes an element and writes 1 + 1/32,
+// unpack the reverse.  A thread takes 8 columns (one 16-byte load of bfloat16, two of
+// float32), so a block of 32 columns is four neighbouring lanes and its largest magnitude
+// two lane exchanges; 4 to 64 lanes take a row (the smallest power of two that covers it,
+// so narrow rows leave few lanes idle), and each keeps kRows rows in flight.
+#include "matrix.h"
+#include "profile.h"
+
+namespace gsk {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRows = 4;
+
+// lanes: lanes per row, a power of two in [4, 64].
+__global__ void __launch_bounds__(kThreads) mx8_pack_kernel(MatArg x, MatArg q, int64_t rows, int cols, int lanes) {
+  const int lane = threadIdx.x & (lanes - 1);
+  const int per = kThreads / lanes;   // rows a block takes at a time
+  const int64_t row0 = int64_t(blockIdx.x) * (per * kRows) + threadIdx.x / lanes;
+  for (int c0 = 0; c0 < cols; c0 += lanes * 8) {
+    const int col = c0 + lane * 8;
+    Raw8 raw[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int64_t row = row0 + int64_t(u) * per;
+      raw[u] = load_raw8(x, row, col, row < rows ? cols - col : 0);
+    }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int64_t row = row0 + int64_t(u) * per;
+      float v[8];
+      raw8_to_float(raw[u], x.type, v);
+      store_mx8_quad(q, row, col, v, row < rows ? cols - col : 0);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) mx8_unpack_kernel(MatArg q, MatArg x, int64_t rows, int cols, int lanes) {
+  const int lane = threadIdx.x & (lanes - 1);
+  const int per = kThreads / lanes;
+  const int64_t row0 = int64_t(blockIdx.x) * (per * kRows) + threadIdx.x / lanes;
+  for (int c0 = 0; c0 < cols; c0 += lanes * 8) {
+    const int col = c0 + lane * 8;
+    Raw8 raw[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int64_t row = row0 + int64_t(u) * per;
+      raw[u] = load_raw8(q, row, col, row < rows ? cols - col : 0);
+    }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int64_t row = row0 + int64_t(u) * per;
+      float v[8];
+      raw8_to_float(raw[u], GS_MAT_MX8, v);
+      if (row < rows && col < cols) store8(x, row, col, v, cols - col);
+    }
+  }
+}
+
+int lanes_for(int cols) {
+  int lanes = 4;
+  while (lanes < 64 && lanes * 8 < cols) lanes *= 2;
+  return lanes;
+}
+
+unsigned blocks_for(int64_t rows, int lanes) { return div_up(rows, int64_t(kThreads / lanes) * kRows); }
+
+}  // namespace
+
+hipError_t launch_mx8_pack(const MatArg& x, const MatArg& q, int64_t rows, int cols, hipStream_t s) {
+  const int lanes = lanes_for(cols);
+  GSK_PROF("mx8_pack", s);
+  mx8_pack_kernel<<<blocks_for(rows, lanes), kThreads, 0, s>>>(x, q, rows, cols, lanes);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx8_unpack(const MatArg& q, const MatArg& x, int64_t rows, int cols, hipStream_t s) {
+  const int lanes = lanes_for(cols);
+  GSK_PROF("mx8_unpack", s);
+  mx8_unpack_kernel<<<blocks_for(rows, lanes), kThreads, 0, s>>>(q, x, rows, cols, lanes);
+  return hipGetLastError();
+}
+
+}  // namespace gsk

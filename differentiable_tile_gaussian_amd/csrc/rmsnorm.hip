@@ -1,0 +1,403 @@
+// gs_rmsnorm_fwd and gs_rmsnorm_bwd: h = x + r, y = h rstd w with rstd = (mean h^2 + eps)^-1/2,
+// and its gradients dh = rstd (u - xhat mean(u xhat)) + dres, dw = sum_rows dy xhat, where
+// u = dy w and xhat = h rstd.
+//
+// Streams bounded by HBM.  A row is held by 4 to 64 lanes, 8 columns a lane at a time (so an
+// MX8 block is four neighbouring lanes), in registers from its load to its store: each input
+// is read once and each output written once, up to kMaxHeld columns.  Wider rows are walked
+// twice by one wave, the second time from the caches.
+#include "matrix.h"
+#include "profile.h"
+
+namespace gsk {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxHeld = 4096;   // 64 lanes x 8 chunks x 8 columns
+
+template <int LANES>
+__device__ inline float row_sum(float v) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o /= 2) v += __shfl_xor(v, o);
+  return v;
+}
+
+struct NormFwdArgs {
+  MatArg x, r, h, ckpt, y;
+  const float* w;
+  float* rstd;
+  float eps, inv_cols;
+  int64_t rows;
+  int cols;
+};
+
+__device__ inline void load_weight(const float* w, int col, int n, float v[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = i < n ? w[col + i] : 0.0f;
+}
+
+__device__ inline void store_chunk(const MatArg& m, int64_t row, int col, const float v[8], int n) {
+  if (m.type == GS_MAT_MX8)
+    store_mx8_quad(m, row, col, v, n);
+  else if (n > 0)
+    store8(m, row, col, v, n);
+}
+
+// LANES lanes hold a row, CHUNKS chunks each.
+template <int LANES, int CHUNKS>
+__global__ void __launch_bounds__(kThreads) rmsnorm_fwd_kernel(NormFwdArgs a) {
+  constexpr int kPer = kThreads / LANES;
+  const int lane = threadIdx.x % LANES;
+  float w[CHUNKS][8];
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c) load_weight(a.w, (c * LANES + lane) * 8, a.cols - (c * LANES + lane) * 8, w[c]);
+  for (int64_t row0 = int64_t(blockIdx.x) * kPer; row0 < a.rows; row0 += int64_t(gridDim.x) * kPer) {
+    const int64_t row = row0 + threadIdx.x / LANES;
+    const bool in = row < a.rows;
+    Raw8 xr[CHUNKS], rr[CHUNKS];
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+      const int col = (c * LANES + lane) * 8;
+      xr[c] = load_raw8(a.x, row, col, in ? a.cols - col : 0);
+    }
+    if (a.r.p) {
+#pragma unroll
+      for (int c = 0; c < CHUNKS; ++c) {
+        const int col = (c * LANES + lane) * 8;
+        rr[c] = load_raw8(a.r, row, col, in ? a.cols - col : 0);
+      }
+    }
+    float h[CHUNKS][8], sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+      raw8_to_float(xr[c], a.x.type, h[c]);
+      if (a.r.p) {
+        float t[8];
+        raw8_to_float(rr[c], a.r.type, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[c][i] += t[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += h[c][i] * h[c][i];
+    }
+    sum = row_sum<LANES>(sum);
+    const float rstd = 1.0f / sqrtf(sum * a.inv_cols + a.eps);
+    if (in && lane == 0 && a.rstd) a.rstd[row] = rstd;
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+      const int col = (c * LANES + lane) * 8, n = in ? a.cols - col : 0;
+      if (a.h.p) store_chunk(a.h, row, col, h[c], n);
+      if (a.ckpt.p) store_mx8_quad(a.ckpt, row, col, h[c], n);
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = h[c][i] * rstd * w[c][i];
+      store_chunk(a.y, row, col, y, n);
+    }
+  }
+}
+
+// Rows of more than kMaxHeld columns: a wave a row, walked twice.
+__global__ void __launch_bounds__(kThreads) rmsnorm_fwd_wide_kernel(NormFwdArgs a) {
+  const int lane = threadIdx.x % 64;
+  const int64_t row = int64_t(blockIdx.x) * (kThreads / 64) + threadIdx.x / 64;
+  if (row >= a.rows) return;
+  float sum = 0.0f;
+  for (int pass = 0; pass < 2; ++pass) {
+    const float rstd = 1.0f / sqrtf(sum * a.inv_cols + a.eps);
+    for (int c0 = 0; c0 < a.cols; c0 += 512) {
+      const int col = c0 + lane * 8, n = a.cols - col;
+      float h[8];
+      raw8_to_float(load_raw8(a.x, row, col, n), a.x.type, h);
+      if (a.r.p) {
+        float t[8];
+        raw8_to_float(load_raw8(a.r, row, col, n), a.r.type, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] += t[i];
+      }
+      if (pass == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += h[i] * h[i];
+      } else {
+        if (a.h.p) store_chunk(a.h, row, col, h, n);
+        if (a.ckpt.p) store_mx8_quad(a.ckpt, row, col, h, n);
+        float w[8], y[8];
+        load_weight(a.w, col, n, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = h[i] * rstd * w[i];
+        store_chunk(a.y, row, col, y, n);
+      }
+    }
+    if (pass == 0) {
+      sum = row_sum<64>(sum);
+    } else if (lane == 0 && a.rstd) {
+      a.rstd[row] = rstd;
+    }
+  }
+}
+
+struct NormBwdArgs {
+  MatArg dy, h, dres, dh;
+  const float *w, *rstd;
+  float* part;   // [gridDim.x][cols] sums of dy xhat, nullptr: not wanted
+  float inv_cols;
+  int64_t rows;
+  int cols;
+};
+
+template <int LANES, int CHUNKS>
+__global__ void __launch_bounds__(kThreads) rmsnorm_bwd_kernel(NormBwdArgs a) {
+  constexpr int kPer = kThreads / LANES;
+  const int lane = threadIdx.x % LANES;
+  float w[CHUNKS][8], acc[CHUNKS][8];
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c) {
+    load_weight(a.w, (c * LANES + lane) * 8, a.cols - (c * LANES + lane) * 8, w[c]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[c][i] = 0.0f;
+  }
+  for (int64_t row0 = int64_t(blockIdx.x) * kPer; row0 < a.rows; row0 += int64_t(gridDim.x) * kPer) {
+    const int64_t row = row0 + threadIdx.x / LANES;
+    const bool in = row < a.rows;
+    Raw8 dr[CHUNKS], hr[CHUNKS], rr[CHUNKS];
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+      const int col = (c * LANES + lane) * 8, n = in ? a.cols - col : 0;
+      dr[c] = load_raw8(a.dy, row, col, n);
+      hr[c] = load_raw8(a.h, row, col, n);
+    }
+    if (a.dres.p) {
+#pragma unroll
+      for (int c = 0; c < CHUNKS; ++c) {
+        const int col = (c * LANES + lane) * 8;
+        rr[c] = load_raw8(a.dres, row, col, in ? a.cols - col : 0);
+      }
+    }
+    const float rstd = in ? a.rstd[row] : 0.0f;
+    float dy[CHUNKS][8], xh[CHUNKS][8], dot = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+      raw8_to_float(dr[c], a.dy.type, dy[c]);
+      raw8_to_float(hr[c], a.h.type, xh[c]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        xh[c][i] *= rstd;
+        const float p = dy[c][i] * xh[c][i];
+        acc[c][i] += p;
+        dot += p * w[c][i];
+      }
+    }
+    const float mean = row_sum<LANES>(dot) * a.inv_cols;
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+      const int col = (c * LANES + lane) * 8, n = in ? a.cols - col : 0;
+      float o[8];
+      if (a.dres.p) {
+        raw8_to_float(rr[c], a.dres.type, o);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] += rstd * (dy[c][i] * w[c][i] - xh[c][i] * mean);
+      if (n > 0) store8(a.dh, row, col, o, n);
+    }
+  }
+  if (!a.part) return;
+  // the block's sum of each column, in the order of its row slots
+  __shared__ float sums[kPer * LANES * 8 <= 2048 ? 2048 : 1];
+  static_assert(kPer * LANES * 8 == 2048, "one chunk of every thread at a time");
+  float* out = a.part + int64_t(blockIdx.x) * a.cols;
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sums[threadIdx.x * 8 + i] = acc[c][i];
+    __syncthreads();
+    for (int j = threadIdx.x; j < LANES * 8; j += kThreads) {
+      float t = 0.0f;
+      for (int k = 0; k < kPer; ++k) t += sums[k * LANES * 8 + j];
+      const int col = c * LANES * 8 + j;
+      if (col < a.cols) out[col] = t;
+    }
+  }
+}
+
+// Rows of more than kMaxHeld columns: a wave a row, walked twice; the weight's gradient has
+// its own kernel.
+__global__ void __launch_bounds__(kThreads) rmsnorm_bwd_wide_kernel(NormBwdArgs a) {
+  const int lane = threadIdx.x % 64;
+  const int64_t row = int64_t(blockIdx.x) * (kThreads / 64) + threadIdx.x / 64;
+  if (row >= a.rows) return;
+  const float rstd = a.rstd[row];
+  float dot = 0.0f;
+  for (int pass = 0; pass < 2; ++pass) {
+    const float mean = dot * a.inv_cols;
+    for (int c0 = 0; c0 < a.cols; c0 += 512) {
+      const int col = c0 + lane * 8, n = a.cols - col;
+      float dy[8], xh[8], w[8];
+      raw8_to_float(load_raw8(a.dy, row, col, n), a.dy.type, dy);
+      raw8_to_float(load_raw8(a.h, row, col, n), a.h.type, xh);
+      load_weight(a.w, col, n, w);
+      if (pass == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dot += dy[i] * (xh[i] * rstd) * w[i];
+      } else {
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = 0.0f;
+        if (a.dres.p) raw8_to_float(load_raw8(a.dres, row, col, n), a.dres.type, o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] += rstd * (dy[i] * w[i] - (xh[i] * rstd) * mean);
+        if (n > 0) store8(a.dh, row, col, o, n);
+      }
+    }
+    if (pass == 0) dot = row_sum<64>(dot);
+  }
+}
+
+// part[b][col] = sum over the b-th slice of the rows of dy xhat: a block takes 512 columns
+// (a wave's width) of its slice, its four waves every fourth row.
+__global__ void __launch_bounds__(kThreads) rmsnorm_dw_wide_kernel(NormBwdArgs a, int slices) {
+  const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+  const int col = blockIdx.y * 512 + lane * 8, n = a.cols - col;
+  const int64_t per = (a.rows + slices - 1) / slices, first = per * blockIdx.x;
+  const int64_t last = first + per < a.rows ? first + per : a.rows;
+  float acc[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+  for (int64_t row = first + wave; row < last; row += kThreads / 64) {
+    const float rstd = a.rstd[row];
+    float dy[8], xh[8];
+    raw8_to_float(load_raw8(a.dy, row, col, n), a.dy.type, dy);
+    raw8_to_float(load_raw8(a.h, row, col, n), a.h.type, xh);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] += dy[i] * (xh[i] * rstd);
+  }
+  __shared__ float sums[kThreads * 8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sums[threadIdx.x * 8 + i] = acc[i];
+  __syncthreads();
+  for (int j = threadIdx.x; j < 512; j += kThreads) {
+    float t = 0.0f;
+    for (int k = 0; k < kThreads / 64; ++k) t += sums[k * 512 + j];
+    if (blockIdx.y * 512 + j < a.cols) a.part[int64_t(blockIdx.x) * a.cols + blockIdx.y * 512 + j] = t;
+  }
+}
+
+int lanes_for(int cols) {
+  int lanes = 4;
+  while (lanes < 64 && lanes * 8 < cols) lanes *= 2;
+  return lanes;
+}
+
+// Blocks of the backward: enough to fill the card, few enough that their partial sums stay
+// small beside the rows.
+int bwd_blocks(int64_t rows, int cols) {
+  if (cols > kMaxHeld) return int(rows < 256 ? (rows < 1 ? 1 : rows) : 256);
+  const int64_t per = kThreads / lanes_for(cols);
+  const int64_t want = (rows + per - 1) / per;
+  return int(want < 1 ? 1 : (want > 1024 ? 1024 : want));
+}
+
+template <template <int, int> class Launch, typename Args>
+void by_width(int cols, const Args& a, unsigned blocks, hipStream_t s) {
+  const int chunks = (cols + 511) / 512;
+  switch (lanes_for(cols)) {
+    case 4: Launch<4, 1>::go(a, blocks, s); break;
+    case 8: Launch<8, 1>::go(a, blocks, s); break;
+    case 16: Launch<16, 1>::go(a, blocks, s); break;
+    case 32: Launch<32, 1>::go(a, blocks, s); break;
+    default:
+      if (chunks <= 1) Launch<64, 1>::go(a, blocks, s);
+      else if (chunks <= 2) Launch<64, 2>::go(a, blocks, s);
+      else if (chunks <= 4) Launch<64, 4>::go(a, blocks, s);
+      else Launch<64, 8>::go(a, blocks, s);
+  }
+}
+
+template <int L, int C>
+struct Fwd {
+  static void go(const NormFwdArgs& a, unsigned blocks, hipStream_t s) {
+    rmsnorm_fwd_kernel<L, C><<<blocks, kThreads, 0, s>>>(a);
+  }
+};
+template <int L, int C>
+struct Bwd {
+  static void go(const NormBwdArgs& a, unsigned blocks, hipStream_t s) {
+    rmsnorm_bwd_kernel<L, C><<<blocks, kThreads, 0, s>>>(a);
+  }
+};
+
+// A block sums 16 columns: 64 groups of parts side by side, then the groups in order.
+__global__ void __launch_bounds__(1024) sum_parts_kernel(const float* __restrict__ part, int parts, int64_t count,
+                                                          int cols, MatArg out) {
+  const int j = threadIdx.x % 16, g = threadIdx.x / 16;
+  const int64_t c = int64_t(blockIdx.x) * 16 + j;
+  float t = 0.0f;
+  if (c < count)
+    for (int p = g; p < parts; p += 64) t += part[p * count + c];
+  __shared__ float sums[64][17];
+  sums[g][j] = t;
+  __syncthreads();
+  if (g == 0 && c < count) {
+    for (int k = 1; k < 64; ++k) t += sums[k][j];
+    const int64_t at = (c / cols) * out.ld + c % cols;
+    if (out.type == GS_MAT_F32)
+      reinterpret_cast<float*>(out.p)[at] = t;
+    else
+      reinterpret_cast<uint16_t*>(out.p)[at] = uint16_t(pack_bf16(t, 0.0f));
+  }
+}
+
+}  // namespace
+
+hipError_t launch_sum_parts(const float* part, int parts, int64_t count, int cols, const MatArg& out, hipStream_t s) {
+  GSK_PROF("sum_parts", s);
+  sum_parts_kernel<<<div_up(count, 16), 1024, 0, s>>>(part, parts, count, cols, out);
+  return hipGetLastError();
+}
+
+hipError_t launch_rmsnorm_fwd(const MatArg& x, const MatArg& r, const float* w, float eps, const MatArg& h,
+                              const MatArg& ckpt, const MatArg& y, float* rstd, int64_t rows, int cols,
+                              hipStream_t s) {
+  const NormFwdArgs a{x, r, h, ckpt, y, w, rstd, eps, 1.0f / float(cols), rows, cols};
+  GSK_PROF("rmsnorm_fwd", s);
+  if (cols > kMaxHeld) {
+    rmsnorm_fwd_wide_kernel<<<div_up(rows, kThreads / 64), kThreads, 0, s>>>(a);
+  } else {
+    const int64_t want = div_up(rows, kThreads / lanes_for(cols));
+    by_width<Fwd>(cols, a, unsigned(want > 4096 ? 4096 : want), s);
+  }
+  return hipGetLastError();
+}
+
+size_t rmsnorm_bwd_ws_bytes(int64_t rows, int cols) {
+  return (size_t(bwd_blocks(rows, cols)) * size_t(cols) * 4 + 255) & ~size_t(255);
+}
+
+hipError_t launch_rmsnorm_bwd(const MatArg& dy, const MatArg& h, const float* w, const float* rstd,
+                              const MatArg& dres, const MatArg& dh, float* dweight, int64_t rows, int cols, void* ws,
+                              hipStream_t s) {
+  const int blocks = bwd_blocks(rows, cols);
+  float* part = dweight ? static_cast<float*>(ws) : nullptr;
+  const NormBwdArgs a{dy, h, dres, dh, w, rstd, part, 1.0f / float(cols), rows, cols};
+  if (cols > kMaxHeld) {
+    if (rows > 0) {
+      GSK_PROF("rmsnorm_bwd", s);
+      rmsnorm_bwd_wide_kernel<<<div_up(rows, kThreads / 64), kThreads, 0, s>>>(a);
+    }
+    if (dweight) {
+      GSK_PROF("rmsnorm_dw", s);
+      rmsnorm_dw_wide_kernel<<<dim3(blocks, div_up(cols, 512)), kThreads, 0, s>>>(a, blocks);
+    }
+  } else {
+    GSK_PROF("rmsnorm_bwd", s);
+    by_width<Bwd>(cols, a, unsigned(blocks), s);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !dweight) return e;
+  const MatArg out{reinterpret_cast<char*>(dweight), nullptr, cols, 0, GS_MAT_F32};
+  return launch_sum_parts(part, blocks, cols, cols, out, s);
+}
+
+}  // namespace gsk

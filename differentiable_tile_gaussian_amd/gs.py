@@ -18,14 +18,18 @@ LIB_PATH = os.path.join(_HERE, "libgs.so")
 
 GS_OK, GS_ERR_INVALID_ARG, GS_ERR_CAPACITY, GS_ERR_UNSUPPORTED, GS_ERR_HIP = 0, -1, -2, -3, -4
 GS_WS_PREPROCESS, GS_WS_BIN_SORT, GS_WS_LOSS, GS_WS_RENDER, GS_WS_DENSIFY, GS_WS_LOSS_CHARBONNIER = 0, 1, 2, 3, 4, 5
-GS_WS_CAMERA_GRAD, GS_WS_RELOCATE = 6, 7
+GS_WS_CAMERA_GRAD, GS_WS_RELOCATE, GS_WS_RMSNORM_BWD, GS_WS_LINEAR_BWD = 6, 7, 8, 9
 GS_GRAD_SUMS_FLOAT, GS_GRAD_SUMS_FIXED = 0, 1
+GS_MAT_F32, GS_MAT_BF16, GS_MAT_MX8 = 0, 1, 2
+GS_ACT_NONE, GS_ACT_RELU, GS_ACT_SILU, GS_ACT_GELU = 0, 1, 2, 3
+ACTIVATIONS = {"none": GS_ACT_NONE, "relu": GS_ACT_RELU, "silu": GS_ACT_SILU, "gelu": GS_ACT_GELU}
 
 EXPORTED = ("gs_preprocess", "gs_bin_sort", "gs_render_fwd", "gs_loss_l1_dssim", "gs_render_bwd",
             "gs_adam_step", "gs_render_bwd_adam", "gs_render_bwd_adam_project", "gs_render_bwd_weighted",
             "gs_camera_grad", "gs_densify_accumulate", "gs_densify", "gs_relocate", "gs_loss_charbonnier",
             "gs_workspace_bytes", "gs_loss_l1_dssim_noalloc", "gs_profile_enable", "gs_profile_query", "gs_param_floats", "gs_params_to_blocked",
-            "gs_params_from_blocked", "gs_last_error")
+            "gs_params_from_blocked", "gs_mx8_pack", "gs_mx8_unpack", "gs_rmsnorm_fwd", "gs_rmsnorm_bwd",
+            "gs_linear_fwd", "gs_linear_bwd", "gs_last_error")
 
 
 class GsError(RuntimeError):
@@ -63,6 +67,11 @@ def _cfg(cfg):
 class GsProj(C.Structure):
     _fields_ = [("splat", C.c_void_p), ("depth", C.c_void_p), ("rect", C.c_void_p), ("tiles", C.c_void_p),
                 ("order", C.c_void_p), ("n_visible", C.c_void_p), ("offs", C.c_void_p), ("rect_order", C.c_void_p)]
+
+
+class GsMatrix(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("scales", C.c_void_p), ("rows", C.c_int64), ("cols", C.c_int64),
+                ("ld", C.c_int64), ("scales_ld", C.c_int64), ("type", C.c_int32)]
 
 
 def _load():
@@ -110,6 +119,15 @@ def _load():
     lib.gs_params_from_blocked.restype = I32
     lib.gs_workspace_bytes.argtypes = [I32, I64, U32, I32, I32, P]
     lib.gs_workspace_bytes.restype = C.c_size_t
+    lib.gs_mx8_pack.argtypes = [P, P, P]
+    lib.gs_mx8_unpack.argtypes = [P, P, P]
+    lib.gs_rmsnorm_fwd.argtypes = [P, P, P, C.c_float, P, P, P, P, P]
+    lib.gs_rmsnorm_bwd.argtypes = [P, P, P, P, P, P, P, P, C.c_size_t, P]
+    lib.gs_linear_fwd.argtypes = [P, P, P, I32, P, P, P, P]
+    lib.gs_linear_bwd.argtypes = [P, P, I32, P, P, P, P, P, P, C.c_size_t, P]
+    for name in ("gs_mx8_pack", "gs_mx8_unpack", "gs_rmsnorm_fwd", "gs_rmsnorm_bwd", "gs_linear_fwd",
+                 "gs_linear_bwd"):
+        getattr(lib, name).restype = I32
     lib.gs_last_error.restype = C.c_char_p
     for name in ("gs_preprocess", "gs_bin_sort", "gs_render_fwd", "gs_loss_l1_dssim", "gs_render_bwd",
                  "gs_adam_step"):
@@ -369,6 +387,119 @@ def gs_loss_charbonnier(img, target, exposure, loss_out, dL_dimg, ws, delta=0.03
     _, H, W = img.shape
     _check(_lib.gs_loss_charbonnier(_ptr(img), _ptr(target), H, W, float(delta), _ptr(exposure), _ptr(loss_out),
                                     _ptr(dL_dimg), _ptr(dL_dexposure), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+# ---- the operators of a network over Gaussians
+
+class Mx8:
+    """An MX8 matrix: q [rows][cols] (torch.float8_e4m3fn) and scales [rows][ceil(cols / 32)]
+    (torch.float8_e8m0fnu), both with adjacent columns; the value of a column is q times its
+    32-column block's scale."""
+
+    __slots__ = ("q", "scales")
+
+    def __init__(self, q, scales):
+        self.q, self.scales = q, scales
+
+    @property
+    def shape(self):
+        return self.q.shape
+
+
+def mx8_empty(rows, cols, device="cuda"):
+    """An uninitialised MX8 matrix whose rows start at multiples of 16 bytes."""
+    q = torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.float8_e4m3fn, device=device)
+    scales = torch.empty((rows, (cols + 31) // 32), dtype=torch.float8_e8m0fnu, device=device)
+    return Mx8(q[:, :cols], scales)
+
+
+def _matrix(t, name):
+    """gs_matrix of a two-dimensional tensor (float32, bfloat16) or Mx8 with adjacent columns."""
+    if t is None:
+        return None
+    scales, sld, q = None, 0, t
+    if isinstance(t, Mx8):
+        q, s = t.q, t.scales
+        if q.dtype != torch.float8_e4m3fn or s.dtype != torch.float8_e8m0fnu or s.dim() != 2 or q.dim() != 2:
+            raise ValueError(f"{name}: an Mx8 is a float8_e4m3fn matrix with float8_e8m0fnu scales")
+        if s.shape[0] != q.shape[0] or s.shape[1] != (q.shape[1] + 31) // 32 or not _adjacent(s):
+            raise ValueError(f"{name}: scales must be [rows][ceil(cols / 32)] with adjacent columns")
+        scales, sld, kind = s.data_ptr(), _pitch(s), GS_MAT_MX8
+    elif t.dtype == torch.float32:
+        kind = GS_MAT_F32
+    elif t.dtype == torch.bfloat16:
+        kind = GS_MAT_BF16
+    else:
+        raise ValueError(f"{name}: expected float32, bfloat16 or an Mx8, got {t.dtype}")
+    if q.dim() != 2 or not _adjacent(q):
+        raise ValueError(f"{name}: expected a matrix with adjacent columns")
+    if not q.is_cuda or (scales is not None and not t.scales.is_cuda):
+        raise ValueError(f"{name}: expected device memory")
+    return C.byref(GsMatrix(q.data_ptr(), scales, q.shape[0], q.shape[1], _pitch(q), sld, kind))
+
+
+def _adjacent(t):
+    return t.shape[1] <= 1 or t.stride(1) == 1
+
+
+def _pitch(t):
+    """Elements between rows; a single row's (or an empty matrix's) stride says nothing."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _floats(t, n, name):
+    """A contiguous float32 vector of n values (None passes)."""
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != n or not t.is_cuda:
+        raise ValueError(f"{name}: expected {n} contiguous float32 values in device memory")
+    return t.data_ptr()
+
+
+def _activation(act):
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act: expected one of {', '.join(ACTIVATIONS)}, got {act!r}")
+    return ACTIVATIONS[act]
+
+
+def gs_mx8_pack(x, q, stream=None):
+    """x (float32 or bfloat16) to the Mx8 q of the same size."""
+    _check(_lib.gs_mx8_pack(_matrix(x, "x"), _matrix(q, "q"), _stream(stream)))
+
+
+def gs_mx8_unpack(q, x, stream=None):
+    """The Mx8 q's values to x (float32 or bfloat16)."""
+    _check(_lib.gs_mx8_unpack(_matrix(q, "q"), _matrix(x, "x"), _stream(stream)))
+
+
+def gs_rmsnorm_fwd(x, weight, eps, y, rstd=None, residual=None, h=None, ckpt=None, stream=None):
+    """h = x + residual, y = h (mean(h^2) + eps)^-1/2 weight by rows; ckpt: an Mx8 for h."""
+    rows, cols = x.shape
+    _check(_lib.gs_rmsnorm_fwd(_matrix(x, "x"), _matrix(residual, "residual"), _floats(weight, cols, "weight"),
+                               float(eps), _matrix(h, "h"), _matrix(ckpt, "ckpt"), _matrix(y, "y"),
+                               _floats(rstd, rows, "rstd"), _stream(stream)))
+
+
+def gs_rmsnorm_bwd(dy, h, weight, rstd, dh, dweight, ws, dres=None, stream=None):
+    """The gradients of h (plus dres) and of the weight; h: float32, bfloat16 or the Mx8 checkpoint."""
+    rows, cols = dy.shape
+    _check(_lib.gs_rmsnorm_bwd(_matrix(dy, "dy"), _matrix(h, "h"), _floats(weight, cols, "weight"),
+                               _floats(rstd, rows, "rstd"), _matrix(dres, "dres"), _matrix(dh, "dh"),
+                               _floats(dweight, cols, "dweight"), _ptr(ws), ws.numel() if ws is not None else 0,
+                               _stream(stream)))
+
+
+def gs_linear_fwd(x, w, y, bias=None, act="none", residual=None, z=None, stream=None):
+    """y = act(x w^T + bias) + residual; z (float32, bfloat16 or Mx8) receives x w^T + bias."""
+    _check(_lib.gs_linear_fwd(_matrix(x, "x"), _matrix(w, "w"), _floats(bias, w.shape[0], "bias"), _activation(act),
+                              _matrix(residual, "residual"), _matrix(z, "z"), _matrix(y, "y"), _stream(stream)))
+
+
+def gs_linear_bwd(dy, x, w, dx, dw, dbias, ws, act="none", z=None, stream=None):
+    """The gradients of x, w and the bias (each output may be None) from x and z as kept."""
+    _check(_lib.gs_linear_bwd(_matrix(dy, "dy"), _matrix(z, "z"), _activation(act), _matrix(x, "x"), _matrix(w, "w"),
+                              _matrix(dx, "dx"), _matrix(dw, "dw"), _floats(dbias, w.shape[0], "dbias"), _ptr(ws),
+                              ws.numel() if ws is not None else 0, _stream(stream)))
 
 
 def gs_profile_enable(on, only=None):

@@ -363,7 +363,6 @@ size_t gs_param_floats(int64_t n, int32_t sh_degree);
 int32_t gs_params_to_blocked(const float* planar, float* blocked, int64_t n, int32_t sh_degree, void* stream);
 int32_t gs_params_from_blocked(const float* blocked, float* planar, int64_t n, int32_t sh_degree, void* stream);
 
-/* Workspace sizes, in bytes, for the calls that take one. */
 /* Density control, statistics ([GST] density-control slide: screen-space centre gradient
  * magnitudes accumulated per visible observation).  After a step's backward (gs_render_bwd or
  * the fused calls), for every Gaussian with proj->tiles[i] > 0:
@@ -422,11 +421,99 @@ int32_t gs_relocate(float* params, float* m, float* v, int64_t n, int32_t sh_deg
                     double dead_opacity, double donor_opacity, int64_t max_moves, int64_t* moves_out, void* ws,
                     size_t ws_bytes, void* stream);
 
-enum { GS_WS_PREPROCESS = 0, GS_WS_BIN_SORT = 1, GS_WS_LOSS = 2, GS_WS_RENDER = 3, GS_WS_DENSIFY = 4,
-       GS_WS_LOSS_CHARBONNIER = 5, GS_WS_CAMERA_GRAD = 6, GS_WS_RELOCATE = 7 };
+/* ---- Networks over Gaussians.
+ *
+ * The operators of a network whose rows are Gaussians (or image tiles) and whose outputs are
+ * Gaussian parameters: RMS norm, linear layers, and 8-bit storage of what their backward
+ * passes read again.  They share the conventions above; rows and columns below are those of
+ * row-major matrices (not the blocked parameter layout).
+ *
+ * gs_matrix: element (i, j) is element i * ld + j of data, of type
+ *   GS_MAT_F32   float32
+ *   GS_MAT_BF16  bfloat16
+ *   GS_MAT_MX8   e4m3 bytes q (the microscaling format): the value is q 2^(s - 127) with s the
+ *                byte scales[i * scales_ld + j / 32], one for each 32 columns of a row (the last
+ *                block of a row may be shorter).  Written with the smallest exponent >= -126 for
+ *                which the block's largest finite magnitude is at most 448 2^(s - 127), and q the
+ *                nearest e4m3 value (ties to even), so nothing saturates; infinities and NaN
+ *                become NaN, and a NaN or infinity leaves its neighbours' scale alone.  Read with
+ *                byte 255 as NaN.
+ * There is no float16: the loss's gradients carry 1 / (3 W H), below its normal range.
+ * 0 <= rows < 2^31, 1 <= cols <= 2^20, ld >= cols, scales_ld >= ceil(cols / 32).  Any ld and any
+ * alignment of the element's own size are taken; rows that start at multiples of 16 bytes are
+ * the fast ones.  An argument marked nullable may be NULL.  With rows == 0 the row matrices'
+ * data may be NULL; sums over the rows are then zero.
+ *
+ * Outputs must not share memory with inputs or each other, except where a call says that one
+ * may be the input itself.  No call uses atomics: the results are reproducible bit for bit.
+ * Every call only enqueues. */
+typedef struct gs_matrix {
+  void* data;
+  uint8_t* scales;      /* GS_MAT_MX8 only */
+  int64_t rows, cols;
+  int64_t ld;           /* elements between rows */
+  int64_t scales_ld;    /* bytes between rows of scales */
+  int32_t type;
+} gs_matrix;
+enum { GS_MAT_F32 = 0, GS_MAT_BF16 = 1, GS_MAT_MX8 = 2 };
 
-/* Workspace size in bytes for the call `which_call` (GS_WS_*) with n Gaussians, `pairs` pairs
- * and a W x H image; cfg as the call will receive it (NULL: defaults).  The render workspace
+/* Activations of a linear layer: none, max(z, 0), z sigmoid(z), and the tanh form of gelu,
+ * z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2. */
+enum { GS_ACT_NONE = 0, GS_ACT_RELU = 1, GS_ACT_SILU = 2, GS_ACT_GELU = 3 };
+
+/* x (F32 or BF16) to q (MX8) of the same size, and back (x rounded to its type; an MX8 value
+ * is exact in both unless it overflows). */
+int32_t gs_mx8_pack(const gs_matrix* x, const gs_matrix* q, void* stream);
+int32_t gs_mx8_unpack(const gs_matrix* q, const gs_matrix* x, void* stream);
+
+/* Root-mean-square norm with the residual's addition: for every row
+ *   h = x + residual (x alone without one),  rstd = (mean(h^2) + eps)^(-1/2),
+ *   y = h rstd weight.
+ * x, residual (nullable): F32 or BF16.  weight: float[cols].  eps > 0.  h (nullable): F32 or
+ * BF16; may be x or residual itself (same type and ld).  ckpt (nullable, MX8): h in 8 bits, for
+ * gs_rmsnorm_bwd.  y: any type (MX8 is what a linear layer reads fastest and keeps).  rstd
+ * (nullable): float[rows].  The sum and y use h before it is rounded; float32 throughout. */
+int32_t gs_rmsnorm_fwd(const gs_matrix* x, const gs_matrix* residual, const float* weight, float eps,
+                       const gs_matrix* h, const gs_matrix* ckpt, const gs_matrix* y, float* rstd, void* stream);
+
+/* Its gradient: with xhat = h rstd and u = dy weight,
+ *   dh = rstd (u - xhat mean(u xhat)) + dres,   dweight = sum over the rows of dy xhat.
+ * dh is the gradient of x and of the residual alike; dres (nullable) is the gradient that
+ * reaches h past the norm.  dy, dres: F32 or BF16; h: any type (MX8: the checkpoint); dh: F32 or
+ * BF16, may be dres itself (same type and ld); dweight (nullable): float[cols], overwritten.
+ * rstd: as the forward wrote it.  ws: gs_workspace_bytes(GS_WS_RMSNORM_BWD, rows, 0, cols, 0,
+ * NULL) bytes. */
+int32_t gs_rmsnorm_bwd(const gs_matrix* dy, const gs_matrix* h, const float* weight, const float* rstd,
+                       const gs_matrix* dres, const gs_matrix* dh, float* dweight, void* ws, size_t ws_bytes,
+                       void* stream);
+
+/* Linear layer with its bias, activation and residual: z = x w^T + bias, y = act(z) + residual.
+ * x [rows][in]: BF16 or MX8; w [out][in]: BF16; bias (nullable): float[out]; residual (nullable)
+ * [rows][out]: F32 or BF16; z (nullable) [rows][out]: any type, the pre-activation kept for
+ * gs_linear_bwd; y [rows][out]: F32 or BF16, may be residual itself (same type and ld).  The
+ * products are exact, their sums float32, and y uses z before it is rounded. */
+int32_t gs_linear_fwd(const gs_matrix* x, const gs_matrix* w, const float* bias, int32_t act,
+                      const gs_matrix* residual, const gs_matrix* z, const gs_matrix* y, void* stream);
+
+/* Its gradients: dz = dy act'(z),  dx = dz w,  dw = dz^T x,  dbias = sum over the rows of dz
+ * (the residual's gradient is dy itself).  dy [rows][out]: F32 or BF16; z (nullable for
+ * GS_ACT_NONE) [rows][out]: any type; x [rows][in]: BF16 or MX8; w [out][in]: BF16; dx [rows][in],
+ * dw [out][in] (each nullable): F32 or BF16; dbias (nullable): float[out].  Outputs are
+ * overwritten.  dz is rounded to bfloat16 for the two products (dbias sums it unrounded); their
+ * sums are float32.  ws: gs_workspace_bytes(GS_WS_LINEAR_BWD, rows, 0, in, out, NULL) bytes. */
+int32_t gs_linear_bwd(const gs_matrix* dy, const gs_matrix* z, int32_t act, const gs_matrix* x, const gs_matrix* w,
+                      const gs_matrix* dx, const gs_matrix* dw, float* dbias, void* ws, size_t ws_bytes,
+                      void* stream);
+
+/* Workspace sizes, in bytes, for the calls that take one. */
+enum { GS_WS_PREPROCESS = 0, GS_WS_BIN_SORT = 1, GS_WS_LOSS = 2, GS_WS_RENDER = 3, GS_WS_DENSIFY = 4,
+       GS_WS_LOSS_CHARBONNIER = 5, GS_WS_CAMERA_GRAD = 6, GS_WS_RELOCATE = 7, GS_WS_RMSNORM_BWD = 8,
+       GS_WS_LINEAR_BWD = 9 };
+
+/* Workspace size in bytes for the call `which_call` (GS_WS_*) with n Gaussians (rows, for the
+ * network operators), `pairs` pairs and a W x H image (for the network operators W is the input
+ * width and H the output width of a linear layer, W the width of a norm); cfg as the call will
+ * receive it (NULL: defaults).  The render workspace
  * (GS_WS_RENDER) depends on cfg's split sizes and gradient-sum mode; the others do not. */
 size_t gs_workspace_bytes(int32_t which_call, int64_t n, uint32_t pairs, int32_t W, int32_t H, const gs_config* cfg);
 
