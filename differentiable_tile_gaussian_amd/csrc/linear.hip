@@ -3,70 +3,13 @@
 //
 // Every product runs on the matrix cores (16x16x32, bfloat16 operands, float32 sums):
 // bfloat16 and MX8 operands are exact there, float32 ones (and dz) are rounded to bfloat16.
-#include "matrix.h"
+#include "linear.h"
 #include "profile.h"
 
 namespace gsk {
 namespace {
 
 constexpr int kThreads = 256;
-
-// ------------------------------------------------------------- epilogue of the forward
-
-struct Epilogue {
-  const float* bias;   // nullable
-  int act;
-  MatArg r, z, y;      // residual and kept pre-activation nullable
-};
-
-// 16 columns of a row to memory; for MX8 the lanes 16 apart hold the two halves of a
-// 32-column block (all lanes active).  n: columns of the 16 that exist (<= 0: none).
-__device__ inline void store16(const MatArg& m, int64_t row, int col, const float v[16], int n) {
-  if (m.type == GS_MAT_MX8) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint32_t u = i < n ? finite_magnitude(v[i]) : 0u;
-      top = u > top ? u : top;
-    }
-    top = max_across16(top);
-    const uint32_t byte = mx8_scale_byte(top);
-    const float inv = mx8_inverse(byte);
-    u32x4 w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = mx8_encode4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], inv);
-    char* p = m.p + row * m.ld + col;
-    if (n >= 16) {
-      __builtin_memcpy(p, &w, 16);
-    } else if (n > 0) {
-      store_bytes8(p, w[0], w[1], n);
-      if (n > 8) store_bytes8(p + 8, w[2], w[3], n - 8);
-    }
-    if (n > 0 && (col & 31) == 0) m.s[row * m.lds + (col >> 5)] = uint8_t(byte);
-    return;
-  }
-  if (n > 0) store8(m, row, col, v, n);
-  if (n > 8) store8(m, row, col + 8, v + 8, n - 8);
-}
-
-// v: x W^T for 16 columns of a row.
-__device__ inline void finish16(const Epilogue& e, int64_t row, int col, float v[16], int n) {
-  if (e.bias) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] += i < n ? e.bias[col + i] : 0.0f;
-  }
-  if (e.z.p) store16(e.z, row, col, v, n);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = activate(v[i], e.act);
-  if (e.r.p) {
-    float r[16];
-    raw8_to_float(load_raw8(e.r, row, col, n), e.r.type, r);
-    raw8_to_float(load_raw8(e.r, row, col + 8, n - 8), e.r.type, r + 8);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] += r[i];
-  }
-  store16(e.y, row, col, v, n);
-}
 
 // ------------------------------------------------- tiled product, contraction contiguous
 
@@ -321,6 +264,7 @@ BwdWs carve_bwd(void* ws, int64_t rows, int k, int n) {
 hipError_t launch_linear_fwd(const MatArg& x, const MatArg& w, const float* bias, int act, const MatArg& r,
                              const MatArg& z, const MatArg& y, int64_t rows, int k, int n, hipStream_t s) {
   const Epilogue e{bias, act, r, z, y};
+  if (rows_fwd_takes(k, n)) return launch_rows_fwd(x, w, e, rows, k, n, s);
   GSK_PROF("linear_fwd", s);
   gemm_nt_kernel<1, 4, 1><<<dim3(div_up(rows, 64), div_up(n, 64)), kThreads, 0, s>>>(w, x, n, rows, k, e);
   return hipGetLastError();

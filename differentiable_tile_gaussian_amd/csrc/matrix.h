@@ -155,10 +155,23 @@ __device__ inline u32x4 raw8_to_bf16(const Raw8& r, int type) {
 
 // ---- encoding
 
-// Bits of |v|, zero for infinities and NaN: a block's scale goes by its finite values.
-__device__ inline uint32_t finite_magnitude(float v) {
-  const uint32_t u = __float_as_uint(v) & 0x7fffffffu;
-  return u < 0x7f800000u ? u : 0u;
+// The largest finite |v| of N values' bits.  The float maximum passes over NaN; only when an
+// infinity is among them are the finite ones gone through one by one.
+template <int N>
+__device__ inline uint32_t finite_top(const float* v) {
+  float top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; i += 2) top = fmaxf(fmaxf(fabsf(v[i]), fabsf(v[i + 1])), top);
+  uint32_t bits = __float_as_uint(top);
+  if (bits >= 0x7f800000u) {
+    bits = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t u = __float_as_uint(v[i]) & 0x7fffffffu;
+      bits = u < 0x7f800000u && u > bits ? u : bits;
+    }
+  }
+  return bits;
 }
 
 // The scale byte for a block whose largest finite magnitude has these bits: the exponent
@@ -169,14 +182,14 @@ __device__ inline uint32_t mx8_scale_byte(uint32_t top) {
   return uint32_t(e < 1 ? 1 : e);
 }
 
-// 1 / scale, exactly (scale bytes from mx8_scale_byte are at most 247).
-__device__ inline float mx8_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
-
-// Four values of a block to e4m3 (nearest even; infinities and NaN become NaN).
-__device__ inline uint32_t mx8_encode4(float a, float b, float c, float d, float inv) {
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, 0, false);
-  w = __builtin_amdgcn_cvt_pk_fp8_f32(c * inv, d * inv, w, true);
-  return uint32_t(w);
+// Four values of a block, divided by its scale, to e4m3 (nearest even; infinities and NaN
+// become NaN).
+__device__ inline uint32_t mx8_encode4(float a, float b, float c, float d, float scale) {
+  typedef short s16x2 __attribute__((ext_vector_type(2)));
+  s16x2 w{0, 0};
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, a, b, scale, false);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, c, d, scale, true);
+  return __builtin_bit_cast(uint32_t, w);
 }
 
 // The larger of x and the same value of the lane 16 or 32 away.
@@ -242,16 +255,9 @@ __device__ inline uint32_t max_over_quad(uint32_t x) {
 // A chunk of 8 columns to MX8, where four neighbouring lanes (all active) hold the four
 // chunks of one block; values of absent columns are zero.
 __device__ inline void store_mx8_quad(const MatArg& m, int64_t row, int col, const float v[8], int n) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t u = finite_magnitude(v[i]);
-    top = u > top ? u : top;
-  }
-  top = max_over_quad(top);
-  const uint32_t byte = mx8_scale_byte(top);
-  const float inv = mx8_inverse(byte);
-  const uint32_t a = mx8_encode4(v[0], v[1], v[2], v[3], inv), b = mx8_encode4(v[4], v[5], v[6], v[7], inv);
+  const uint32_t byte = mx8_scale_byte(max_over_quad(finite_top<8>(v)));
+  const float scale = mx8_scale(byte);
+  const uint32_t a = mx8_encode4(v[0], v[1], v[2], v[3], scale), b = mx8_encode4(v[4], v[5], v[6], v[7], scale);
   if (n > 0) {
     store_bytes8(m.p + row * m.ld + col, a, b, n);
     if ((col & 31) == 0) m.s[row * m.lds + (col >> 5)] = uint8_t(byte);
@@ -260,7 +266,11 @@ __device__ inline void store_mx8_quad(const MatArg& m, int64_t row, int col, con
 
 // ---- activations (GS_ACT_*)
 
-__device__ inline float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
+// exp2 and the reciprocal are the hardware's (1 unit in the last place each); the exponential
+// overflows to infinity and the reciprocal of that is zero.
+__device__ inline float sigmoid(float z) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
+}
 
 constexpr float kGelu = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 
@@ -271,17 +281,18 @@ __device__ inline float activate(float z, int act) {
   return z;
 }
 
-// act'(z).  With g the sigmoid of u, the slope is g + z u' g (1 - g); where g (1 - g)
-// underflows the second term's limit is zero, whatever z is.
+// act'(z).  With g the sigmoid of u, the slope is g + z u' g (1 - g).  Where g (1 - g)
+// underflows the second term's limit is zero, so its z may be bounded (an infinity would
+// make NaN of zero); a NaN in z comes through g.
 __device__ inline float act_slope(float z, int act) {
   if (act == GS_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
   if (act == GS_ACT_SILU) {
-    const float g = sigmoid(z), t = g * (1.0f - g);
-    return t == 0.0f ? g : g + z * t;
+    const float g = sigmoid(z);
+    return g + __builtin_amdgcn_fmed3f(z, -128.0f, 128.0f) * (g * (1.0f - g));
   }
   if (act == GS_ACT_GELU) {
-    const float g = sigmoid(kGelu * z * (1.0f + 0.044715f * z * z)), t = g * (1.0f - g);
-    return t == 0.0f ? g : g + z * t * kGelu * (1.0f + 0.134145f * z * z);
+    const float g = sigmoid(kGelu * z * (1.0f + 0.044715f * z * z)), b = __builtin_amdgcn_fmed3f(z, -32.0f, 32.0f);
+    return g + b * (kGelu + 0.134145f * kGelu * b * b) * (g * (1.0f - g));
   }
   return 1.0f;
 }
