@@ -62,4 +62,11 @@ bool rows_fwd_takes(int k, int n);
 hipError_t launch_rows_fwd(const MatArg& x, const MatArg& w, const Epilogue& e, int64_t rows, int k, int n,
                            hipStream_t s);
 
+// ---- linear_rows_bwd.hip: the gradients of the narrowest of them in one pass
+bool rows_bwd_takes(int k, int n);
+size_t rows_bwd_ws_bytes(int64_t rows, int k, int n);
+hipError_t launch_rows_bwd(const MatArg& dy, const MatArg& z, int act, const MatArg& x, const MatArg& w,
+                           const MatArg& dx, const MatArg& dw, float* dbias, int64_t rows, int k, int n, void* ws,
+                           hipStream_t s);
+
 }  // namespace gsk

@@ -270,11 +270,14 @@ hipError_t launch_linear_fwd(const MatArg& x, const MatArg& w, const float* bias
   return hipGetLastError();
 }
 
-size_t linear_bwd_ws_bytes(int64_t rows, int k, int n) { return carve_bwd(nullptr, rows, k, n).bytes; }
+size_t linear_bwd_ws_bytes(int64_t rows, int k, int n) {
+  return rows_bwd_takes(k, n) ? rows_bwd_ws_bytes(rows, k, n) : carve_bwd(nullptr, rows, k, n).bytes;
+}
 
 hipError_t launch_linear_bwd(const MatArg& dy, const MatArg& z, int act, const MatArg& x, const MatArg& w,
                              const MatArg& dx, const MatArg& dw, float* dbias, int64_t rows, int k, int n, void* ws,
                              hipStream_t s) {
+  if (rows_bwd_takes(k, n)) return launch_rows_bwd(dy, z, act, x, w, dx, dw, dbias, rows, k, n, ws, s);
   const BwdWs b = carve_bwd(ws, rows, k, n);
   const bool own_dz = act != GS_ACT_NONE && (dx.p || dw.p);
   const MatArg dz = own_dz ? MatArg{b.dz, nullptr, b.dz_ld, 0, GS_MAT_BF16} : dy;

@@ -1,0 +1,347 @@
+// Gradients of a narrow linear layer over many rows (in and out widths of at most 128): one
+// pass over the rows for dz, dx, dW and db.  Bounded by HBM: dy, z and x are read once and
+// dx written once; dz exists only in registers and LDS.
+//
+// A block of eight waves takes 128 rows a turn, 16 to a wave.  A lane loads the 16 columns
+// of its row that it will hold as an operand, forms dz there, adds it to its column sums
+// (db, before the rounding) and rounds it: that is the operand of dx = dz W, whose other
+// operand W^T lies in LDS.  dz and x also go to LDS as rows, where the contraction over the
+// rows, dW += dz^T x, reads them transposed; the eight waves share dW's tiles, whose sums stay
+// in registers over all of the block's turns.  The next turn's loads are issued before the
+// products of the present one.  Each block writes its sums of dW and db once; they are joined
+// in order by launch_sum_parts.
+#include "linear.h"
+#include "profile.h"
+
+namespace gsk {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kRows = 128;
+
+// 16 columns of a row as loaded, of any type.
+struct Piece {
+  u32x4 v[4];
+  uint32_t scale;
+};
+
+__device__ inline void load_piece(Piece& p, const MatArg& m, int64_t row, int col, int cols) {
+  if (col + 16 <= cols) {
+    if (m.type == GS_MAT_MX8) {
+      __builtin_memcpy(&p.v[0], m.p + row * m.ld + col, 16);
+      p.scale = m.s[row * m.lds + (col >> 5)];
+    } else if (m.type == GS_MAT_BF16) {
+      const char* a = m.p + (row * m.ld + col) * 2;
+      __builtin_memcpy(&p.v[0], __builtin_assume_aligned(a, 2), 16);
+      __builtin_memcpy(&p.v[1], __builtin_assume_aligned(a + 16, 2), 16);
+    } else {
+      const char* a = m.p + (row * m.ld + col) * 4;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) __builtin_memcpy(&p.v[i], __builtin_assume_aligned(a + 16 * i, 4), 16);
+    }
+    return;
+  }
+  const Raw8 lo = load_raw8(m, row, col, cols - col), hi = load_raw8(m, row, col + 8, cols - col - 8);
+  p.scale = lo.scale;
+  if (m.type == GS_MAT_MX8) {
+    p.v[0] = u32x4{lo.lo[0], lo.lo[1], hi.lo[0], hi.lo[1]};
+  } else if (m.type == GS_MAT_BF16) {
+    p.v[0] = lo.lo;
+    p.v[1] = hi.lo;
+  } else {
+    p.v[0] = lo.lo;
+    p.v[1] = lo.hi;
+    p.v[2] = hi.lo;
+    p.v[3] = hi.hi;
+  }
+}
+
+__device__ inline void piece_to_float(const Piece& p, int type, float v[16]) {
+  if (type == GS_MAT_MX8) {
+    const float s = mx8_scale(p.scale);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(p.v[0][i], s, false);
+      const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(p.v[0][i], s, true);
+      v[4 * i] = a[0];
+      v[4 * i + 1] = a[1];
+      v[4 * i + 2] = b[0];
+      v[4 * i + 3] = b[1];
+    }
+  } else if (type == GS_MAT_BF16) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[2 * i] = bf16_lo(p.v[i / 4][i % 4]);
+      v[2 * i + 1] = bf16_hi(p.v[i / 4][i % 4]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(p.v[i / 4][i % 4]);
+  }
+}
+
+__device__ inline void piece_to_bf16(const Piece& p, int type, u32x4& a, u32x4& b) {
+  if (type == GS_MAT_MX8) {
+    const float s = mx8_scale(p.scale);
+    const u32x2 w0 = mx8_to_bf16x4(p.v[0][0], s), w1 = mx8_to_bf16x4(p.v[0][1], s);
+    const u32x2 w2 = mx8_to_bf16x4(p.v[0][2], s), w3 = mx8_to_bf16x4(p.v[0][3], s);
+    a = u32x4{w0[0], w0[1], w1[0], w1[1]};
+    b = u32x4{w2[0], w2[1], w3[0], w3[1]};
+  } else {
+    a = p.v[0];
+    b = p.v[1];
+  }
+}
+
+// Orders LDS accesses around a barrier; global loads stay in flight across it.
+__device__ inline void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+struct RowsBwdArgs {
+  MatArg dy, z, x, w, dx;
+  float *dw, *db;   // [parts][n][k], [blocks][n]; nullptr: not wanted
+  int64_t rows;
+  int act, k, n;
+};
+
+// How the eight waves share dW: kWP groups of 64 columns (k), kWQ groups of 16 kQT rows (n),
+// and kMS shares of a turn's rows (each a part of its own).
+template <int NC, int KC>
+struct Share {
+  static constexpr int kQT = NC * KC == 4 ? 2 : 1, kWP = KC, kWQ = NC * 4 / kQT, kMS = 8 / (kWP * kWQ);
+};
+
+// NC, KC: groups of 64 columns of dz and of x.
+template <int NC, int KC>
+__global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(RowsBwdArgs a) {
+  using S = Share<NC, KC>;
+  constexpr int kPitchQ = NC * 128 + 32, kPitchP = KC * 128 + 32;
+  extern __shared__ __align__(16) uint8_t lds[];
+  uint8_t* wt = lds;                                  // NC KC 8 KiB of operands
+  uint8_t* zt = lds + NC * KC * 8192;                 // dz rows
+  uint8_t* xt = zt + kRows * kPitchQ;                 // x rows
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, g = lane / 16, r = lane % 16;
+  const int wp = wave % S::kWP, wq = wave / S::kWP % S::kWQ, ms = wave / (S::kWP * S::kWQ);
+
+  // W^T as operands of tile (kc, t), piece (nc, half): lane (g, r) holds rows n = 64 nc + 16 g
+  // + 8 half .. + 7 of column k = 64 kc + 16 (r / 4) + 4 t + r % 4.
+  for (int i = threadIdx.x; i < NC * KC * 4096; i += kThreads) {
+    const int n = i / (KC * 64), k = i % (KC * 64);
+    const uint16_t v = n < a.n && k < a.k ? reinterpret_cast<const uint16_t*>(a.w.p)[int64_t(n) * a.w.ld + k] : 0;
+    const int frag = ((k / 64 * 4 + k / 4 % 4) * NC + n / 64) * 2 + n / 8 % 2;
+    const int l = n / 16 % 4 * 16 + k / 16 % 4 * 4 + k % 4;
+    *reinterpret_cast<uint16_t*>(wt + frag * 1024 + l * 16 + n % 8 * 2) = v;
+  }
+
+  float db[NC][16];
+  f32x4 dw[S::kQT][4];
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) db[c][i] = 0.0f;
+#pragma unroll
+  for (int q = 0; q < S::kQT; ++q)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) dw[q][t] = f32x4{0, 0, 0, 0};
+
+  Piece dy[NC], z[NC], x[KC];
+  auto fetch = [&](int64_t row0) {
+    const int64_t row = row0 + wave * 16 + r;
+    const bool in = row < a.rows;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) load_piece(dy[c], a.dy, row, c * 64 + g * 16, in ? a.n : 0);
+    if (a.act != GS_ACT_NONE) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) load_piece(z[c], a.z, row, c * 64 + g * 16, in ? a.n : 0);
+    }
+    if (a.dw) {
+#pragma unroll
+      for (int c = 0; c < KC; ++c) load_piece(x[c], a.x, row, c * 64 + g * 16, in ? a.k : 0);
+    }
+  };
+  const int64_t step = int64_t(gridDim.x) * kRows;
+  fetch(int64_t(blockIdx.x) * kRows);
+  for (int64_t row0 = int64_t(blockIdx.x) * kRows; row0 < a.rows; row0 += step) {
+    u32x4 dz[NC][2];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      float v[16];
+      piece_to_float(dy[c], a.dy.type, v);
+      if (a.act != GS_ACT_NONE) {
+        float t[16];
+        piece_to_float(z[c], a.z.type, t);
+        if (a.act == GS_ACT_SILU) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] *= act_slope(t[i], GS_ACT_SILU);
+        } else if (a.act == GS_ACT_GELU) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] *= act_slope(t[i], GS_ACT_GELU);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] *= act_slope(t[i], GS_ACT_RELU);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) db[c][i] += v[i];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dz[c][i / 4][i % 4] = pack_bf16(v[2 * i], v[2 * i + 1]);
+    }
+    lds_barrier();   // the last turn's readers are done (and, at first, W^T is written)
+    if (a.dw) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        uint8_t* p = zt + (wave * 16 + r) * kPitchQ + (c * 64 + g * 16) * 2;
+        *reinterpret_cast<u32x4*>(p) = dz[c][0];
+        *reinterpret_cast<u32x4*>(p + 16) = dz[c][1];
+      }
+#pragma unroll
+      for (int c = 0; c < KC; ++c) {
+        u32x4 lo, hi;
+        piece_to_bf16(x[c], a.x.type, lo, hi);
+        uint8_t* p = xt + (wave * 16 + r) * kPitchP + (c * 64 + g * 16) * 2;
+        *reinterpret_cast<u32x4*>(p) = lo;
+        *reinterpret_cast<u32x4*>(p + 16) = hi;
+      }
+    }
+    if (row0 + step < a.rows) fetch(row0 + step);
+    lds_barrier();
+    if (a.dx.p) {
+      const int64_t row = row0 + wave * 16 + r;
+#pragma unroll
+      for (int kc = 0; kc < KC; ++kc) {
+        f32x4 acc[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          acc[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const bf16x8 wf =
+                  *reinterpret_cast<const bf16x8*>(wt + (((kc * 4 + t) * NC + c) * 2 + h) * 1024 + lane * 16);
+              acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, __builtin_bit_cast(bf16x8, dz[c][h]), acc[t], 0, 0, 0);
+            }
+        }
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = acc[i / 4][i % 4];
+        const int col = kc * 64 + g * 16;
+        if (row < a.rows && col < a.k) {
+          store8(a.dx, row, col, v, a.k - col);
+          if (col + 8 < a.k) store8(a.dx, row, col + 8, v + 8, a.k - col - 8);
+        }
+      }
+    }
+    if (a.dw) {
+#pragma unroll
+      for (int kk = 0; kk < kRows / 32 / S::kMS; ++kk) {
+        const int m = (kk * S::kMS + ms) * 32 + g * 8 + r / 4, c = lane % 4 * 4;
+        bf16x8 pf[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) pf[t] = read_transposed(xt + m * kPitchP + (wp * 64 + t * 16 + c) * 2, kPitchP);
+#pragma unroll
+        for (int q = 0; q < S::kQT; ++q) {
+          const bf16x8 qf = read_transposed(zt + m * kPitchQ + ((wq * S::kQT + q) * 16 + c) * 2, kPitchQ);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) dw[q][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[t], qf, dw[q][t], 0, 0, 0);
+        }
+      }
+    }
+  }
+
+  if (a.dw) {
+    float* out = a.dw + (int64_t(blockIdx.x) * S::kMS + ms) * a.n * a.k;
+#pragma unroll
+    for (int q = 0; q < S::kQT; ++q) {
+      const int n = (wq * S::kQT + q) * 16 + r;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = wp * 64 + t * 16 + g * 4 + i;
+          if (n < a.n && k < a.k) out[n * a.k + k] = dw[q][t][i];
+        }
+    }
+  }
+  if (a.db) {
+    // over the wave's 16 rows, then over the waves in order
+    float* sums = reinterpret_cast<float*>(zt);   // [8][NC 64]
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float t = db[c][i];
+#pragma unroll
+        for (int o = 1; o < 16; o *= 2) t += __shfl_xor(t, o);
+        if (r == 0) sums[wave * NC * 64 + c * 64 + g * 16 + i] = t;
+      }
+    __syncthreads();
+    for (int j = threadIdx.x; j < a.n; j += kThreads) {
+      float t = 0.0f;
+      for (int w = 0; w < 8; ++w) t += sums[w * NC * 64 + j];
+      a.db[int64_t(blockIdx.x) * a.n + j] = t;
+    }
+  }
+}
+
+template <int NC, int KC>
+struct Launch {
+  static constexpr size_t kLds = NC * KC * 8192 + size_t(kRows) * ((NC + KC) * 128 + 64);
+  static hipError_t go(const RowsBwdArgs& a, int blocks, hipStream_t s) {
+    static const hipError_t allowed =
+        hipFuncSetAttribute(reinterpret_cast<const void*>(&rows_bwd_kernel<NC, KC>),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, int(kLds));
+    if (allowed != hipSuccess) return allowed;
+    GSK_PROF("linear_rows_bwd", s);
+    rows_bwd_kernel<NC, KC><<<blocks, kThreads, kLds, s>>>(a);
+    return hipGetLastError();
+  }
+};
+
+// Blocks: as many as stay resident at once, each of at least two turns where there are
+// enough rows (a block's sums of dW cost about as much traffic as a turn).
+int blocks_for(int64_t rows, int k, int n) {
+  const int resident = k <= 64 && n <= 64 ? 512 : 256;
+  const int64_t turns = (rows + kRows - 1) / kRows, want = turns < 2 * resident ? (turns + 1) / 2 : resident;
+  return int(want < 1 ? 1 : want);
+}
+
+int shares(int k, int n) { return k <= 64 && n <= 64 ? 2 : 1; }
+
+inline size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
+
+}  // namespace
+
+bool rows_bwd_takes(int k, int n) { return k <= 128 && n <= 128; }
+
+size_t rows_bwd_ws_bytes(int64_t rows, int k, int n) {
+  const size_t blocks = size_t(blocks_for(rows, k, n));
+  return align256(blocks * n * 4) + blocks * shares(k, n) * size_t(n) * k * 4;
+}
+
+hipError_t launch_rows_bwd(const MatArg& dy, const MatArg& z, int act, const MatArg& x, const MatArg& w,
+                           const MatArg& dx, const MatArg& dw, float* dbias, int64_t rows, int k, int n, void* ws,
+                           hipStream_t s) {
+  const int blocks = blocks_for(rows, k, n);
+  float* db_part = static_cast<float*>(ws);
+  float* dw_part = reinterpret_cast<float*>(static_cast<char*>(ws) + align256(size_t(blocks) * n * 4));
+  const RowsBwdArgs a{dy, z, x, w, dx, dw.p ? dw_part : nullptr, dbias ? db_part : nullptr, rows, act, k, n};
+  hipError_t e;
+  if (n <= 64)
+    e = k <= 64 ? Launch<1, 1>::go(a, blocks, s) : Launch<1, 2>::go(a, blocks, s);
+  else
+    e = k <= 64 ? Launch<2, 1>::go(a, blocks, s) : Launch<2, 2>::go(a, blocks, s);
+  if (e != hipSuccess) return e;
+  if (dw.p && (e = launch_sum_parts(dw_part, blocks * shares(k, n), int64_t(n) * k, k, dw, s)) != hipSuccess) return e;
+  if (dbias) {
+    const MatArg out{reinterpret_cast<char*>(dbias), nullptr, n, 0, GS_MAT_F32};
+    return launch_sum_parts(db_part, blocks, n, n, out, s);
+  }
+  return hipSuccess;
+}
+
+}  // namespace gsk
