@@ -25,12 +25,20 @@ struct Piece {
   uint32_t scale;
 };
 
-__device__ inline void load_piece(Piece& p, const MatArg& m, int64_t row, int col, int cols) {
-  if (col + 16 <= cols) {
-    if (m.type == GS_MAT_MX8) {
+// type: m.type.  WHOLE: cols is a multiple of 16, so that a piece is there or is not.
+template <bool WHOLE>
+__device__ inline void load_piece(Piece& p, const MatArg& m, int type, int64_t row, int col, int cols) {
+  if (WHOLE && col >= cols) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p.v[i] = u32x4{0, 0, 0, 0};
+    p.scale = 0;
+    return;
+  }
+  if (WHOLE || col + 16 <= cols) {
+    if (type == GS_MAT_MX8) {
       __builtin_memcpy(&p.v[0], m.p + row * m.ld + col, 16);
       p.scale = m.s[row * m.lds + (col >> 5)];
-    } else if (m.type == GS_MAT_BF16) {
+    } else if (type == GS_MAT_BF16) {
       const char* a = m.p + (row * m.ld + col) * 2;
       __builtin_memcpy(&p.v[0], __builtin_assume_aligned(a, 2), 16);
       __builtin_memcpy(&p.v[1], __builtin_assume_aligned(a + 16, 2), 16);
@@ -43,9 +51,9 @@ __device__ inline void load_piece(Piece& p, const MatArg& m, int64_t row, int co
   }
   const Raw8 lo = load_raw8(m, row, col, cols - col), hi = load_raw8(m, row, col + 8, cols - col - 8);
   p.scale = lo.scale;
-  if (m.type == GS_MAT_MX8) {
+  if (type == GS_MAT_MX8) {
     p.v[0] = u32x4{lo.lo[0], lo.lo[1], hi.lo[0], hi.lo[1]};
-  } else if (m.type == GS_MAT_BF16) {
+  } else if (type == GS_MAT_BF16) {
     p.v[0] = lo.lo;
     p.v[1] = hi.lo;
   } else {
@@ -114,10 +122,16 @@ struct Share {
   static constexpr int kQT = NC * KC == 4 ? 2 : 1, kWP = KC, kWQ = NC * 4 / kQT, kMS = 8 / (kWP * kWQ);
 };
 
-// NC, KC: groups of 64 columns of dz and of x.
-template <int NC, int KC>
+constexpr int kAny = -1;   // a type that the arguments tell (any width)
+
+// NC, KC: groups of 64 columns of dz and of x.  DY, Z, X: the types of dy, z (GS_MAT_F32: no
+// activation) and x, widths being multiples of 16; or all kAny.
+template <int NC, int KC, int DY, int Z, int X>
 __global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(RowsBwdArgs a) {
   using S = Share<NC, KC>;
+  constexpr bool kWhole = DY != kAny;
+  const int dyt = kWhole ? DY : a.dy.type, zt_ = kWhole ? Z : a.z.type, xt_ = kWhole ? X : a.x.type;
+  const int act = Z == GS_MAT_F32 ? GS_ACT_NONE : a.act;
   constexpr int kPitchQ = NC * 128 + 32, kPitchP = KC * 128 + 32;
   extern __shared__ __align__(16) uint8_t lds[];
   uint8_t* wt = lds;                                  // NC KC 8 KiB of operands
@@ -152,14 +166,14 @@ __global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(RowsBwdArgs a) {
     const int64_t row = row0 + wave * 16 + r;
     const bool in = row < a.rows;
 #pragma unroll
-    for (int c = 0; c < NC; ++c) load_piece(dy[c], a.dy, row, c * 64 + g * 16, in ? a.n : 0);
-    if (a.act != GS_ACT_NONE) {
+    for (int c = 0; c < NC; ++c) load_piece<kWhole>(dy[c], a.dy, dyt, row, c * 64 + g * 16, in ? a.n : 0);
+    if (act != GS_ACT_NONE) {
 #pragma unroll
-      for (int c = 0; c < NC; ++c) load_piece(z[c], a.z, row, c * 64 + g * 16, in ? a.n : 0);
+      for (int c = 0; c < NC; ++c) load_piece<kWhole>(z[c], a.z, zt_, row, c * 64 + g * 16, in ? a.n : 0);
     }
     if (a.dw) {
 #pragma unroll
-      for (int c = 0; c < KC; ++c) load_piece(x[c], a.x, row, c * 64 + g * 16, in ? a.k : 0);
+      for (int c = 0; c < KC; ++c) load_piece<kWhole>(x[c], a.x, xt_, row, c * 64 + g * 16, in ? a.k : 0);
     }
   };
   const int64_t step = int64_t(gridDim.x) * kRows;
@@ -169,14 +183,14 @@ __global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(RowsBwdArgs a) {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       float v[16];
-      piece_to_float(dy[c], a.dy.type, v);
-      if (a.act != GS_ACT_NONE) {
+      piece_to_float(dy[c], dyt, v);
+      if (act != GS_ACT_NONE) {
         float t[16];
-        piece_to_float(z[c], a.z.type, t);
-        if (a.act == GS_ACT_SILU) {
+        piece_to_float(z[c], zt_, t);
+        if (act == GS_ACT_SILU) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] *= act_slope(t[i], GS_ACT_SILU);
-        } else if (a.act == GS_ACT_GELU) {
+        } else if (act == GS_ACT_GELU) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] *= act_slope(t[i], GS_ACT_GELU);
         } else {
@@ -200,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(RowsBwdArgs a) {
 #pragma unroll
       for (int c = 0; c < KC; ++c) {
         u32x4 lo, hi;
-        piece_to_bf16(x[c], a.x.type, lo, hi);
+        piece_to_bf16(x[c], xt_, lo, hi);
         uint8_t* p = xt + (wave * 16 + r) * kPitchP + (c * 64 + g * 16) * 2;
         *reinterpret_cast<u32x4*>(p) = lo;
         *reinterpret_cast<u32x4*>(p + 16) = hi;
@@ -230,8 +244,8 @@ __global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(RowsBwdArgs a) {
         for (int i = 0; i < 16; ++i) v[i] = acc[i / 4][i % 4];
         const int col = kc * 64 + g * 16;
         if (row < a.rows && col < a.k) {
-          store8(a.dx, row, col, v, a.k - col);
-          if (col + 8 < a.k) store8(a.dx, row, col + 8, v + 8, a.k - col - 8);
+          store8(a.dx, row, col, v, kWhole ? 8 : a.k - col);
+          if (kWhole || col + 8 < a.k) store8(a.dx, row, col + 8, v + 8, kWhole ? 8 : a.k - col - 8);
         }
       }
     }
@@ -288,19 +302,38 @@ __global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(RowsBwdArgs a) {
   }
 }
 
+template <int NC, int KC, int DY, int Z, int X>
+hipError_t go(const RowsBwdArgs& a, int blocks, hipStream_t s) {
+  constexpr size_t kLds = NC * KC * 8192 + size_t(kRows) * ((NC + KC) * 128 + 64);
+  static const hipError_t allowed =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(&rows_bwd_kernel<NC, KC, DY, Z, X>),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, int(kLds));
+  if (allowed != hipSuccess) return allowed;
+  GSK_PROF("linear_rows_bwd", s);
+  rows_bwd_kernel<NC, KC, DY, Z, X><<<blocks, kThreads, kLds, s>>>(a);
+  return hipGetLastError();
+}
+
+template <int NC, int KC, int DY, int Z>
+hipError_t by_x(const RowsBwdArgs& a, int blocks, hipStream_t s) {
+  return a.x.type == GS_MAT_MX8 ? go<NC, KC, DY, Z, GS_MAT_MX8>(a, blocks, s)
+                                : go<NC, KC, DY, Z, GS_MAT_BF16>(a, blocks, s);
+}
+
+template <int NC, int KC, int DY>
+hipError_t by_z(const RowsBwdArgs& a, int blocks, hipStream_t s) {
+  if (a.act == GS_ACT_NONE) return by_x<NC, KC, DY, GS_MAT_F32>(a, blocks, s);
+  return a.z.type == GS_MAT_MX8 ? by_x<NC, KC, DY, GS_MAT_MX8>(a, blocks, s) : by_x<NC, KC, DY, GS_MAT_BF16>(a, blocks, s);
+}
+
+// The types are compiled in for widths of whole 16-column pieces; other widths (and a
+// float32 z) take one kernel that reads its types from the arguments.
 template <int NC, int KC>
-struct Launch {
-  static constexpr size_t kLds = NC * KC * 8192 + size_t(kRows) * ((NC + KC) * 128 + 64);
-  static hipError_t go(const RowsBwdArgs& a, int blocks, hipStream_t s) {
-    static const hipError_t allowed =
-        hipFuncSetAttribute(reinterpret_cast<const void*>(&rows_bwd_kernel<NC, KC>),
-                            hipFuncAttributeMaxDynamicSharedMemorySize, int(kLds));
-    if (allowed != hipSuccess) return allowed;
-    GSK_PROF("linear_rows_bwd", s);
-    rows_bwd_kernel<NC, KC><<<blocks, kThreads, kLds, s>>>(a);
-    return hipGetLastError();
-  }
-};
+hipError_t by_type(const RowsBwdArgs& a, int blocks, hipStream_t s) {
+  if (a.k % 16 || a.n % 16 || (a.act != GS_ACT_NONE && a.z.type == GS_MAT_F32))
+    return go<NC, KC, kAny, kAny, kAny>(a, blocks, s);
+  return a.dy.type == GS_MAT_F32 ? by_z<NC, KC, GS_MAT_F32>(a, blocks, s) : by_z<NC, KC, GS_MAT_BF16>(a, blocks, s);
+}
 
 // Blocks: as many as stay resident at once, each of at least two turns where there are
 // enough rows (a block's sums of dW cost about as much traffic as a turn).
@@ -332,9 +365,9 @@ hipError_t launch_rows_bwd(const MatArg& dy, const MatArg& z, int act, const Mat
   const RowsBwdArgs a{dy, z, x, w, dx, dw.p ? dw_part : nullptr, dbias ? db_part : nullptr, rows, act, k, n};
   hipError_t e;
   if (n <= 64)
-    e = k <= 64 ? Launch<1, 1>::go(a, blocks, s) : Launch<1, 2>::go(a, blocks, s);
+    e = k <= 64 ? by_type<1, 1>(a, blocks, s) : by_type<1, 2>(a, blocks, s);
   else
-    e = k <= 64 ? Launch<2, 1>::go(a, blocks, s) : Launch<2, 2>::go(a, blocks, s);
+    e = k <= 64 ? by_type<2, 1>(a, blocks, s) : by_type<2, 2>(a, blocks, s);
   if (e != hipSuccess) return e;
   if (dw.p && (e = launch_sum_parts(dw_part, blocks * shares(k, n), int64_t(n) * k, k, dw, s)) != hipSuccess) return e;
   if (dbias) {
