@@ -14,47 +14,83 @@ struct Epilogue {
   MatArg r, z, y;      // residual and kept pre-activation nullable
 };
 
-// 16 columns of a row to memory; for MX8 the lanes 16 apart hold the two halves of a
-// 32-column block (all lanes active).  n: columns of the 16 that exist (<= 0: none); the
-// others' values are zero where m is MX8.
-__device__ inline void store16(const MatArg& m, int64_t row, int col, const float v[16], int n) {
-  if (m.type == GS_MAT_MX8) {
-    const uint32_t byte = mx8_scale_byte(max_across16(finite_top<16>(v)));
-    const float scale = mx8_scale(byte);
-    u32x4 w;
+constexpr int kAny = -1;    // a matrix type that the arguments tell
+constexpr int kNone = -2;   // no such matrix
+
+// 16 columns of a row in MX8; the lanes 16 apart hold the two halves of a 32-column block
+// (all lanes active).  Values of absent columns are zero.
+struct Mx8x16 {
+  u32x4 q;
+  uint32_t byte;
+};
+
+__device__ inline Mx8x16 encode16(const float v[16]) {
+  Mx8x16 o;
+  o.byte = mx8_scale_byte(max_across16(finite_top<16>(v)));
+  const float scale = mx8_scale(o.byte);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = mx8_encode4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], scale);
-    char* p = m.p + row * m.ld + col;
-    if (n >= 16) {
-      __builtin_memcpy(p, &w, 16);
-    } else if (n > 0) {
-      store_bytes8(p, w[0], w[1], n);
-      if (n > 8) store_bytes8(p + 8, w[2], w[3], n - 8);
-    }
-    if (n > 0 && (col & 31) == 0) m.s[row * m.lds + (col >> 5)] = uint8_t(byte);
-    return;
-  }
-  if (n > 0) store8(m, row, col, v, n);
-  if (n > 8) store8(m, row, col + 8, v + 8, n - 8);
+  for (int i = 0; i < 4; ++i) o.q[i] = mx8_encode4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], scale);
+  return o;
 }
 
-// v: x W^T for 16 columns of a row.
-__device__ inline void finish16(const Epilogue& e, int64_t row, int col, float v[16], int n) {
-  if (e.bias) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] += i < n ? e.bias[col + i] : 0.0f;
+// n: columns of the 16 that exist (<= 0: none).  WHOLE: all or none of the 16 exist.
+template <bool WHOLE>
+__device__ inline void store_mx8x16(const MatArg& m, int64_t row, int col, const Mx8x16& o, int n) {
+  if (n <= 0) return;
+  char* p = m.p + row * m.ld + col;
+  if (WHOLE || n >= 16) {
+    __builtin_memcpy(p, &o.q, 16);
+  } else {
+    store_bytes8(p, o.q[0], o.q[1], n);
+    if (n > 8) store_bytes8(p + 8, o.q[2], o.q[3], n - 8);
   }
-  if (e.z.p) store16(e.z, row, col, v, n);
+  if ((col & 31) == 0) m.s[row * m.lds + (col >> 5)] = uint8_t(o.byte);
+}
+
+// 16 columns of a row to memory (all lanes active for MX8).
+template <bool WHOLE>
+__device__ inline void store16(const MatArg& m, int type, int64_t row, int col, const float v[16], int n) {
+  if (type == GS_MAT_MX8) {
+    store_mx8x16<WHOLE>(m, row, col, encode16(v), n);
+    return;
+  }
+  if (n <= 0) return;
+  if (type == GS_MAT_F32) {
+    float* p = reinterpret_cast<float*>(m.p) + row * m.ld + col;
+    store_f32x8(p, v, WHOLE ? 8 : n);
+    if (WHOLE || n > 8) store_f32x8(p + 8, v + 8, WHOLE ? 8 : n - 8);
+  } else {
+    char* p = m.p + (row * m.ld + col) * 2;
+    store_bf16x8(p, v, WHOLE ? 8 : n);
+    if (WHOLE || n > 8) store_bf16x8(p + 16, v + 8, WHOLE ? 8 : n - 8);
+  }
+}
+
+template <int ACT>
+__device__ inline void activate16(float v[16]) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = activate(v[i], e.act);
-  if (e.r.p) {
+  for (int i = 0; i < 16; ++i) v[i] = activate(v[i], ACT);
+}
+
+// v: x W^T (with the bias) for 16 columns of a row.  Z, Y: the types of z and y, or kAny,
+// or kNone for z.
+template <bool WHOLE, int Z, int Y>
+__device__ inline void finish16(const Epilogue& e, int64_t row, int col, float v[16], int n) {
+  if (Z != kNone && (Z != kAny || e.z.p)) store16<WHOLE>(e.z, Z == kAny ? e.z.type : Z, row, col, v, n);
+  if (e.act == GS_ACT_SILU)
+    activate16<GS_ACT_SILU>(v);
+  else if (e.act == GS_ACT_GELU)
+    activate16<GS_ACT_GELU>(v);
+  else if (e.act == GS_ACT_RELU)
+    activate16<GS_ACT_RELU>(v);
+  if (e.r.p && n > 0) {
     float r[16];
-    raw8_to_float(load_raw8(e.r, row, col, n), e.r.type, r);
-    raw8_to_float(load_raw8(e.r, row, col + 8, n - 8), e.r.type, r + 8);
+    raw8_to_float(load_raw8(e.r, row, col, WHOLE ? 8 : n), e.r.type, r);
+    raw8_to_float(load_raw8(e.r, row, col + 8, WHOLE ? 8 : n - 8), e.r.type, r + 8);
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] += r[i];
   }
-  store16(e.y, row, col, v, n);
+  store16<WHOLE>(e.y, Y == kAny ? e.y.type : Y, row, col, v, n);
 }
 
 // ---- linear_rows.hip: narrow layers over many rows, the weight kept in LDS

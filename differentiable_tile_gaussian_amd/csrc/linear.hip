@@ -78,7 +78,11 @@ __global__ void __launch_bounds__(WP* WQ * 64) gemm_nt_kernel(MatArg P, MatArg Q
     for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[4 * t + j] = acc[i][t][j];
-    finish16(e, row, int(col), v, row < nq ? int(np - col < 16 ? np - col : 16) : 0);
+    if (e.bias) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] += col + i < np ? e.bias[col + i] : 0.0f;
+    }
+    finish16<false, kAny, kAny>(e, row, int(col), v, row < nq ? int(np - col < 16 ? np - col : 16) : 0);
   }
 }
 

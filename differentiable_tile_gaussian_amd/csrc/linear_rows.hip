@@ -1,37 +1,33 @@
-// Linear layers of narrow width over many rows (Gaussians): K and N of at most a few
-// hundred, where a row's input and output are a few hundred bytes and the weight fits a
-// compute unit's LDS.  Bounded by HBM (and, with an activation, closely by the vector ALU),
-// so each row's operands go from memory straight into matrix-core operands in registers
-// and each result from the accumulators to memory.
+// Linear layers of narrow width over many rows (Gaussians): widths of at most 256, where a
+// row's input and output are a few hundred bytes and the weight fits a compute unit's LDS.
+// Bounded by HBM, so each row's operands go from memory straight into matrix-core operands
+// in registers and each result from the accumulators to memory.
+//
+// Both operands are taken in pieces of 64 k in which lane group g = lane / 16 holds
+// k = 16 g .. 16 g + 15 (two 16x16x32 products): 32 contiguous bytes of bfloat16 or 16 of MX8
+// a lane, 128 or 64 a row.  The results come in groups of 64 columns, tile t holding the
+// columns 16 g + 4 t + i, so that a lane's four tiles are 16 consecutive columns of one row:
+// wide stores, and half an MX8 block.
 #include "linear.h"
 #include "profile.h"
 
 namespace gsk {
 namespace {
 
-constexpr int kThreads = 256;
-
-// Both operands are taken in pieces of 64 k in which lane group g = lane / 16 holds
-// k = 16 g .. 16 g + 15 (two 16x16x32 products): 32 contiguous bytes of bfloat16 or 16 of MX8
-// a lane, 128 or 64 a row.  The sum's order over k is the matrix core's.
-
-// Piece kc of a row: as loaded, and as two operands.
+// Piece kc of a row as loaded, and as two operands.
 template <bool MX>
 struct Piece;
 
 template <>
 struct Piece<false> {
   u32x4 a, b;
-  template <bool FULL>
-  __device__ void load(const MatArg& x, int64_t row, int k, int cols) {
-    if (FULL) {
-      const char* p = x.p + (row * x.ld + k) * 2;
-      __builtin_memcpy(&a, __builtin_assume_aligned(p, 2), 16);
-      __builtin_memcpy(&b, __builtin_assume_aligned(p + 16, 2), 16);
-    } else {
-      a = load_raw8(x, row, k, cols - k).lo;
-      b = load_raw8(x, row, k + 8, cols - k - 8).lo;
-    }
+  __device__ void load(Buffer data, Buffer, uint32_t off, uint32_t, int kc) {
+    a = buffer_load16(data, off + kc * 128);
+    b = buffer_load16(data, off + kc * 128 + 16);
+  }
+  __device__ void load_any(const MatArg& x, int64_t row, int k, int cols) {
+    a = load_raw8(x, row, k, cols - k).lo;
+    b = load_raw8(x, row, k + 8, cols - k - 8).lo;
   }
   __device__ void operands(bf16x8& p, bf16x8& q) const {
     p = __builtin_bit_cast(bf16x8, a);
@@ -43,16 +39,14 @@ template <>
 struct Piece<true> {
   u32x4 a;
   uint32_t scale;
-  template <bool FULL>
-  __device__ void load(const MatArg& x, int64_t row, int k, int cols) {
-    if (FULL) {
-      __builtin_memcpy(&a, x.p + row * x.ld + k, 16);
-      scale = x.s[row * x.lds + (k >> 5)];
-    } else {
-      const Raw8 lo = load_raw8(x, row, k, cols - k), hi = load_raw8(x, row, k + 8, cols - k - 8);
-      a = u32x4{lo.lo[0], lo.lo[1], hi.lo[0], hi.lo[1]};
-      scale = lo.scale;
-    }
+  __device__ void load(Buffer data, Buffer scales, uint32_t off, uint32_t soff, int kc) {
+    a = buffer_load16(data, off + kc * 64);
+    scale = buffer_load1(scales, soff + kc * 2);
+  }
+  __device__ void load_any(const MatArg& x, int64_t row, int k, int cols) {
+    const Raw8 lo = load_raw8(x, row, k, cols - k), hi = load_raw8(x, row, k + 8, cols - k - 8);
+    a = u32x4{lo.lo[0], lo.lo[1], hi.lo[0], hi.lo[1]};
+    scale = lo.scale;
   }
   __device__ void operands(bf16x8& p, bf16x8& q) const {
     const float s = mx8_scale(scale);
@@ -63,132 +57,323 @@ struct Piece<true> {
   }
 };
 
-// y for 64 columns at a time: tile t of a group of 64 holds the columns 16 g + 4 t + i, so a
-// lane's four tiles are 16 consecutive columns of one row.
-//
-// The block's part of W (groups of 64 columns c0 .. c0 + nc) lies in LDS as operands,
-// 1 KiB for each (column group, tile, piece, half): a read is 64 consecutive 16-byte words.
-// Wave w of the grid takes rows in turns of 16 MT; the next turn's rows are loaded before
-// the present one is computed.
-template <int KC, bool MX, bool FULL, int MT>
-__global__ void __launch_bounds__(kThreads) rows_fwd_kernel(MatArg x, MatArg w, Epilogue e, int64_t rows, int k, int n,
-                                                             int groups) {
-  extern __shared__ __align__(16) uint8_t lds[];
-  const int c0 = blockIdx.y * groups;
-  const int nc = (n + 63) / 64 - c0 < groups ? (n + 63) / 64 - c0 : groups;
-  const int lane = threadIdx.x % 64, g = lane / 16, r = lane % 16;
-  const uint8_t* wl = lds + lane * 16;
-  float* bias = reinterpret_cast<float*>(lds + size_t(groups) * KC * 8192);
-  for (int f = threadIdx.x; f < nc * KC * 512; f += kThreads) {
+// The block's part of W (nc groups of 64 columns from group c0) as operands, 1 KiB for each
+// (column group, tile, piece, half), so that a read is 64 consecutive 16-byte words; and the
+// bias, from which the sums start.
+template <int KC>
+__device__ inline void stage_weight(const MatArg& w, const float* bias, int k, int n, int c0, int nc, uint8_t* wl,
+                                    float* bl) {
+  for (int f = threadIdx.x; f < nc * KC * 512; f += blockDim.x) {
     const int l = f % 64, frag = f / 64, half = frag % 2, kc = frag / 2 % KC, t = frag / (2 * KC) % 4;
     const int c = frag / (8 * KC);
     const int row = (c0 + c) * 64 + l % 16 / 4 * 16 + t * 4 + l % 4, col = kc * 64 + l / 16 * 16 + half * 8;
-    *reinterpret_cast<u32x4*>(lds + size_t(f) * 16) = load_raw8(w, row, col, row < n ? k - col : 0).lo;
+    *reinterpret_cast<u32x4*>(wl + size_t(f) * 16) = load_raw8(w, row, col, row < n ? k - col : 0).lo;
   }
-  for (int j = threadIdx.x; j < nc * 64; j += kThreads)
-    bias[j] = e.bias && c0 * 64 + j < n ? e.bias[c0 * 64 + j] : 0.0f;
-  e.bias = nullptr;   // the sums start from it
+  for (int j = threadIdx.x; j < nc * 64; j += blockDim.x) bl[j] = bias && c0 * 64 + j < n ? bias[c0 * 64 + j] : 0.0f;
+}
+
+// One column group's sums for 16 MT rows.  The weight does not change from turn to turn; the
+// compiler must not see that, or it keeps all of it in registers it does not have (KEEP: it may).
+template <int KC, int MT, bool KEEP>
+__device__ inline void products(const uint8_t* wl, const float* bl, int c, int lane, const bf16x8 (&xf)[MT][KC][2],
+                                f32x4 (&acc)[MT][4]) {
+  if (!KEEP) asm volatile("" : "+v"(lane));
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const f32x4 b = *reinterpret_cast<const f32x4*>(bl + c * 64 + lane / 16 * 16 + t * 4);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[m][t] = b;
+#pragma unroll
+    for (int kc = 0; kc < KC; ++kc)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bf16x8 wf = *reinterpret_cast<const bf16x8*>(wl + (((c * 4 + t) * KC + kc) * 2 + h) * 1024 + lane * 16);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf[m][kc][h], acc[m][t], 0, 0, 0);
+      }
+  }
+}
+
+__device__ inline void activate_any(float v[16], int act) {
+  if (act == GS_ACT_SILU)
+    activate16<GS_ACT_SILU>(v);
+  else if (act == GS_ACT_GELU)
+    activate16<GS_ACT_GELU>(v);
+  else if (act == GS_ACT_RELU)
+    activate16<GS_ACT_RELU>(v);
+}
+
+// Rows from row0 on, as far as a turn looks.
+__device__ inline int rows_left(int64_t rows, int64_t row0) {
+  const int64_t left = rows - row0;
+  return left > 1024 ? 1024 : left < 0 ? 0 : int(left);
+}
+
+struct RowsArgs {
+  MatArg x, w;
+  Epilogue e;
+  int64_t rows;
+  int k, n;
+};
+
+// Rows taken in turns of 16 MT by each wave of the grid; a turn's loads are issued before the
+// turn in front of it is computed.  The widths are multiples of 16 and every access goes
+// through buffers (matrix.h): no branch is taken between a load and its use, so the waits are
+// for the loads alone and the stores drain behind them.
+// KC, NC: pieces of k and groups of columns.  MX: x is MX8.  Z: MX8 or kNone.  R: the
+// residual's type or kNone.
+template <int KC_, int NC_, bool MX_, int Z_, int Y_, int R_>
+struct Shape {
+  static constexpr int KC = KC_, NC = NC_, Z = Z_, Y = Y_, R = R_;
+  static constexpr bool MX = MX_;
+  static constexpr int kMT = KC <= 2 && KC * NC <= 4 && R == kNone ? 2 : 1;
+  static constexpr int kThreads = KC * NC <= 4 ? 256 : KC * NC <= 8 ? 384 : 512;
+  static constexpr int kWaves = KC * NC <= 8 ? 3 : 2;   // per SIMD
+  static constexpr size_t kLds = NC * (KC * 8192 + 256);
+};
+
+template <class S>
+__global__ void __launch_bounds__(S::kThreads, S::kWaves) rows_fwd_kernel(RowsArgs a) {
+  constexpr int KC = S::KC, NC = S::NC, Z = S::Z, Y = S::Y, R = S::R, MT = S::kMT;
+  constexpr bool MX = S::MX;
+  extern __shared__ __align__(16) uint8_t lds[];
+  float* bl = reinterpret_cast<float*>(lds + NC * KC * 8192);
+  const int c0 = blockIdx.y * NC, col0 = c0 * 64;
+  const int nc = (a.n + 63) / 64 - c0 < NC ? (a.n + 63) / 64 - c0 : NC;
+  stage_weight<KC>(a.w, a.e.bias, a.k, a.n, c0, nc, lds, bl);
   __syncthreads();
-  const int64_t step = int64_t(gridDim.x) * (kThreads / 64) * (16 * MT);
-  int64_t row0 = (int64_t(blockIdx.x) * (kThreads / 64) + threadIdx.x / 64) * (16 * MT);
-  if (row0 >= rows) return;
+  const int lane = threadIdx.x % 64, g = lane / 16, r = lane % 16;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int turns = int((a.rows + 16 * MT - 1) / (16 * MT)), step = gridDim.x * (S::kThreads / 64);
+  int turn = blockIdx.x * (S::kThreads / 64) + wave;
+
+  const uint32_t xp = uint32_t(a.x.ld) * (MX ? 1 : 2), xs = uint32_t(a.x.lds);
+  const bool last_piece = (KC - 1) * 64 + g * 16 < a.k;
   Piece<MX> next[MT][KC];
-  auto fetch = [&](int64_t from) {
+  auto fetch = [&](int t) {
+    const int64_t from = int64_t(__builtin_amdgcn_readfirstlane(t)) * (16 * MT);
+    const Buffer data = buffer_at(a.x.p + from * xp), scales = buffer_at(MX ? a.x.s + from * xs : nullptr);
+    const int left = rows_left(a.rows, from);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const int64_t row = from + m * 16 + r < rows ? from + m * 16 + r : rows - 1;   // past the end: not used
+      const bool in = m * 16 + r < left;
+      const uint32_t off = (m * 16 + r) * xp + g * (MX ? 16 : 32), soff = (m * 16 + r) * xs + g / 2;
 #pragma unroll
-      for (int kc = 0; kc < KC; ++kc) next[m][kc].template load<FULL>(x, row, kc * 64 + g * 16, k);
+      for (int kc = 0; kc < KC; ++kc) {
+        const bool there = in && (kc < KC - 1 || last_piece);
+        next[m][kc].load(data, scales, there ? off : kAbsent, there ? soff : kAbsent, kc);
+      }
     }
   };
-  fetch(row0);
-  for (; row0 < rows; row0 += step) {
-    bf16x8 xf[MT][KC][2];
+  fetch(turn);
+  bf16x8 xf[MT][KC][2];
+  auto convert = [&]() {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int kc = 0; kc < KC; ++kc) next[m][kc].operands(xf[m][kc][0], xf[m][kc][1]);
-    if (row0 + step < rows) fetch(row0 + step);
-    for (int c = 0; c < nc; ++c) {
+  };
+  convert();
+  for (; turn < turns; turn += step) {
+    const int64_t row0 = int64_t(__builtin_amdgcn_readfirstlane(turn)) * (16 * MT);
+    const int left = rows_left(a.rows, row0);
+    // where this turn's rows of the outputs lie; absent rows have no place
+    constexpr int kY = element_bytes(Y), kR = R == kNone ? 1 : element_bytes(R);
+    const Buffer yb = buffer_at(a.e.y.p + (row0 * a.e.y.ld + col0) * kY);
+    const Buffer zb = buffer_at(Z == kNone ? nullptr : a.e.z.p + row0 * a.e.z.ld + col0);
+    const Buffer sb = buffer_at(Z == kNone ? nullptr : a.e.z.s + row0 * a.e.z.lds + col0 / 32);
+    const Buffer rb = buffer_at(R == kNone ? nullptr : a.e.r.p + (row0 * a.e.r.ld + col0) * kR);
+    u32x4 res[MT][NC][R == GS_MAT_F32 ? 4 : 2];
+    if (R != kNone) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const bool there = m * 16 + r < left && col0 + c * 64 + g * 16 < a.n;
+          const uint32_t off = ((m * 16 + r) * uint32_t(a.e.r.ld) + c * 64 + g * 16) * kR;
+#pragma unroll
+          for (int i = 0; i < (R == GS_MAT_F32 ? 4 : 2); ++i)
+            res[m][c][i] = buffer_load16(rb, there ? off + i * 16 : kAbsent);
+        }
+    }
+    fetch(turn + step);   // past the last row: all absent
+    // MX8 z of two column groups, written together: the halves of a 128-byte line written
+    // microseconds apart leave the L2 one by one (1M rows of 128
+    // with silu: 148 us, written together 135)
+    Mx8x16 zz[MT][2];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
       f32x4 acc[MT][4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const f32x4 b = *reinterpret_cast<const f32x4*>(bias + c * 64 + g * 16 + t * 4);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) acc[m][t] = b;
-      }
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int kc = 0; kc < KC; ++kc)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const bf16x8 wf =
-                *reinterpret_cast<const bf16x8*>(wl + (((c * 4 + t) * KC + kc) * 2 + h) * 1024);
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-              acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf[m][kc][h], acc[m][t], 0, 0, 0);
-          }
-      const int col = (c0 + c) * 64 + g * 16;
+      products<KC, MT, KC * NC == 1>(lds, bl, c, lane, xf, acc);
+      const int col = c * 64 + g * 16;
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const int64_t row = row0 + m * 16 + r;
+        const bool there = m * 16 + r < left && col0 + col < a.n;
         float v[16];
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int i = 0; i < 16; ++i) v[i] = acc[m][i / 4][i % 4];
+        if (Z == GS_MAT_MX8) {
+          zz[m][c % 2] = encode16(v);
+          if (c % 2 || c == NC - 1) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[4 * t + i] = acc[m][t][i];
-        finish16(e, row, col, v, row < rows ? (n - col < 16 ? n - col : 16) : 0);
+            for (int h = 0; h <= c % 2; ++h) {
+              const int zc = (c - c % 2 + h) * 64 + g * 16;
+              const bool at = m * 16 + r < left && col0 + zc < a.n;
+              buffer_store16(zb, at ? (m * 16 + r) * uint32_t(a.e.z.ld) + zc : kAbsent, zz[m][h].q);
+              buffer_store1(sb, at && g % 2 == 0 ? (m * 16 + r) * uint32_t(a.e.z.lds) + zc / 32 : kAbsent, zz[m][h].byte);
+            }
+          }
+        }
+        activate_any(v, a.e.act);
+        if (R == GS_MAT_F32) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(res[m][c][i / 4][i % 4]);
+        } else if (R == GS_MAT_BF16) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            v[2 * i] += bf16_lo(res[m][c][i / 4][i % 4]);
+            v[2 * i + 1] += bf16_hi(res[m][c][i / 4][i % 4]);
+          }
+        }
+        const uint32_t off = ((m * 16 + r) * uint32_t(a.e.y.ld) + col) * kY;
+        if (Y == GS_MAT_F32) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const f32x4 o{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+            buffer_store16(yb, there ? off + i * 16 : kAbsent, __builtin_bit_cast(u32x4, o));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float* o = v + 8 * i;
+            buffer_store16(yb, there ? off + i * 16 : kAbsent,
+                           u32x4{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
+                                 pack_bf16(o[6], o[7])});
+          }
+        }
       }
+    }
+    convert();   // the wait for the next turn's loads, behind this turn's stores
+  }
+}
+
+// Any width, alignment and types: the same products with loads and stores piece by piece.
+constexpr int kAnyThreads = 256;
+
+template <int KC, bool MX>
+__global__ void __launch_bounds__(kAnyThreads) rows_fwd_any_kernel(RowsArgs a, int groups) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  float* bl = reinterpret_cast<float*>(lds + size_t(groups) * KC * 8192);
+  const int c0 = blockIdx.y * groups;
+  const int nc = (a.n + 63) / 64 - c0 < groups ? (a.n + 63) / 64 - c0 : groups;
+  stage_weight<KC>(a.w, a.e.bias, a.k, a.n, c0, nc, lds, bl);
+  __syncthreads();
+  const int lane = threadIdx.x % 64, g = lane / 16, r = lane % 16;
+  const int64_t step = int64_t(gridDim.x) * (kAnyThreads / 64) * 16;
+  for (int64_t row0 = (int64_t(blockIdx.x) * (kAnyThreads / 64) + threadIdx.x / 64) * 16; row0 < a.rows; row0 += step) {
+    const int64_t row = row0 + r;
+    Piece<MX> piece[KC];
+    bf16x8 xf[1][KC][2];
+#pragma unroll
+    for (int kc = 0; kc < KC; ++kc) piece[kc].load_any(a.x, row, kc * 64 + g * 16, row < a.rows ? a.k : 0);
+#pragma unroll
+    for (int kc = 0; kc < KC; ++kc) piece[kc].operands(xf[0][kc][0], xf[0][kc][1]);
+    for (int c = 0; c < nc; ++c) {
+      f32x4 acc[1][4];
+      products<KC, 1, false>(lds, bl, c, lane, xf, acc);
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = acc[0][i / 4][i % 4];
+      const int col = (c0 + c) * 64 + g * 16;
+      finish16<false, kAny, kAny>(a.e, row, col, v, row < a.rows ? (a.n - col < 16 ? a.n - col : 16) : 0);
     }
   }
 }
 
-constexpr int kMaxLds = 128 << 10;
+constexpr int kMaxLds = 132 << 10;
 
-size_t lds_bytes(int kc, int groups) { return size_t(groups) * (kc * 8192 + 256); }
+// Column groups per block: with few rows they go to blocks of their own.
+int split_for(int64_t turns, int groups) { return turns * groups <= 512 ? groups : 1; }
 
-template <int KC, bool MX, bool FULL>
-hipError_t go(const MatArg& x, const MatArg& w, const Epilogue& e, int64_t rows, int k, int n, hipStream_t s) {
-  constexpr int MT = KC <= 2 ? 2 : 1;
-  const int all = (n + 63) / 64;
-  const int64_t turns = div_up(rows, 16 * MT * (kThreads / 64));
-  // few rows: the column groups go to blocks of their own
-  const int split = turns * all <= 512 ? all : 1;
-  const int groups = (all + split - 1) / split;
-  const size_t lds = lds_bytes(KC, groups);
-  static const hipError_t allowed = hipFuncSetAttribute(
-      reinterpret_cast<const void*>(&rows_fwd_kernel<KC, MX, FULL, MT>), hipFuncAttributeMaxDynamicSharedMemorySize,
-      kMaxLds);
+int64_t blocks_for(int64_t turns, size_t lds, int most) {
+  const int fit = int((160 << 10) / lds), resident = fit < most ? fit : most;
+  return turns < 256 * resident ? turns : 256 * resident;
+}
+
+template <int KC, int NC, bool MX, int Z, int Y, int R>
+hipError_t go(const RowsArgs& a, hipStream_t s) {
+  using S = Shape<KC, NC, MX, Z, Y, R>;
+  const auto kernel = &rows_fwd_kernel<S>;
+  static const hipError_t allowed = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                                        hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLds);
   if (allowed != hipSuccess) return allowed;
-  const int resident = int((160 << 10) / lds) < 4 ? int((160 << 10) / lds) : 4;
-  const int64_t blocks = turns < 256 * resident ? turns : 256 * resident;
+  const int64_t turns = div_up(a.rows, 16 * S::kMT * (S::kThreads / 64));
   GSK_PROF("linear_rows_fwd", s);
-  rows_fwd_kernel<KC, MX, FULL, MT><<<dim3(unsigned(blocks), split), kThreads, lds, s>>>(x, w, e, rows, k, n, groups);
+  kernel<<<dim3(unsigned(blocks_for(turns, S::kLds, S::kWaves * 256 / S::kThreads)), div_up(a.n, NC * 64)), S::kThreads,
+           S::kLds, s>>>(a);
   return hipGetLastError();
 }
 
+template <int KC, int NC, bool MX>
+hipError_t by_output(const RowsArgs& a, hipStream_t s) {
+  const bool f32 = a.e.y.type == GS_MAT_F32;
+  if (a.e.z.p) return go<KC, NC, MX, GS_MAT_MX8, GS_MAT_BF16, kNone>(a, s);
+  if (a.e.r.p)
+    return f32 ? go<KC, NC, MX, kNone, GS_MAT_F32, GS_MAT_F32>(a, s) : go<KC, NC, MX, kNone, GS_MAT_BF16, GS_MAT_BF16>(a, s);
+  return f32 ? go<KC, NC, MX, kNone, GS_MAT_F32, kNone>(a, s) : go<KC, NC, MX, kNone, GS_MAT_BF16, kNone>(a, s);
+}
+
+template <int KC, int NC>
+hipError_t by_input(const RowsArgs& a, hipStream_t s) {
+  return a.x.type == GS_MAT_MX8 ? by_output<KC, NC, true>(a, s) : by_output<KC, NC, false>(a, s);
+}
+
 template <int KC>
-hipError_t by_type(const MatArg& x, const MatArg& w, const Epilogue& e, int64_t rows, int k, int n, hipStream_t s) {
-  const bool full = k == KC * 64;
-  if (x.type == GS_MAT_MX8)
-    return full ? go<KC, true, true>(x, w, e, rows, k, n, s) : go<KC, true, false>(x, w, e, rows, k, n, s);
-  return full ? go<KC, false, true>(x, w, e, rows, k, n, s) : go<KC, false, false>(x, w, e, rows, k, n, s);
+hipError_t by_columns(const RowsArgs& a, hipStream_t s) {
+  const int groups = (a.n + 63) / 64;
+  if (split_for(div_up(a.rows, 128), groups) == groups) return by_input<KC, 1>(a, s);
+  return groups <= 2 ? by_input<KC, 2>(a, s) : by_input<KC, 4>(a, s);
+}
+
+template <int KC, bool MX>
+hipError_t go_any(const RowsArgs& a, hipStream_t s) {
+  static const hipError_t allowed =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(&rows_fwd_any_kernel<KC, MX>),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLds);
+  if (allowed != hipSuccess) return allowed;
+  const int all = (a.n + 63) / 64;
+  const int64_t turns = div_up(a.rows, 16 * (kAnyThreads / 64));
+  const int split = split_for(turns, all), groups = (all + split - 1) / split;
+  const size_t lds = size_t(groups) * (KC * 8192 + 256);
+  GSK_PROF("linear_rows_fwd_any", s);
+  rows_fwd_any_kernel<KC, MX>
+      <<<dim3(unsigned(blocks_for(turns, lds, 4)), split), kAnyThreads, lds, s>>>(a, groups);
+  return hipGetLastError();
+}
+
+// The fast kernel's conditions: whole 16-column pieces, buffers, and one of the combinations
+// of outputs that a network makes (a kept MX8 z, or a residual of y's type, or neither).
+bool fast(const RowsArgs& a) {
+  const Epilogue& e = a.e;
+  if (a.k % 16 || a.n % 16 || !buffer_ok(a.x) || !buffer_ok(e.y) || !buffer_ok(e.z) || !buffer_ok(e.r)) return false;
+  if (e.z.p) return e.z.type == GS_MAT_MX8 && e.y.type == GS_MAT_BF16 && !e.r.p;
+  return !e.r.p || e.r.type == e.y.type;
 }
 
 }  // namespace
 
-bool rows_fwd_takes(int k, int n) {
-  return k <= 256 && lds_bytes((k + 63) / 64, (n + 63) / 64) <= kMaxLds;
-}
+bool rows_fwd_takes(int k, int n) { return k <= 256 && n <= 256; }
 
 hipError_t launch_rows_fwd(const MatArg& x, const MatArg& w, const Epilogue& e, int64_t rows, int k, int n,
                            hipStream_t s) {
+  const RowsArgs a{x, w, e, rows, k, n};
+  const bool mx = x.type == GS_MAT_MX8;
+  if (fast(a)) return k <= 64 ? by_columns<1>(a, s) : k <= 128 ? by_columns<2>(a, s) : by_columns<4>(a, s);
   switch ((k + 63) / 64) {
-    case 1: return by_type<1>(x, w, e, rows, k, n, s);
-    case 2: return by_type<2>(x, w, e, rows, k, n, s);
-    case 3: return by_type<3>(x, w, e, rows, k, n, s);
-    default: return by_type<4>(x, w, e, rows, k, n, s);
+    case 1: return mx ? go_any<1, true>(a, s) : go_any<1, false>(a, s);
+    case 2: return mx ? go_any<2, true>(a, s) : go_any<2, false>(a, s);
+    default: return mx ? go_any<4, true>(a, s) : go_any<4, false>(a, s);
   }
 }
 

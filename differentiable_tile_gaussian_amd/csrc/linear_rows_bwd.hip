@@ -122,8 +122,6 @@ struct Share {
   static constexpr int kQT = NC * KC == 4 ? 2 : 1, kWP = KC, kWQ = NC * 4 / kQT, kMS = 8 / (kWP * kWQ);
 };
 
-constexpr int kAny = -1;   // a type that the arguments tell (any width)
-
 // NC, KC: groups of 64 columns of dz and of x.  DY, Z, X: the types of dy, z (GS_MAT_F32: no
 // activation) and x, widths being multiples of 16; or all kAny.
 template <int NC, int KC, int DY, int Z, int X>

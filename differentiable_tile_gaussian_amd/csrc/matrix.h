@@ -153,6 +153,56 @@ __device__ inline u32x4 raw8_to_bf16(const Raw8& r, int type) {
   return u32x4{a[0], a[1], b[0], b[1]};
 }
 
+// ---- buffer access
+//
+// The row kernels' fast paths load and store through buffer descriptors, whose range check
+// stands in for branches: an absent row or piece gets the offset kAbsent, past the
+// descriptor's range, and then reads as zero or is not written.  Without branches the number
+// of memory operations in flight is known at compile time, and a wait for one turn's loads
+// does not also wait for the stores issued since.
+typedef __amdgpu_buffer_rsrc_t Buffer;
+constexpr uint32_t kAbsent = 0x80000000u;
+
+// p is the same in all lanes (and said to be, so that the descriptor is in scalar registers).
+__device__ inline Buffer buffer_at(const void* p) {
+  const uint64_t u = reinterpret_cast<uint64_t>(p);
+  const uint64_t lo = uint32_t(__builtin_amdgcn_readfirstlane(int(u)));
+  const uint64_t hi = uint32_t(__builtin_amdgcn_readfirstlane(int(u >> 32)));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(lo | hi << 32), 0, 0x7fffffff, 0x00020000);
+}
+__device__ inline u32x4 buffer_load16(Buffer b, uint32_t off) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, int(off), 0, 0));
+}
+__device__ inline u32x2 buffer_load8(Buffer b, uint32_t off) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(b, int(off), 0, 0));
+}
+__device__ inline uint32_t buffer_load1(Buffer b, uint32_t off) {
+  return uint32_t(uint8_t(__builtin_amdgcn_raw_buffer_load_b8(b, int(off), 0, 0)));
+}
+__device__ inline void buffer_store16(Buffer b, uint32_t off, u32x4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, b, int(off), 0, 0);
+}
+__device__ inline void buffer_store8(Buffer b, uint32_t off, u32x2 v) {
+  __builtin_amdgcn_raw_buffer_store_b64(v, b, int(off), 0, 0);
+}
+__device__ inline void buffer_store1(Buffer b, uint32_t off, uint32_t v) {
+  __builtin_amdgcn_raw_buffer_store_b8(uint8_t(v), b, int(off), 0, 0);
+}
+
+// Bytes of an element, and of n of them.
+__host__ __device__ constexpr uint32_t element_bytes(int type) {
+  return type == GS_MAT_F32 ? 4 : type == GS_MAT_BF16 ? 2 : 1;
+}
+
+// Whether a matrix can be taken through buffers: rows start at multiples of 4 bytes, and 256
+// rows (at most what a block spans from its base) stay within the descriptor's range.
+inline bool buffer_ok(const MatArg& m) {
+  if (!m.p) return true;
+  const int64_t pitch = m.ld * element_bytes(m.type);
+  return reinterpret_cast<uintptr_t>(m.p) % 4 == 0 && pitch % 4 == 0 && pitch < (int64_t(1) << 22) &&
+         (m.type != GS_MAT_MX8 || m.lds < (int64_t(1) << 22));
+}
+
 // ---- encoding
 
 // The largest finite |v| of N values' bits.  The float maximum passes over NaN; only when an
