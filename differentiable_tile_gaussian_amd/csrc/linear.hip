@@ -298,8 +298,7 @@ hipError_t launch_linear_bwd(const MatArg& dy, const MatArg& z, int act, const M
                                                                         dbias ? b.db : nullptr, rows, n, per, lanes);
     }
     if (dbias) {
-      const MatArg out{reinterpret_cast<char*>(dbias), nullptr, n, 0, GS_MAT_F32};
-      if ((e = launch_sum_parts(b.db, slices, n, n, out, s)) != hipSuccess) return e;
+      if ((e = launch_sum_parts(b.db, slices, n, 0, 1, MatArg{}, dbias, s)) != hipSuccess) return e;
     }
   }
   if (dx.p && rows > 0) {
@@ -321,7 +320,8 @@ hipError_t launch_linear_bwd(const MatArg& dy, const MatArg& z, int act, const M
       gemm_tn_kernel<1, 4, 1><<<dim3(div_up(k, 64), div_up(n, 64), slices), kThreads, 0, s>>>(x, dz, k, n, rows, per,
                                                                                               part, dw);
     }
-    if (part && (e = launch_sum_parts(part, slices, int64_t(n) * k, k, dw, s)) != hipSuccess) return e;
+    if (part && (e = launch_sum_parts(part, slices, int64_t(n) * k, int64_t(n) * k, k, dw, nullptr, s)) != hipSuccess)
+      return e;
   }
   return hipGetLastError();
 }

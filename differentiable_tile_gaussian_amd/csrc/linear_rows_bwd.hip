@@ -25,35 +25,13 @@ struct Piece {
   uint32_t scale;
 };
 
-// type: m.type.  WHOLE: cols is a multiple of 16, so that a piece is there or is not.
-template <bool WHOLE>
-__device__ inline void load_piece(Piece& p, const MatArg& m, int type, int64_t row, int col, int cols) {
-  if (WHOLE && col >= cols) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p.v[i] = u32x4{0, 0, 0, 0};
-    p.scale = 0;
-    return;
-  }
-  if (WHOLE || col + 16 <= cols) {
-    if (type == GS_MAT_MX8) {
-      __builtin_memcpy(&p.v[0], m.p + row * m.ld + col, 16);
-      p.scale = m.s[row * m.lds + (col >> 5)];
-    } else if (type == GS_MAT_BF16) {
-      const char* a = m.p + (row * m.ld + col) * 2;
-      __builtin_memcpy(&p.v[0], __builtin_assume_aligned(a, 2), 16);
-      __builtin_memcpy(&p.v[1], __builtin_assume_aligned(a + 16, 2), 16);
-    } else {
-      const char* a = m.p + (row * m.ld + col) * 4;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) __builtin_memcpy(&p.v[i], __builtin_assume_aligned(a + 16 * i, 4), 16);
-    }
-    return;
-  }
+// Columns col .. col + 15 of a row of any matrix (cols: 0 for an absent row).
+__device__ inline void load_piece_any(Piece& p, const MatArg& m, int64_t row, int col, int cols) {
   const Raw8 lo = load_raw8(m, row, col, cols - col), hi = load_raw8(m, row, col + 8, cols - col - 8);
   p.scale = lo.scale;
-  if (type == GS_MAT_MX8) {
+  if (m.type == GS_MAT_MX8) {
     p.v[0] = u32x4{lo.lo[0], lo.lo[1], hi.lo[0], hi.lo[1]};
-  } else if (type == GS_MAT_BF16) {
+  } else if (m.type == GS_MAT_BF16) {
     p.v[0] = lo.lo;
     p.v[1] = hi.lo;
   } else {
@@ -61,6 +39,22 @@ __device__ inline void load_piece(Piece& p, const MatArg& m, int type, int64_t r
     p.v[1] = lo.hi;
     p.v[2] = hi.lo;
     p.v[3] = hi.hi;
+  }
+}
+
+// The pieces of a lane's row through buffers: rows row0 + row, columns 64 c + 16 g.
+template <int TYPE, int C>
+__device__ inline void load_pieces(Piece (&p)[C], const MatArg& m, int64_t row0, int row, bool in, int g, int cols) {
+  constexpr uint32_t kE = element_bytes(TYPE);
+  const Buffer data = buffer_at(m.p + row0 * m.ld * kE);
+  const Buffer scales = buffer_at(TYPE == GS_MAT_MX8 ? m.s + row0 * m.lds : nullptr);
+  const uint32_t off = (row * uint32_t(m.ld) + g * 16) * kE, soff = row * uint32_t(m.lds) + g / 2;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const bool there = in && c * 64 + g * 16 < cols;
+#pragma unroll
+    for (int i = 0; i < int(kE); ++i) p[c].v[i] = buffer_load16(data, there ? off + c * 64 * kE + i * 16 : kAbsent);
+    p[c].scale = TYPE == GS_MAT_MX8 ? buffer_load1(scales, there ? soff + c * 2 : kAbsent) : 0;
   }
 }
 
@@ -110,7 +104,9 @@ __device__ inline void lds_barrier() {
 
 struct RowsBwdArgs {
   MatArg dy, z, x, w, dx;
-  float *dw, *db;   // [parts][n][k], [blocks][n]; nullptr: not wanted
+  float* part;      // a part's sums of dW [n][k], then of db [n]; the parts part_size apart
+  int64_t part_size;
+  bool want_dw, want_db;
   int64_t rows;
   int act, k, n;
 };
@@ -125,7 +121,7 @@ struct Share {
 // NC, KC: groups of 64 columns of dz and of x.  DY, Z, X: the types of dy, z (GS_MAT_F32: no
 // activation) and x, widths being multiples of 16; or all kAny.
 template <int NC, int KC, int DY, int Z, int X>
-__global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(RowsBwdArgs a) {
+__global__ void __launch_bounds__(kThreads) rows_bwd_kernel(RowsBwdArgs a) {
   using S = Share<NC, KC>;
   constexpr bool kWhole = DY != kAny;
   const int dyt = kWhole ? DY : a.dy.type, zt_ = kWhole ? Z : a.z.type, xt_ = kWhole ? X : a.x.type;
@@ -160,24 +156,26 @@ __global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(RowsBwdArgs a) {
     for (int t = 0; t < 4; ++t) dw[q][t] = f32x4{0, 0, 0, 0};
 
   Piece dy[NC], z[NC], x[KC];
-  auto fetch = [&](int64_t row0) {
-    const int64_t row = row0 + wave * 16 + r;
-    const bool in = row < a.rows;
+  auto fetch = [&](int turn) {
+    const int64_t row0 = int64_t(turn) * kRows;
+    const int row = wave * 16 + r;
+    const bool in = row < a.rows - row0;
+    if constexpr (kWhole) {
+      load_pieces<DY>(dy, a.dy, row0, row, in, g, a.n);
+      if constexpr (Z != GS_MAT_F32) load_pieces<Z>(z, a.z, row0, row, in, g, a.n);
+      load_pieces<X>(x, a.x, row0, row, in, g, a.k);
+    } else {
 #pragma unroll
-    for (int c = 0; c < NC; ++c) load_piece<kWhole>(dy[c], a.dy, dyt, row, c * 64 + g * 16, in ? a.n : 0);
-    if (act != GS_ACT_NONE) {
+      for (int c = 0; c < NC; ++c) {
+        load_piece_any(dy[c], a.dy, row0 + row, c * 64 + g * 16, in ? a.n : 0);
+        if (act != GS_ACT_NONE) load_piece_any(z[c], a.z, row0 + row, c * 64 + g * 16, in ? a.n : 0);
+      }
 #pragma unroll
-      for (int c = 0; c < NC; ++c) load_piece<kWhole>(z[c], a.z, zt_, row, c * 64 + g * 16, in ? a.n : 0);
-    }
-    if (a.dw) {
-#pragma unroll
-      for (int c = 0; c < KC; ++c) load_piece<kWhole>(x[c], a.x, xt_, row, c * 64 + g * 16, in ? a.k : 0);
+      for (int c = 0; c < KC; ++c) load_piece_any(x[c], a.x, row0 + row, c * 64 + g * 16, in ? a.k : 0);
     }
   };
-  const int64_t step = int64_t(gridDim.x) * kRows;
-  fetch(int64_t(blockIdx.x) * kRows);
-  for (int64_t row0 = int64_t(blockIdx.x) * kRows; row0 < a.rows; row0 += step) {
-    u32x4 dz[NC][2];
+  u32x4 dz[NC][2], xb[KC][2];
+  auto convert = [&]() {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       float v[16];
@@ -201,53 +199,48 @@ __global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(RowsBwdArgs a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) dz[c][i / 4][i % 4] = pack_bf16(v[2 * i], v[2 * i + 1]);
     }
+#pragma unroll
+    for (int c = 0; c < KC; ++c) piece_to_bf16(x[c], xt_, xb[c][0], xb[c][1]);
+  };
+  const int turns = int((a.rows + kRows - 1) / kRows);
+  fetch(blockIdx.x);
+  convert();
+  for (int turn = blockIdx.x; turn < turns; turn += gridDim.x) {
     lds_barrier();   // the last turn's readers are done (and, at first, W^T is written)
-    if (a.dw) {
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        uint8_t* p = zt + (wave * 16 + r) * kPitchQ + (c * 64 + g * 16) * 2;
-        *reinterpret_cast<u32x4*>(p) = dz[c][0];
-        *reinterpret_cast<u32x4*>(p + 16) = dz[c][1];
-      }
-#pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        u32x4 lo, hi;
-        piece_to_bf16(x[c], xt_, lo, hi);
-        uint8_t* p = xt + (wave * 16 + r) * kPitchP + (c * 64 + g * 16) * 2;
-        *reinterpret_cast<u32x4*>(p) = lo;
-        *reinterpret_cast<u32x4*>(p + 16) = hi;
-      }
+    for (int c = 0; c < NC; ++c) {
+      uint8_t* p = zt + (wave * 16 + r) * kPitchQ + (c * 64 + g * 16) * 2;
+      *reinterpret_cast<u32x4*>(p) = dz[c][0];
+      *reinterpret_cast<u32x4*>(p + 16) = dz[c][1];
     }
-    if (row0 + step < a.rows) fetch(row0 + step);
-    lds_barrier();
-    if (a.dx.p) {
-      const int64_t row = row0 + wave * 16 + r;
 #pragma unroll
-      for (int kc = 0; kc < KC; ++kc) {
-        f32x4 acc[4];
+    for (int c = 0; c < KC; ++c) {
+      uint8_t* p = xt + (wave * 16 + r) * kPitchP + (c * 64 + g * 16) * 2;
+      *reinterpret_cast<u32x4*>(p) = xb[c][0];
+      *reinterpret_cast<u32x4*>(p + 16) = xb[c][1];
+    }
+    fetch(turn + gridDim.x);   // past the last row: all absent
+    lds_barrier();
+    f32x4 acc[KC][4];
+    if (a.dx.p) {
+      int at = lane * 16;
+      asm volatile("" : "+v"(at));   // W^T stays in LDS: the compiler may not keep it in registers
+#pragma unroll
+      for (int kc = 0; kc < KC; ++kc)
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          acc[t] = f32x4{0, 0, 0, 0};
+          acc[kc][t] = f32x4{0, 0, 0, 0};
 #pragma unroll
           for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const bf16x8 wf =
-                  *reinterpret_cast<const bf16x8*>(wt + (((kc * 4 + t) * NC + c) * 2 + h) * 1024 + lane * 16);
-              acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, __builtin_bit_cast(bf16x8, dz[c][h]), acc[t], 0, 0, 0);
+              const bf16x8 wf = *reinterpret_cast<const bf16x8*>(wt + (((kc * 4 + t) * NC + c) * 2 + h) * 1024 + at);
+              acc[kc][t] =
+                  __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, __builtin_bit_cast(bf16x8, dz[c][h]), acc[kc][t], 0, 0, 0);
             }
         }
-        float v[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = acc[i / 4][i % 4];
-        const int col = kc * 64 + g * 16;
-        if (row < a.rows && col < a.k) {
-          store8(a.dx, row, col, v, kWhole ? 8 : a.k - col);
-          if (kWhole || col + 8 < a.k) store8(a.dx, row, col + 8, v + 8, kWhole ? 8 : a.k - col - 8);
-        }
-      }
     }
-    if (a.dw) {
+    if (a.want_dw) {
 #pragma unroll
       for (int kk = 0; kk < kRows / 32 / S::kMS; ++kk) {
         const int m = (kk * S::kMS + ms) * 32 + g * 8 + r / 4, c = lane % 4 * 4;
@@ -262,10 +255,42 @@ __global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(RowsBwdArgs a) {
         }
       }
     }
+    convert();   // waits for the next turn's loads; this turn's stores come after, and drain meanwhile
+    if (a.dx.p) {
+      const int64_t row0 = int64_t(turn) * kRows;
+      const int row = wave * 16 + r;
+      const bool in = row < a.rows - row0;
+      const uint32_t e = element_bytes(a.dx.type);
+      const Buffer out = buffer_at(a.dx.p + row0 * a.dx.ld * e);
+#pragma unroll
+      for (int kc = 0; kc < KC; ++kc) {
+        const int col = kc * 64 + g * 16;
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = acc[kc][i / 4][i % 4];
+        if constexpr (kWhole) {
+          const uint32_t off = in && col < a.k ? (row * uint32_t(a.dx.ld) + col) * e : kAbsent;
+          if (a.dx.type == GS_MAT_F32) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) buffer_store16(out, off + i * 16, __builtin_bit_cast(u32x4, acc[kc][i]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float* o = v + 8 * i;
+              buffer_store16(out, off + i * 16, u32x4{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]),
+                                                      pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7])});
+            }
+          }
+        } else if (in && col < a.k) {
+          store8(a.dx, row0 + row, col, v, a.k - col);
+          if (col + 8 < a.k) store8(a.dx, row0 + row, col + 8, v + 8, a.k - col - 8);
+        }
+      }
+    }
   }
 
-  if (a.dw) {
-    float* out = a.dw + (int64_t(blockIdx.x) * S::kMS + ms) * a.n * a.k;
+  if (a.want_dw) {
+    float* out = a.part + (int64_t(blockIdx.x) * S::kMS + ms) * a.part_size;
 #pragma unroll
     for (int q = 0; q < S::kQT; ++q) {
       const int n = (wq * S::kQT + q) * 16 + r;
@@ -278,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(RowsBwdArgs a) {
         }
     }
   }
-  if (a.db) {
+  if (a.want_db) {
     // over the wave's 16 rows, then over the waves in order
     float* sums = reinterpret_cast<float*>(zt);   // [8][NC 64]
     __syncthreads();
@@ -295,7 +320,9 @@ __global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(RowsBwdArgs a) {
     for (int j = threadIdx.x; j < a.n; j += kThreads) {
       float t = 0.0f;
       for (int w = 0; w < 8; ++w) t += sums[w * NC * 64 + j];
-      a.db[int64_t(blockIdx.x) * a.n + j] = t;
+      // the block's first part takes the sum, the others nothing
+      float* out = a.part + int64_t(blockIdx.x) * S::kMS * a.part_size + int64_t(a.n) * a.k + j;
+      for (int p = 0; p < S::kMS; ++p) out[p * a.part_size] = p ? 0.0f : t;
     }
   }
 }
@@ -324,11 +351,12 @@ hipError_t by_z(const RowsBwdArgs& a, int blocks, hipStream_t s) {
   return a.z.type == GS_MAT_MX8 ? by_x<NC, KC, DY, GS_MAT_MX8>(a, blocks, s) : by_x<NC, KC, DY, GS_MAT_BF16>(a, blocks, s);
 }
 
-// The types are compiled in for widths of whole 16-column pieces; other widths (and a
-// float32 z) take one kernel that reads its types from the arguments.
+// The types are compiled in for widths of whole 16-column pieces in buffers' reach; other
+// widths and pitches (and a float32 z) take one kernel that reads its types from the arguments.
 template <int NC, int KC>
 hipError_t by_type(const RowsBwdArgs& a, int blocks, hipStream_t s) {
-  if (a.k % 16 || a.n % 16 || (a.act != GS_ACT_NONE && a.z.type == GS_MAT_F32))
+  if (a.k % 16 || a.n % 16 || (a.act != GS_ACT_NONE && a.z.type == GS_MAT_F32) || !buffer_ok(a.dy) ||
+      !buffer_ok(a.x) || !buffer_ok(a.dx) || (a.act != GS_ACT_NONE && !buffer_ok(a.z)))
     return go<NC, KC, kAny, kAny, kAny>(a, blocks, s);
   return a.dy.type == GS_MAT_F32 ? by_z<NC, KC, GS_MAT_F32>(a, blocks, s) : by_z<NC, KC, GS_MAT_BF16>(a, blocks, s);
 }
@@ -343,36 +371,28 @@ int blocks_for(int64_t rows, int k, int n) {
 
 int shares(int k, int n) { return k <= 64 && n <= 64 ? 2 : 1; }
 
-inline size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
-
 }  // namespace
 
 bool rows_bwd_takes(int k, int n) { return k <= 128 && n <= 128; }
 
 size_t rows_bwd_ws_bytes(int64_t rows, int k, int n) {
-  const size_t blocks = size_t(blocks_for(rows, k, n));
-  return align256(blocks * n * 4) + blocks * shares(k, n) * size_t(n) * k * 4;
+  return size_t(blocks_for(rows, k, n)) * shares(k, n) * (size_t(n) * k + n) * 4;
 }
 
 hipError_t launch_rows_bwd(const MatArg& dy, const MatArg& z, int act, const MatArg& x, const MatArg& w,
                            const MatArg& dx, const MatArg& dw, float* dbias, int64_t rows, int k, int n, void* ws,
                            hipStream_t s) {
   const int blocks = blocks_for(rows, k, n);
-  float* db_part = static_cast<float*>(ws);
-  float* dw_part = reinterpret_cast<float*>(static_cast<char*>(ws) + align256(size_t(blocks) * n * 4));
-  const RowsBwdArgs a{dy, z, x, w, dx, dw.p ? dw_part : nullptr, dbias ? db_part : nullptr, rows, act, k, n};
+  const int64_t size = int64_t(n) * k + n;
+  float* part = static_cast<float*>(ws);
+  const RowsBwdArgs a{dy, z, x, w, dx, part, size, dw.p != nullptr, dbias != nullptr, rows, act, k, n};
   hipError_t e;
   if (n <= 64)
     e = k <= 64 ? by_type<1, 1>(a, blocks, s) : by_type<1, 2>(a, blocks, s);
   else
     e = k <= 64 ? by_type<2, 1>(a, blocks, s) : by_type<2, 2>(a, blocks, s);
-  if (e != hipSuccess) return e;
-  if (dw.p && (e = launch_sum_parts(dw_part, blocks * shares(k, n), int64_t(n) * k, k, dw, s)) != hipSuccess) return e;
-  if (dbias) {
-    const MatArg out{reinterpret_cast<char*>(dbias), nullptr, n, 0, GS_MAT_F32};
-    return launch_sum_parts(db_part, blocks, n, n, out, s);
-  }
-  return hipSuccess;
+  if (e != hipSuccess || (!dw.p && !dbias)) return e;
+  return launch_sum_parts(part, blocks * shares(k, n), size, int64_t(n) * k, k, dw, dbias, s);
 }
 
 }  // namespace gsk

@@ -359,9 +359,11 @@ __device__ inline bf16x8 read_transposed(const uint8_t* p, int pitch) {
   return __builtin_bit_cast(bf16x8, v);
 }
 
-// ---- partial sums: out[c] = sum over parts of part[p * count + c], in the order of the
-// parts' index groups (a fixed order); out float32 or bfloat16.
-hipError_t launch_sum_parts(const float* part, int parts, int64_t count, int cols, const MatArg& out, hipStream_t s);
+// ---- partial sums of `size` entries each (part p at part + p size): entries below split go
+// to the matrix out (its rows have cols entries; absent: not wanted), the others to tail
+// (nullable).  The order of the additions depends on the number of parts alone.
+hipError_t launch_sum_parts(const float* part, int parts, int64_t size, int64_t split, int cols, const MatArg& out,
+                            float* tail, hipStream_t s);
 
 // ---- mx8.hip, rmsnorm.hip, linear.hip: the calls' launches (arguments checked by the caller)
 hipError_t launch_mx8_pack(const MatArg& x, const MatArg& q, int64_t rows, int cols, hipStream_t s);

@@ -328,19 +328,27 @@ struct Bwd {
   }
 };
 
-// A block sums 16 columns: 64 groups of parts side by side, then the groups in order.
-__global__ void __launch_bounds__(1024) sum_parts_kernel(const float* __restrict__ part, int parts, int64_t count,
-                                                          int cols, MatArg out) {
+// A block sums 16 entries: 64 groups of parts side by side, then the groups in order.
+__global__ void __launch_bounds__(1024) sum_parts_kernel(const float* __restrict__ part, int parts, int64_t size,
+                                                          int64_t first, int64_t last, int64_t split, int cols,
+                                                          MatArg out, float* tail) {
   const int j = threadIdx.x % 16, g = threadIdx.x / 16;
-  const int64_t c = int64_t(blockIdx.x) * 16 + j;
+  const int64_t c = first + int64_t(blockIdx.x) * 16 + j;
   float t = 0.0f;
-  if (c < count)
-    for (int p = g; p < parts; p += 64) t += part[p * count + c];
+  if (c < last) {
+#pragma unroll 4
+    for (int p = g; p < parts; p += 64) t += part[p * size + c];
+  }
   __shared__ float sums[64][17];
   sums[g][j] = t;
   __syncthreads();
-  if (g == 0 && c < count) {
+  if (g == 0 && c < last) {
+#pragma unroll 8
     for (int k = 1; k < 64; ++k) t += sums[k][j];
+    if (c >= split) {
+      tail[c - split] = t;
+      return;
+    }
     const int64_t at = (c / cols) * out.ld + c % cols;
     if (out.type == GS_MAT_F32)
       reinterpret_cast<float*>(out.p)[at] = t;
@@ -351,9 +359,11 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float* __restrict
 
 }  // namespace
 
-hipError_t launch_sum_parts(const float* part, int parts, int64_t count, int cols, const MatArg& out, hipStream_t s) {
+hipError_t launch_sum_parts(const float* part, int parts, int64_t size, int64_t split, int cols, const MatArg& out,
+                            float* tail, hipStream_t s) {
+  const int64_t first = out.p ? 0 : split, last = tail ? size : split;
   GSK_PROF("sum_parts", s);
-  sum_parts_kernel<<<div_up(count, 16), 1024, 0, s>>>(part, parts, count, cols, out);
+  sum_parts_kernel<<<div_up(last - first, 16), 1024, 0, s>>>(part, parts, size, first, last, split, cols, out, tail);
   return hipGetLastError();
 }
 
@@ -396,8 +406,7 @@ hipError_t launch_rmsnorm_bwd(const MatArg& dy, const MatArg& h, const float* w,
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !dweight) return e;
-  const MatArg out{reinterpret_cast<char*>(dweight), nullptr, cols, 0, GS_MAT_F32};
-  return launch_sum_parts(part, blocks, cols, cols, out, s);
+  return launch_sum_parts(part, blocks, cols, 0, 1, MatArg{}, dweight, s);
 }
 
 }  // namespace gsk
