@@ -258,7 +258,8 @@ BwdWs carve_bwd(void* ws, int64_t rows, int k, int n) {
   w.db = reinterpret_cast<float*>(p + at);
   at += align256(size_t(dz_slices(rows)) * n * 4);
   w.dw = reinterpret_cast<float*>(p + at);
-  at += align256(size_t(dw_slices(rows, k, n)) * n * k * 4);
+  const int a = dw_slices(rows, k, n), c = tile_tn_slices(rows, k, n);
+  at += align256(size_t(a > c ? a : c) * n * k * 4);
   w.bytes = at;
   return w;
 }
@@ -269,6 +270,10 @@ hipError_t launch_linear_fwd(const MatArg& x, const MatArg& w, const float* bias
                              const MatArg& z, const MatArg& y, int64_t rows, int k, int n, hipStream_t s) {
   const Epilogue e{bias, act, r, z, y};
   if (rows_fwd_takes(k, n)) return launch_rows_fwd(x, w, e, rows, k, n, s);
+  if (tile_nt_takes(w, x, k)) {
+    GSK_PROF("linear_tile_fwd", s);
+    return launch_tile_nt(w, x, n, rows, k, e, s);
+  }
   GSK_PROF("linear_fwd", s);
   gemm_nt_kernel<1, 4, 1><<<dim3(div_up(rows, 64), div_up(n, 64)), kThreads, 0, s>>>(w, x, n, rows, k, e);
   return hipGetLastError();
@@ -283,7 +288,8 @@ hipError_t launch_linear_bwd(const MatArg& dy, const MatArg& z, int act, const M
                              hipStream_t s) {
   if (rows_bwd_takes(k, n)) return launch_rows_bwd(dy, z, act, x, w, dx, dw, dbias, rows, k, n, ws, s);
   const BwdWs b = carve_bwd(ws, rows, k, n);
-  const bool own_dz = act != GS_ACT_NONE && (dx.p || dw.p);
+  // dz in memory: as the activation makes it, or a float32 dy rounded once for both products
+  const bool own_dz = (act != GS_ACT_NONE || dy.type == GS_MAT_F32) && (dx.p || dw.p);
   const MatArg dz = own_dz ? MatArg{b.dz, nullptr, b.dz_ld, 0, GS_MAT_BF16} : dy;
   const MatArg none{nullptr, nullptr, 0, 0, GS_MAT_F32};
   hipError_t e;
@@ -309,9 +315,20 @@ hipError_t launch_linear_bwd(const MatArg& dy, const MatArg& z, int act, const M
     }
     const Epilogue out{nullptr, GS_ACT_NONE, none, none, dx};
     GSK_PROF("linear_dx", s);
+    if (tile_nt_takes(wt, dz, n)) {
+      if ((e = launch_tile_nt(wt, dz, k, rows, n, out, s)) != hipSuccess) return e;
+    } else
     gemm_nt_kernel<1, 4, 1><<<dim3(div_up(rows, 64), div_up(k, 64)), kThreads, 0, s>>>(wt, dz, k, rows, n, out);
   }
-  if (dw.p) {
+  if (dw.p && tile_tn_takes(x, dz, k, n)) {
+    const int slices = tile_tn_slices(rows, k, n);
+    {
+      GSK_PROF("linear_dw", s);
+      if ((e = launch_tile_tn(x, dz, k, n, rows, slices, b.dw, dw, s)) != hipSuccess) return e;
+    }
+    const int64_t size = int64_t(n) * k;
+    if (slices > 1 && (e = launch_sum_parts(b.dw, slices, size, size, k, dw, nullptr, s)) != hipSuccess) return e;
+  } else if (dw.p) {
     const int slices = dw_slices(rows, k, n);
     const int64_t per = ((rows + slices - 1) / slices + 63) / 64 * 64;
     float* part = slices > 1 ? b.dw : nullptr;

@@ -1,0 +1,328 @@
+// Products of wide layers, bounded by the matrix cores: 128 x 256 tiles of the result (64 x
+// 16 QT for each of four waves), with the contraction in steps of 64 staged through registers
+// into two LDS buffers.  A step's operands are loaded from memory while the step before the
+// last is computed and written to LDS while the last one is, so that one barrier a step
+// suffices and nothing waits for memory.
+//
+// Why 128 x 256 by four waves: a wave's 64 x 128 part reads 12 operand fragments from LDS
+// for 32 matrix instructions, 96 bytes a clock for the compute unit's four SIMDs, below
+// LDS's 128; square 64 x 64 parts read 16 for 32 and sit at that limit.
+#include "linear.h"
+#include "profile.h"
+
+namespace gsk {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Ends a step: LDS writes done, all waves there; loads from memory stay in flight.
+__device__ inline void step_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Which tile a block takes: consecutive blocks go to different XCDs, each with its own L2, so
+// an XCD is given neighbouring tiles (the P tiles of one Q tile after another).
+__device__ inline int tile_of(int block, int tiles) {
+  const int per = (tiles + 7) / 8;
+  return block % 8 * per + block / 8;
+}
+
+// 16 values of a row as loaded: bfloat16 (two 16-byte words) or MX8 (one, and the scale).
+template <int TYPE>
+struct Unit {
+  u32x4 a, b;
+  uint32_t scale;
+  __device__ void load(Buffer data, Buffer scales, uint32_t off, uint32_t soff) {
+    a = buffer_load16(data, off);
+    if constexpr (TYPE == GS_MAT_MX8)
+      scale = buffer_load1(scales, soff);
+    else
+      b = buffer_load16(data, off + 16);
+  }
+  __device__ void operands(u32x4& p, u32x4& q) const {
+    if constexpr (TYPE == GS_MAT_MX8) {
+      const float s = mx8_scale(scale);
+      const u32x2 w0 = mx8_to_bf16x4(a[0], s), w1 = mx8_to_bf16x4(a[1], s);
+      const u32x2 w2 = mx8_to_bf16x4(a[2], s), w3 = mx8_to_bf16x4(a[3], s);
+      p = u32x4{w0[0], w0[1], w1[0], w1[1]};
+      q = u32x4{w2[0], w2[1], w3[0], w3[1]};
+    } else {
+      p = a;
+      q = b;
+    }
+  }
+};
+
+// ------------------------------------------------- contraction contiguous in both operands
+
+// out(q, p) = sum_k Q(q, k) P(p, k) for the rows q of Q (bfloat16 or MX8) and p of P
+// (bfloat16); nk a multiple of 16.  An LDS row is 64 k, 128 bytes, whose 16-byte pieces are
+// permuted by the row's number so that a fragment read's 16 rows fall into different banks;
+// P's rows are stored so that a lane's four result tiles are 16 consecutive columns.
+template <int QTYPE, int QT>
+__global__ void __launch_bounds__(kThreads) tile_nt_kernel(MatArg P, MatArg Q, int np, int64_t nq, int nk, Epilogue e,
+                                                            int ptiles, int tiles) {
+  constexpr int BP = 128, BQ = 32 * QT, kStep = (BP + BQ) * 128;
+  extern __shared__ __align__(16) uint8_t lds[];
+  const int tile = tile_of(blockIdx.x, tiles);
+  if (tile >= tiles) return;
+  const int p0 = tile % ptiles * BP;
+  const int64_t q0 = int64_t(tile / ptiles) * BQ;
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, wp = wave % 2, wq = wave / 2;
+  // a thread stages piece `piece` (16 k) of the rows row + 64 u
+  const int row = threadIdx.x / 4, piece = threadIdx.x % 4;
+  constexpr uint32_t kQ = element_bytes(QTYPE);
+  const Buffer pb = buffer_at(P.p + int64_t(p0) * P.ld * 2), qb = buffer_at(Q.p + q0 * Q.ld * kQ);
+  const Buffer sb = buffer_at(QTYPE == GS_MAT_MX8 ? Q.s + q0 * Q.lds : nullptr);
+  uint32_t poff[BP / 64], qoff[BQ / 64], soff[BQ / 64];
+#pragma unroll
+  for (int u = 0; u < BP / 64; ++u)
+    poff[u] = p0 + u * 64 + row < np ? (u * 64 + row) * uint32_t(P.ld) * 2 + piece * 32 : kAbsent;
+#pragma unroll
+  for (int u = 0; u < BQ / 64; ++u) {
+    const bool in = q0 + u * 64 + row < nq;
+    qoff[u] = in ? (u * 64 + row) * uint32_t(Q.ld) * kQ + piece * 16 * kQ : kAbsent;
+    soff[u] = in ? (u * 64 + row) * uint32_t(Q.lds) + piece / 2 : kAbsent;
+  }
+  Unit<GS_MAT_BF16> pr[BP / 64];
+  Unit<QTYPE> qr[BQ / 64];
+  auto fetch = [&](int k0) {
+    const bool in = k0 + piece * 16 < nk;
+#pragma unroll
+    for (int u = 0; u < BP / 64; ++u) pr[u].load(pb, pb, in ? poff[u] + k0 * 2 : kAbsent, 0);
+#pragma unroll
+    for (int u = 0; u < BQ / 64; ++u)
+      qr[u].load(qb, sb, in ? qoff[u] + k0 * kQ : kAbsent, in ? soff[u] + k0 / 32 : kAbsent);
+  };
+  auto put = [&](uint8_t* at, int r, u32x4 a, u32x4 b) {
+    const int s = (r >> 1) & 7;
+    *reinterpret_cast<u32x4*>(at + r * 128 + ((piece * 2) ^ s) * 16) = a;
+    *reinterpret_cast<u32x4*>(at + r * 128 + ((piece * 2 + 1) ^ s) * 16) = b;
+  };
+  auto stage = [&](uint8_t* at) {
+    u32x4 a, b;
+#pragma unroll
+    for (int u = 0; u < BP / 64; ++u) {
+      const int r = u * 64 + row;
+      pr[u].operands(a, b);
+      put(at, (r & ~63) | ((r & 12) << 2) | ((r & 48) >> 2) | (r & 3), a, b);
+    }
+#pragma unroll
+    for (int u = 0; u < BQ / 64; ++u) {
+      qr[u].operands(a, b);
+      put(at + BP * 128, u * 64 + row, a, b);
+    }
+  };
+  f32x4 acc[QT][4];
+#pragma unroll
+  for (int i = 0; i < QT; ++i)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
+  // a fragment's place within its rows: the row's number enters through bits 1-3 only
+  const int r16 = lane % 16, g = lane / 16, sw = (r16 >> 1) & 7;
+  const int frag0 = r16 * 128 + (g ^ sw) * 16, frag1 = r16 * 128 + ((g + 4) ^ sw) * 16;
+  fetch(0);
+  stage(lds);
+  fetch(64);
+  const int steps = (nk + 63) / 64;
+  for (int s = 0; s < steps; ++s) {
+    step_barrier();
+    const uint8_t* now = lds + (s & 1) * kStep;
+    stage(lds + (~s & 1) * kStep);   // past the end: zeros, not read
+    fetch((s + 2) * 64);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      const uint8_t* at = now + (kk ? frag1 : frag0);
+      bf16x8 pf[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) pf[t] = *reinterpret_cast<const bf16x8*>(at + (wp * 64 + t * 16) * 128);
+#pragma unroll
+      for (int i = 0; i < QT; ++i) {
+        const bf16x8 qf = *reinterpret_cast<const bf16x8*>(at + (BP + (wq * QT + i) * 16) * 128);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[t], qf, acc[i][t], 0, 0, 0);
+      }
+    }
+  }
+  const int col = p0 + wp * 64 + g * 16, n = np - col < 16 ? np - col : 16;
+  float bias[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) bias[i] = e.bias && i < n ? e.bias[col + i] : 0.0f;
+#pragma unroll
+  for (int i = 0; i < QT; ++i) {
+    const int64_t r = q0 + (wq * QT + i) * 16 + r16;
+    float v[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = acc[i][j / 4][j % 4] + bias[j];
+    finish16<false, kAny, kAny>(e, r, col, v, r < nq ? n : 0);
+  }
+}
+
+// ------------------------------------------------- contraction over the operands' rows
+
+// out(q, p) = sum_m Q(m, q) P(m, p) for m in the block's slice: the weight's gradient (Q =
+// dz, bfloat16; P = x, bfloat16 or MX8); np and nq multiples of 16.  LDS holds 64 rows m
+// as they are in memory (plus 32 bytes a row, so that eight rows fall into different banks),
+// read transposed.
+template <int PTYPE, int QT>
+__global__ void __launch_bounds__(kThreads) tile_tn_kernel(MatArg P, MatArg Q, int np, int nq, int64_t rows,
+                                                            int64_t per_slice, float* part, MatArg out, int ptiles,
+                                                            int tiles) {
+  constexpr int BP = 128, BQ = 32 * QT, kPitchP = BP * 2 + 32, kPitchQ = BQ * 2 + 32;
+  constexpr int kStep = 64 * (kPitchP + kPitchQ), kUP = BP / 64, kUQ = BQ / 64;
+  extern __shared__ __align__(16) uint8_t lds[];
+  const int tile = tile_of(blockIdx.x, tiles);
+  if (tile >= tiles) return;
+  const int p0 = tile % ptiles * BP, q0 = tile / ptiles * BQ;
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, wp = wave % 2, wq = wave / 2;
+  const int64_t first = int64_t(blockIdx.y) * per_slice;
+  const int64_t last = first + per_slice < rows ? first + per_slice : rows;
+  // a thread stages 16 columns of kUP + kUQ row pieces: P's rows hold BP / 16 of them, Q's BQ / 16
+  constexpr uint32_t kP = element_bytes(PTYPE);
+  const int pm = threadIdx.x / (BP / 16), pc = threadIdx.x % (BP / 16) * 16;
+  const int qm = threadIdx.x / (BQ / 16), qc = threadIdx.x % (BQ / 16) * 16;
+  Unit<PTYPE> pr[kUP];
+  Unit<GS_MAT_BF16> qr[kUQ];
+  auto fetch = [&](int64_t m0) {
+    const Buffer pb = buffer_at(P.p + (m0 * P.ld + p0) * kP), qb = buffer_at(Q.p + (m0 * Q.ld + q0) * 2);
+    const Buffer sb = buffer_at(PTYPE == GS_MAT_MX8 ? P.s + m0 * P.lds + p0 / 32 : nullptr);
+    const int left = last - m0 < 64 ? int(last - m0) : 64;
+#pragma unroll
+    for (int u = 0; u < kUP; ++u) {
+      const int m = pm + u * (kThreads * 16 / BP);
+      const bool in = m < left && p0 + pc < np;
+      pr[u].load(pb, sb, in ? (m * uint32_t(P.ld) + pc) * kP : kAbsent, in ? m * uint32_t(P.lds) + pc / 32 : kAbsent);
+    }
+#pragma unroll
+    for (int u = 0; u < kUQ; ++u) {
+      const int m = qm + u * (kThreads * 16 / BQ);
+      qr[u].load(qb, qb, m < left && q0 + qc < nq ? (m * uint32_t(Q.ld) + qc) * 2 : kAbsent, 0);
+    }
+  };
+  auto stage = [&](uint8_t* at) {
+    u32x4 a, b;
+#pragma unroll
+    for (int u = 0; u < kUP; ++u) {
+      uint8_t* o = at + (pm + u * (kThreads * 16 / BP)) * kPitchP + pc * 2;
+      pr[u].operands(a, b);
+      *reinterpret_cast<u32x4*>(o) = a;
+      *reinterpret_cast<u32x4*>(o + 16) = b;
+    }
+#pragma unroll
+    for (int u = 0; u < kUQ; ++u) {
+      uint8_t* o = at + 64 * kPitchP + (qm + u * (kThreads * 16 / BQ)) * kPitchQ + qc * 2;
+      qr[u].operands(a, b);
+      *reinterpret_cast<u32x4*>(o) = a;
+      *reinterpret_cast<u32x4*>(o + 16) = b;
+    }
+  };
+  f32x4 acc[QT][4];
+#pragma unroll
+  for (int i = 0; i < QT; ++i)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
+  const int m = lane / 16 * 8 + lane % 16 / 4, c = lane % 4 * 4;
+  const int pat = m * kPitchP + (wp * 64 + c) * 2, qat = 64 * kPitchP + m * kPitchQ + (wq * QT * 16 + c) * 2;
+  fetch(first);
+  stage(lds);
+  fetch(first + 64);
+  const int steps = last > first ? int((last - first + 63) / 64) : 0;
+  for (int s = 0; s < steps; ++s) {
+    step_barrier();
+    const uint8_t* now = lds + (s & 1) * kStep;
+    stage(lds + (~s & 1) * kStep);
+    fetch(first + int64_t(s + 2) * 64);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      bf16x8 pf[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) pf[t] = read_transposed(now + pat + kk * 32 * kPitchP + t * 32, kPitchP);
+#pragma unroll
+      for (int i = 0; i < QT; ++i) {
+        const bf16x8 qf = read_transposed(now + qat + kk * 32 * kPitchQ + i * 32, kPitchQ);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[t], qf, acc[i][t], 0, 0, 0);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < QT; ++i) {
+    const int q = q0 + (wq * QT + i) * 16 + lane % 16;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int p = p0 + wp * 64 + t * 16 + lane / 16 * 4;
+      if (q >= nq || p >= np) continue;
+      const f32x4 v = acc[i][t];
+      if (part) {
+        __builtin_memcpy(part + (int64_t(blockIdx.y) * nq + q) * np + p, &v, 16);
+      } else if (out.type == GS_MAT_F32) {
+        __builtin_memcpy(__builtin_assume_aligned(reinterpret_cast<float*>(out.p) + int64_t(q) * out.ld + p, 4), &v, 16);
+      } else {
+        const u32x2 w{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+        __builtin_memcpy(__builtin_assume_aligned(out.p + (int64_t(q) * out.ld + p) * 2, 2), &w, 8);
+      }
+    }
+  }
+}
+
+template <int QTYPE, int QT>
+hipError_t go_nt(const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, const Epilogue& e, hipStream_t s) {
+  constexpr int kLds = 2 * (128 + 32 * QT) * 128;
+  const auto kernel = &tile_nt_kernel<QTYPE, QT>;
+  static const hipError_t allowed =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  if (allowed != hipSuccess) return allowed;
+  const int ptiles = int(div_up(np, 128)), tiles = int(ptiles * int64_t(div_up(nq, 32 * QT)));
+  kernel<<<(tiles + 7) / 8 * 8, kThreads, kLds, s>>>(P, Q, np, nq, nk, e, ptiles, tiles);
+  return hipGetLastError();
+}
+
+template <int PTYPE, int QT>
+hipError_t go_tn(const MatArg& P, const MatArg& Q, int np, int nq, int64_t rows, int slices, float* part,
+                 const MatArg& out, hipStream_t s) {
+  constexpr int kLds = 2 * 64 * (128 * 2 + 32 + 32 * QT * 2 + 32);
+  const auto kernel = &tile_tn_kernel<PTYPE, QT>;
+  static const hipError_t allowed =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  if (allowed != hipSuccess) return allowed;
+  const int ptiles = int(div_up(np, 128)), tiles = ptiles * int(div_up(nq, 32 * QT));
+  const int64_t per = ((rows + slices - 1) / slices + 63) / 64 * 64;
+  kernel<<<dim3((tiles + 7) / 8 * 8, slices), kThreads, kLds, s>>>(P, Q, np, nq, rows, per, slices > 1 ? part : nullptr,
+                                                                  out, ptiles, tiles);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+bool tile_nt_takes(const MatArg& P, const MatArg& Q, int nk) {
+  return P.type == GS_MAT_BF16 && Q.type != GS_MAT_F32 && nk % 16 == 0 && buffer_ok(P) && buffer_ok(Q);
+}
+
+hipError_t launch_tile_nt(const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, const Epilogue& e,
+                          hipStream_t s) {
+  // tiles of 256 rows where they fill the card, else of 128
+  const bool big = int64_t(div_up(np, 128)) * div_up(nq, 256) >= 192;
+  if (Q.type == GS_MAT_MX8)
+    return big ? go_nt<GS_MAT_MX8, 8>(P, Q, np, nq, nk, e, s) : go_nt<GS_MAT_MX8, 4>(P, Q, np, nq, nk, e, s);
+  return big ? go_nt<GS_MAT_BF16, 8>(P, Q, np, nq, nk, e, s) : go_nt<GS_MAT_BF16, 4>(P, Q, np, nq, nk, e, s);
+}
+
+bool tile_tn_takes(const MatArg& P, const MatArg& Q, int np, int nq) {
+  return Q.type == GS_MAT_BF16 && P.type != GS_MAT_F32 && np % 16 == 0 && nq % 16 == 0 && buffer_ok(P) && buffer_ok(Q);
+}
+
+int tile_tn_slices(int64_t rows, int np, int nq) {
+  const int64_t tiles = int64_t(div_up(np, 128)) * div_up(nq, 128);
+  const int64_t want = tiles >= 256 ? 1 : (512 + tiles - 1) / tiles, most = rows < 512 ? 1 : rows / 256;
+  return int(want < most ? want : most);
+}
+
+hipError_t launch_tile_tn(const MatArg& P, const MatArg& Q, int np, int nq, int64_t rows, int slices, float* part,
+                          const MatArg& out, hipStream_t s) {
+  return P.type == GS_MAT_MX8 ? go_tn<GS_MAT_MX8, 4>(P, Q, np, nq, rows, slices, part, out, s)
+                              : go_tn<GS_MAT_BF16, 4>(P, Q, np, nq, rows, slices, part, out, s);
+}
+
+}  // namespace gsk
