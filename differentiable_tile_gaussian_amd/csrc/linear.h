@@ -117,4 +117,9 @@ int tile_tn_slices(int64_t rows, int np, int nq);
 hipError_t launch_tile_tn(const MatArg& P, const MatArg& Q, int np, int nq, int64_t rows, int slices, float* part,
                           const MatArg& out, hipStream_t s);
 
+// ---- linear_split.hip: the same product where it has too few tiles to fill the card
+bool split_nt_takes(const MatArg& P, const MatArg& Q, int np, int64_t nq);
+hipError_t launch_split_nt(const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, const Epilogue& e,
+                           hipStream_t s);
+
 }  // namespace gsk

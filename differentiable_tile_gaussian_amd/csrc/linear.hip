@@ -226,6 +226,17 @@ __global__ void __launch_bounds__(kThreads) transpose_kernel(MatArg w, MatArg wt
   }
 }
 
+// out(q, p) = sum_k Q(q, k) P(p, k) by the kernel that fits: few tiles share the contraction
+// among waves, many go by tiles; the plain kernel takes widths and alignments that neither does.
+hipError_t launch_nt(const char* name, const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, const Epilogue& e,
+                     hipStream_t s) {
+  GSK_PROF(name, s);
+  if (split_nt_takes(P, Q, np, nq)) return launch_split_nt(P, Q, np, nq, nk, e, s);
+  if (tile_nt_takes(P, Q, nk)) return launch_tile_nt(P, Q, np, nq, nk, e, s);
+  gemm_nt_kernel<1, 4, 1><<<dim3(div_up(nq, 64), div_up(np, 64)), kThreads, 0, s>>>(P, Q, np, nq, nk, e);
+  return hipGetLastError();
+}
+
 inline size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
 inline int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
 
@@ -270,13 +281,7 @@ hipError_t launch_linear_fwd(const MatArg& x, const MatArg& w, const float* bias
                              const MatArg& z, const MatArg& y, int64_t rows, int k, int n, hipStream_t s) {
   const Epilogue e{bias, act, r, z, y};
   if (rows_fwd_takes(k, n)) return launch_rows_fwd(x, w, e, rows, k, n, s);
-  if (tile_nt_takes(w, x, k)) {
-    GSK_PROF("linear_tile_fwd", s);
-    return launch_tile_nt(w, x, n, rows, k, e, s);
-  }
-  GSK_PROF("linear_fwd", s);
-  gemm_nt_kernel<1, 4, 1><<<dim3(div_up(rows, 64), div_up(n, 64)), kThreads, 0, s>>>(w, x, n, rows, k, e);
-  return hipGetLastError();
+  return launch_nt("linear_fwd", w, x, n, rows, k, e, s);
 }
 
 size_t linear_bwd_ws_bytes(int64_t rows, int k, int n) {
@@ -314,11 +319,7 @@ hipError_t launch_linear_bwd(const MatArg& dy, const MatArg& z, int act, const M
       transpose_kernel<<<dim3(div_up(k, 64), div_up(n, 64)), kThreads, 0, s>>>(w, wt, n, k);
     }
     const Epilogue out{nullptr, GS_ACT_NONE, none, none, dx};
-    GSK_PROF("linear_dx", s);
-    if (tile_nt_takes(wt, dz, n)) {
-      if ((e = launch_tile_nt(wt, dz, k, rows, n, out, s)) != hipSuccess) return e;
-    } else
-    gemm_nt_kernel<1, 4, 1><<<dim3(div_up(rows, 64), div_up(k, 64)), kThreads, 0, s>>>(wt, dz, k, rows, n, out);
+    if ((e = launch_nt("linear_dx", wt, dz, k, rows, n, out, s)) != hipSuccess) return e;
   }
   if (dw.p && tile_tn_takes(x, dz, k, n)) {
     const int slices = tile_tn_slices(rows, k, n);

@@ -1,0 +1,155 @@
+// Products with few rows (a view's code, a small batch): the result has too few tiles to fill
+// the card, and what there is to do is reading the weight.  A block takes 64 columns by 16 QT
+// rows and its waves share the contraction, each loading its operands from memory
+// straight into registers one step ahead; the waves' sums are joined through LDS in order.
+#include "linear.h"
+#include "profile.h"
+
+namespace gsk {
+namespace {
+
+// 16 k of a row (a lane's share of a step of 64, two products), in bfloat16.
+struct Operands {
+  bf16x8 a, b;
+};
+
+// As loaded: bfloat16 (two words) or MX8 (one, and the scale).  WHOLE: nk is a multiple of 16
+// and the matrix in buffers' reach.
+template <int TYPE, bool WHOLE>
+struct Share {
+  u32x4 a, b;
+  uint32_t scale;
+  __device__ void load(const MatArg& m, Buffer data, Buffer scales, int64_t row0, int row, bool in, int k, int nk) {
+    if constexpr (WHOLE) {
+      const bool there = in && k < nk;
+      const uint32_t off = there ? (row * uint32_t(m.ld) + k) * element_bytes(TYPE) : kAbsent;
+      a = buffer_load16(data, off);
+      if constexpr (TYPE == GS_MAT_MX8)
+        scale = buffer_load1(scales, there ? row * uint32_t(m.lds) + k / 32 : kAbsent);
+      else
+        b = buffer_load16(data, off + 16);
+    } else {
+      const int n = in ? nk - k : 0;
+      const Raw8 lo = load_raw8(m, row0 + row, k, n), hi = load_raw8(m, row0 + row, k + 8, n - 8);
+      scale = lo.scale;
+      if constexpr (TYPE == GS_MAT_MX8) {
+        a = u32x4{lo.lo[0], lo.lo[1], hi.lo[0], hi.lo[1]};
+      } else {
+        a = lo.lo;
+        b = hi.lo;
+      }
+    }
+  }
+  __device__ Operands operands() const {
+    if constexpr (TYPE == GS_MAT_MX8) {
+      const float s = mx8_scale(scale);
+      const u32x2 w0 = mx8_to_bf16x4(a[0], s), w1 = mx8_to_bf16x4(a[1], s);
+      const u32x2 w2 = mx8_to_bf16x4(a[2], s), w3 = mx8_to_bf16x4(a[3], s);
+      return {__builtin_bit_cast(bf16x8, u32x4{w0[0], w0[1], w1[0], w1[1]}),
+              __builtin_bit_cast(bf16x8, u32x4{w2[0], w2[1], w3[0], w3[1]})};
+    } else {
+      return {__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b)};
+    }
+  }
+};
+
+// Waves of a block: enough loads in flight with few rows, 64 KiB of sums at most with many.
+__host__ __device__ constexpr int waves_for(int qt) { return qt == 4 ? 4 : 8; }
+
+// out(q, p) = sum_k Q(q, k) P(p, k), P bfloat16, Q bfloat16 or MX8.
+template <int QTYPE, int QT, bool WHOLE>
+__global__ void __launch_bounds__(waves_for(QT) * 64) split_nt_kernel(MatArg P, MatArg Q, int np, int64_t nq, int nk, Epilogue e) {
+  constexpr int kWaves = waves_for(QT);
+  extern __shared__ __align__(16) uint8_t lds[];
+  f32x4* sums = reinterpret_cast<f32x4*>(lds);   // [wave][QT][4][lane]
+  const int lane = threadIdx.x % 64, g = lane / 16, r = lane % 16;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int p0 = blockIdx.y * 64;
+  const int64_t q0 = int64_t(blockIdx.x) * (16 * QT);
+  const Buffer pb = buffer_at(P.p + int64_t(p0) * P.ld * 2), qb = buffer_at(Q.p + q0 * Q.ld * element_bytes(QTYPE));
+  const Buffer sb = buffer_at(QTYPE == GS_MAT_MX8 ? Q.s + q0 * Q.lds : nullptr);
+  Share<GS_MAT_BF16, WHOLE> ps[4];
+  Share<QTYPE, WHOLE> qs[QT];
+  auto fetch = [&](int step) {
+    const int k = step * 64 + g * 16;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int row = r / 4 * 16 + t * 4 + r % 4;
+      ps[t].load(P, pb, pb, p0, row, p0 + row < np, k, nk);
+    }
+#pragma unroll
+    for (int i = 0; i < QT; ++i) qs[i].load(Q, qb, sb, q0, i * 16 + r, q0 + i * 16 + r < nq, k, nk);
+  };
+  f32x4 acc[QT][4];
+#pragma unroll
+  for (int i = 0; i < QT; ++i)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
+  const int steps = (nk + 63) / 64;
+  fetch(wave);
+  for (int s = wave; s < steps; s += kWaves) {
+    Operands po[4], qo[QT];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) po[t] = ps[t].operands();
+#pragma unroll
+    for (int i = 0; i < QT; ++i) qo[i] = qs[i].operands();
+    fetch(s + kWaves);   // past the end: all absent
+#pragma unroll
+    for (int i = 0; i < QT; ++i)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(po[t].a, qo[i].a, acc[i][t], 0, 0, 0);
+        acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(po[t].b, qo[i].b, acc[i][t], 0, 0, 0);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < QT; ++i)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) sums[((wave * QT + i) * 4 + t) * 64 + lane] = acc[i][t];
+  __syncthreads();
+  if (wave >= QT) return;
+  f32x4 total[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) total[t] = sums[(wave * 4 + t) * 64 + lane];
+#pragma unroll 2
+  for (int w = 1; w < kWaves; ++w)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) total[t] += sums[((w * QT + wave) * 4 + t) * 64 + lane];
+  const int col = p0 + g * 16, n = np - col < 16 ? np - col : 16;
+  const int64_t row = q0 + wave * 16 + r;
+  float v[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] = total[j / 4][j % 4] + (e.bias && j < n ? e.bias[col + j] : 0.0f);
+  finish16<false, kAny, kAny>(e, row, col, v, row < nq ? n : 0);
+}
+
+template <int QTYPE, int QT, bool WHOLE>
+hipError_t go(const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, const Epilogue& e, hipStream_t s) {
+  constexpr int kWaves = waves_for(QT), kLds = kWaves * QT * 4096;
+  split_nt_kernel<QTYPE, QT, WHOLE>
+      <<<dim3(div_up(nq, 16 * QT), div_up(np, 64)), kWaves * 64, kLds, s>>>(P, Q, np, nq, nk, e);
+  return hipGetLastError();
+}
+
+template <int QTYPE, bool WHOLE>
+hipError_t by_rows(const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, const Epilogue& e, hipStream_t s) {
+  return nq <= 16   ? go<QTYPE, 1, WHOLE>(P, Q, np, nq, nk, e, s)
+         : nq <= 32 ? go<QTYPE, 2, WHOLE>(P, Q, np, nq, nk, e, s)
+                    : go<QTYPE, 4, WHOLE>(P, Q, np, nq, nk, e, s);
+}
+
+}  // namespace
+
+bool split_nt_takes(const MatArg& P, const MatArg& Q, int np, int64_t nq) {
+  return P.type == GS_MAT_BF16 && Q.type != GS_MAT_F32 && int64_t(div_up(np, 128)) * div_up(nq, 128) <= 64;
+}
+
+hipError_t launch_split_nt(const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, const Epilogue& e,
+                           hipStream_t s) {
+  const bool whole = nk % 16 == 0 && buffer_ok(P) && buffer_ok(Q);
+  if (Q.type == GS_MAT_MX8)
+    return whole ? by_rows<GS_MAT_MX8, true>(P, Q, np, nq, nk, e, s) : by_rows<GS_MAT_MX8, false>(P, Q, np, nq, nk, e, s);
+  return whole ? by_rows<GS_MAT_BF16, true>(P, Q, np, nq, nk, e, s) : by_rows<GS_MAT_BF16, false>(P, Q, np, nq, nk, e, s);
+}
+
+}  // namespace gsk

@@ -1,12 +1,8 @@
-// Products of wide layers, bounded by the matrix cores: 128 x 256 tiles of the result (64 x
-// 16 QT for each of four waves), with the contraction in steps of 64 staged through registers
-// into two LDS buffers.  A step's operands are loaded from memory while the step before the
-// last is computed and written to LDS while the last one is, so that one barrier a step
-// suffices and nothing waits for memory.
-//
-// Why 128 x 256 by four waves: a wave's 64 x 128 part reads 12 operand fragments from LDS
-// for 32 matrix instructions, 96 bytes a clock for the compute unit's four SIMDs, below
-// LDS's 128; square 64 x 64 parts read 16 for 32 and sit at that limit.
+// Products of wide layers, bounded by the matrix cores: tiles of 128 columns by 32 QT rows of
+// the result (64 x 16 QT for each of four waves), with the contraction in steps of 64 staged
+// through registers into two LDS buffers.  The operands of the next D steps are in flight from
+// memory and the next step's are written to LDS while the present one is computed, so that
+// one barrier a step suffices and nothing waits for memory.
 #include "linear.h"
 #include "profile.h"
 
@@ -15,11 +11,34 @@ namespace {
 
 constexpr int kThreads = 256;
 
+
 // Ends a step: LDS writes done, all waves there; loads from memory stay in flight.
 __device__ inline void step_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// The order in which a step's instructions are issued: a few operand reads, then four matrix
+// instructions at a time with what the next ones need in between: an operand read or two, an
+// LDS write of the step to come, a load from memory.  (Left to itself the compiler puts the
+// writes first, and every wave waits for them in front of its first operand.)
+template <int READS, int WRITES, int LOADS, int GROUPS, int I = 0>
+__device__ inline void interleave() {
+  constexpr int kFirst = READS / 4, kRest = READS - kFirst, kOver = GROUPS - 2;
+  if constexpr (I == 0) __builtin_amdgcn_sched_group_barrier(0x100, kFirst, 0);
+  if constexpr (I < GROUPS) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+    if constexpr (I < kOver) {
+      constexpr int reads = (I + 1) * kRest / kOver - I * kRest / kOver;
+      if constexpr (reads > 0) __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);
+    }
+    constexpr int writes = (I + 1) * WRITES / GROUPS - I * WRITES / GROUPS;
+    if constexpr (writes > 0) __builtin_amdgcn_sched_group_barrier(0x200, writes, 0);
+    constexpr int loads = (I + 1) * LOADS / GROUPS - I * LOADS / GROUPS;
+    if constexpr (loads > 0) __builtin_amdgcn_sched_group_barrier(0x020, loads, 0);
+    interleave<READS, WRITES, LOADS, GROUPS, I + 1>();
+  }
 }
 
 // Which tile a block takes: consecutive blocks go to different XCDs, each with its own L2, so
@@ -61,7 +80,7 @@ struct Unit {
 // (bfloat16); nk a multiple of 16.  An LDS row is 64 k, 128 bytes, whose 16-byte pieces are
 // permuted by the row's number so that a fragment read's 16 rows fall into different banks;
 // P's rows are stored so that a lane's four result tiles are 16 consecutive columns.
-template <int QTYPE, int QT>
+template <int QTYPE, int QT, int D>
 __global__ void __launch_bounds__(kThreads) tile_nt_kernel(MatArg P, MatArg Q, int np, int64_t nq, int nk, Epilogue e,
                                                             int ptiles, int tiles) {
   constexpr int BP = 128, BQ = 32 * QT, kStep = (BP + BQ) * 128;
@@ -86,32 +105,32 @@ __global__ void __launch_bounds__(kThreads) tile_nt_kernel(MatArg P, MatArg Q, i
     qoff[u] = in ? (u * 64 + row) * uint32_t(Q.ld) * kQ + piece * 16 * kQ : kAbsent;
     soff[u] = in ? (u * 64 + row) * uint32_t(Q.lds) + piece / 2 : kAbsent;
   }
-  Unit<GS_MAT_BF16> pr[BP / 64];
-  Unit<QTYPE> qr[BQ / 64];
-  auto fetch = [&](int k0) {
+  Unit<GS_MAT_BF16> pr[D][BP / 64];
+  Unit<QTYPE> qr[D][BQ / 64];
+  auto fetch = [&](int d, int k0) {
     const bool in = k0 + piece * 16 < nk;
 #pragma unroll
-    for (int u = 0; u < BP / 64; ++u) pr[u].load(pb, pb, in ? poff[u] + k0 * 2 : kAbsent, 0);
+    for (int u = 0; u < BP / 64; ++u) pr[d][u].load(pb, pb, in ? poff[u] + k0 * 2 : kAbsent, 0);
 #pragma unroll
     for (int u = 0; u < BQ / 64; ++u)
-      qr[u].load(qb, sb, in ? qoff[u] + k0 * kQ : kAbsent, in ? soff[u] + k0 / 32 : kAbsent);
+      qr[d][u].load(qb, sb, in ? qoff[u] + k0 * kQ : kAbsent, in ? soff[u] + k0 / 32 : kAbsent);
   };
   auto put = [&](uint8_t* at, int r, u32x4 a, u32x4 b) {
     const int s = (r >> 1) & 7;
     *reinterpret_cast<u32x4*>(at + r * 128 + ((piece * 2) ^ s) * 16) = a;
     *reinterpret_cast<u32x4*>(at + r * 128 + ((piece * 2 + 1) ^ s) * 16) = b;
   };
-  auto stage = [&](uint8_t* at) {
+  auto stage = [&](int d, uint8_t* at) {
     u32x4 a, b;
 #pragma unroll
     for (int u = 0; u < BP / 64; ++u) {
       const int r = u * 64 + row;
-      pr[u].operands(a, b);
+      pr[d][u].operands(a, b);
       put(at, (r & ~63) | ((r & 12) << 2) | ((r & 48) >> 2) | (r & 3), a, b);
     }
 #pragma unroll
     for (int u = 0; u < BQ / 64; ++u) {
-      qr[u].operands(a, b);
+      qr[d][u].operands(a, b);
       put(at + BP * 128, u * 64 + row, a, b);
     }
   };
@@ -123,27 +142,38 @@ __global__ void __launch_bounds__(kThreads) tile_nt_kernel(MatArg P, MatArg Q, i
   // a fragment's place within its rows: the row's number enters through bits 1-3 only
   const int r16 = lane % 16, g = lane / 16, sw = (r16 >> 1) & 7;
   const int frag0 = r16 * 128 + (g ^ sw) * 16, frag1 = r16 * 128 + ((g + 4) ^ sw) * 16;
-  fetch(0);
-  stage(lds);
-  fetch(64);
+  // loads of D steps are in flight: step s + 1 + d in set (s + d) % D
+  fetch(0, 0);
+  stage(0, lds);
+#pragma unroll
+  for (int d = 0; d < D; ++d) fetch(d, (d + 1) * 64);
   const int steps = (nk + 63) / 64;
-  for (int s = 0; s < steps; ++s) {
-    step_barrier();
-    const uint8_t* now = lds + (s & 1) * kStep;
-    stage(lds + (~s & 1) * kStep);   // past the end: zeros, not read
-    fetch((s + 2) * 64);
+  for (int s0 = 0; s0 < steps; s0 += D) {
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      const uint8_t* at = now + (kk ? frag1 : frag0);
-      bf16x8 pf[4];
+    for (int d = 0; d < D; ++d) {
+      const int s = s0 + d;
+      if (s >= steps) break;
+      step_barrier();
+      const uint8_t* now = lds + (s & 1) * kStep;
+      bf16x8 pf[2][4], qf[2][QT];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) pf[t] = *reinterpret_cast<const bf16x8*>(at + (wp * 64 + t * 16) * 128);
+      for (int kk = 0; kk < 2; ++kk) {
+        const uint8_t* at = now + (kk ? frag1 : frag0);
 #pragma unroll
-      for (int i = 0; i < QT; ++i) {
-        const bf16x8 qf = *reinterpret_cast<const bf16x8*>(at + (BP + (wq * QT + i) * 16) * 128);
+        for (int t = 0; t < 4; ++t) pf[kk][t] = *reinterpret_cast<const bf16x8*>(at + (wp * 64 + t * 16) * 128);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[t], qf, acc[i][t], 0, 0, 0);
+        for (int i = 0; i < QT; ++i) qf[kk][i] = *reinterpret_cast<const bf16x8*>(at + (BP + (wq * QT + i) * 16) * 128);
       }
+      stage(d, lds + (~s & 1) * kStep);   // past the end: zeros, not read
+      fetch(d, (s + 1 + D) * 64);
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int i = 0; i < QT; ++i)
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+            acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[kk][t], qf[kk][i], acc[i][t], 0, 0, 0);
+      interleave<2 * (4 + QT), (BP + BQ) / 32, (BP + BQ) / 32, 2 * QT>();
     }
   }
   const int col = p0 + wp * 64 + g * 16, n = np - col < 16 ? np - col : 16;
@@ -166,7 +196,7 @@ __global__ void __launch_bounds__(kThreads) tile_nt_kernel(MatArg P, MatArg Q, i
 // dz, bfloat16; P = x, bfloat16 or MX8); np and nq multiples of 16.  LDS holds 64 rows m
 // as they are in memory (plus 32 bytes a row, so that eight rows fall into different banks),
 // read transposed.
-template <int PTYPE, int QT>
+template <int PTYPE, int QT, int D>
 __global__ void __launch_bounds__(kThreads) tile_tn_kernel(MatArg P, MatArg Q, int np, int nq, int64_t rows,
                                                             int64_t per_slice, float* part, MatArg out, int ptiles,
                                                             int tiles) {
@@ -183,9 +213,9 @@ __global__ void __launch_bounds__(kThreads) tile_tn_kernel(MatArg P, MatArg Q, i
   constexpr uint32_t kP = element_bytes(PTYPE);
   const int pm = threadIdx.x / (BP / 16), pc = threadIdx.x % (BP / 16) * 16;
   const int qm = threadIdx.x / (BQ / 16), qc = threadIdx.x % (BQ / 16) * 16;
-  Unit<PTYPE> pr[kUP];
-  Unit<GS_MAT_BF16> qr[kUQ];
-  auto fetch = [&](int64_t m0) {
+  Unit<PTYPE> pr[D][kUP];
+  Unit<GS_MAT_BF16> qr[D][kUQ];
+  auto fetch = [&](int d, int64_t m0) {
     const Buffer pb = buffer_at(P.p + (m0 * P.ld + p0) * kP), qb = buffer_at(Q.p + (m0 * Q.ld + q0) * 2);
     const Buffer sb = buffer_at(PTYPE == GS_MAT_MX8 ? P.s + m0 * P.lds + p0 / 32 : nullptr);
     const int left = last - m0 < 64 ? int(last - m0) : 64;
@@ -193,27 +223,27 @@ __global__ void __launch_bounds__(kThreads) tile_tn_kernel(MatArg P, MatArg Q, i
     for (int u = 0; u < kUP; ++u) {
       const int m = pm + u * (kThreads * 16 / BP);
       const bool in = m < left && p0 + pc < np;
-      pr[u].load(pb, sb, in ? (m * uint32_t(P.ld) + pc) * kP : kAbsent, in ? m * uint32_t(P.lds) + pc / 32 : kAbsent);
+      pr[d][u].load(pb, sb, in ? (m * uint32_t(P.ld) + pc) * kP : kAbsent, in ? m * uint32_t(P.lds) + pc / 32 : kAbsent);
     }
 #pragma unroll
     for (int u = 0; u < kUQ; ++u) {
       const int m = qm + u * (kThreads * 16 / BQ);
-      qr[u].load(qb, qb, m < left && q0 + qc < nq ? (m * uint32_t(Q.ld) + qc) * 2 : kAbsent, 0);
+      qr[d][u].load(qb, qb, m < left && q0 + qc < nq ? (m * uint32_t(Q.ld) + qc) * 2 : kAbsent, 0);
     }
   };
-  auto stage = [&](uint8_t* at) {
+  auto stage = [&](int d, uint8_t* at) {
     u32x4 a, b;
 #pragma unroll
     for (int u = 0; u < kUP; ++u) {
       uint8_t* o = at + (pm + u * (kThreads * 16 / BP)) * kPitchP + pc * 2;
-      pr[u].operands(a, b);
+      pr[d][u].operands(a, b);
       *reinterpret_cast<u32x4*>(o) = a;
       *reinterpret_cast<u32x4*>(o + 16) = b;
     }
 #pragma unroll
     for (int u = 0; u < kUQ; ++u) {
       uint8_t* o = at + 64 * kPitchP + (qm + u * (kThreads * 16 / BQ)) * kPitchQ + qc * 2;
-      qr[u].operands(a, b);
+      qr[d][u].operands(a, b);
       *reinterpret_cast<u32x4*>(o) = a;
       *reinterpret_cast<u32x4*>(o + 16) = b;
     }
@@ -225,26 +255,36 @@ __global__ void __launch_bounds__(kThreads) tile_tn_kernel(MatArg P, MatArg Q, i
     for (int t = 0; t < 4; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
   const int m = lane / 16 * 8 + lane % 16 / 4, c = lane % 4 * 4;
   const int pat = m * kPitchP + (wp * 64 + c) * 2, qat = 64 * kPitchP + m * kPitchQ + (wq * QT * 16 + c) * 2;
-  fetch(first);
-  stage(lds);
-  fetch(first + 64);
+  fetch(0, first);
+  stage(0, lds);
+#pragma unroll
+  for (int d = 0; d < D; ++d) fetch(d, first + (d + 1) * 64);
   const int steps = last > first ? int((last - first + 63) / 64) : 0;
-  for (int s = 0; s < steps; ++s) {
-    step_barrier();
-    const uint8_t* now = lds + (s & 1) * kStep;
-    stage(lds + (~s & 1) * kStep);
-    fetch(first + int64_t(s + 2) * 64);
+  for (int s0 = 0; s0 < steps; s0 += D) {
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      bf16x8 pf[4];
+    for (int d = 0; d < D; ++d) {
+      const int s = s0 + d;
+      if (s >= steps) break;
+      step_barrier();
+      const uint8_t* now = lds + (s & 1) * kStep;
+      bf16x8 pf[2][4], qf[2][QT];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) pf[t] = read_transposed(now + pat + kk * 32 * kPitchP + t * 32, kPitchP);
+      for (int kk = 0; kk < 2; ++kk) {
 #pragma unroll
-      for (int i = 0; i < QT; ++i) {
-        const bf16x8 qf = read_transposed(now + qat + kk * 32 * kPitchQ + i * 32, kPitchQ);
+        for (int t = 0; t < 4; ++t) pf[kk][t] = read_transposed(now + pat + kk * 32 * kPitchP + t * 32, kPitchP);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[t], qf, acc[i][t], 0, 0, 0);
+        for (int i = 0; i < QT; ++i) qf[kk][i] = read_transposed(now + qat + kk * 32 * kPitchQ + i * 32, kPitchQ);
       }
+      stage(d, lds + (~s & 1) * kStep);
+      fetch(d, first + int64_t(s + 1 + D) * 64);
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int i = 0; i < QT; ++i)
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+            acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[kk][t], qf[kk][i], acc[i][t], 0, 0, 0);
+      interleave<4 * (4 + QT), 2 * (kUP + kUQ), 2 * (kUP + kUQ), 2 * QT>();
     }
   }
 #pragma unroll
@@ -267,10 +307,10 @@ __global__ void __launch_bounds__(kThreads) tile_tn_kernel(MatArg P, MatArg Q, i
   }
 }
 
-template <int QTYPE, int QT>
+template <int QTYPE, int QT, int D>
 hipError_t go_nt(const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, const Epilogue& e, hipStream_t s) {
   constexpr int kLds = 2 * (128 + 32 * QT) * 128;
-  const auto kernel = &tile_nt_kernel<QTYPE, QT>;
+  const auto kernel = &tile_nt_kernel<QTYPE, QT, D>;
   static const hipError_t allowed =
       hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
   if (allowed != hipSuccess) return allowed;
@@ -279,11 +319,11 @@ hipError_t go_nt(const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, c
   return hipGetLastError();
 }
 
-template <int PTYPE, int QT>
+template <int PTYPE, int QT, int D>
 hipError_t go_tn(const MatArg& P, const MatArg& Q, int np, int nq, int64_t rows, int slices, float* part,
                  const MatArg& out, hipStream_t s) {
   constexpr int kLds = 2 * 64 * (128 * 2 + 32 + 32 * QT * 2 + 32);
-  const auto kernel = &tile_tn_kernel<PTYPE, QT>;
+  const auto kernel = &tile_tn_kernel<PTYPE, QT, D>;
   static const hipError_t allowed =
       hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
   if (allowed != hipSuccess) return allowed;
@@ -302,11 +342,13 @@ bool tile_nt_takes(const MatArg& P, const MatArg& Q, int nk) {
 
 hipError_t launch_tile_nt(const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, const Epilogue& e,
                           hipStream_t s) {
-  // tiles of 256 rows where they fill the card, else of 128
-  const bool big = int64_t(div_up(np, 128)) * div_up(nq, 256) >= 192;
-  if (Q.type == GS_MAT_MX8)
-    return big ? go_nt<GS_MAT_MX8, 8>(P, Q, np, nq, nk, e, s) : go_nt<GS_MAT_MX8, 4>(P, Q, np, nq, nk, e, s);
-  return big ? go_nt<GS_MAT_BF16, 8>(P, Q, np, nq, nk, e, s) : go_nt<GS_MAT_BF16, 4>(P, Q, np, nq, nk, e, s);
+  // One 128 x 256 block a compute unit or two of 128 x 128: a long contraction runs better on
+  // the larger (8160 x 4096 to 1024: 82 us, smaller tiles 89; from MX8 the two are level, 91 and
+  // 93), but two blocks hide each other's epilogue (8160 x 1024 to 4096: 110 us and 106; with
+  // gelu and a kept z 138 and 118).
+  const bool big = nk >= 2048 && int64_t(div_up(np, 128)) * div_up(nq, 256) >= 192;
+  if (Q.type == GS_MAT_MX8) return go_nt<GS_MAT_MX8, 4, 2>(P, Q, np, nq, nk, e, s);
+  return big ? go_nt<GS_MAT_BF16, 8, 3>(P, Q, np, nq, nk, e, s) : go_nt<GS_MAT_BF16, 4, 2>(P, Q, np, nq, nk, e, s);
 }
 
 bool tile_tn_takes(const MatArg& P, const MatArg& Q, int np, int nq) {
@@ -321,8 +363,8 @@ int tile_tn_slices(int64_t rows, int np, int nq) {
 
 hipError_t launch_tile_tn(const MatArg& P, const MatArg& Q, int np, int nq, int64_t rows, int slices, float* part,
                           const MatArg& out, hipStream_t s) {
-  return P.type == GS_MAT_MX8 ? go_tn<GS_MAT_MX8, 4>(P, Q, np, nq, rows, slices, part, out, s)
-                              : go_tn<GS_MAT_BF16, 4>(P, Q, np, nq, rows, slices, part, out, s);
+  return P.type == GS_MAT_MX8 ? go_tn<GS_MAT_MX8, 4, 4>(P, Q, np, nq, rows, slices, part, out, s)
+                              : go_tn<GS_MAT_BF16, 4, 4>(P, Q, np, nq, rows, slices, part, out, s);
 }
 
 }  // namespace gsk

@@ -151,8 +151,15 @@ def _ptr(t):
     return None if t is None else C.c_void_p(t.data_ptr())
 
 
+# The current stream's handle without building a torch.cuda.Stream (3 us of a small call's
+# 12); absent from a torch that does not offer it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return C.c_void_p(_raw_stream(torch.cuda.current_device()))
         stream = torch.cuda.current_stream()
     return C.c_void_p(stream.cuda_stream)
 
@@ -408,43 +415,43 @@ class Mx8:
 
 def mx8_empty(rows, cols, device="cuda"):
     """An uninitialised MX8 matrix whose rows start at multiples of 16 bytes."""
-    q = torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.float8_e4m3fn, device=device)
+    pitch = (cols + 15) // 16 * 16
+    q = torch.empty((rows, pitch), dtype=torch.float8_e4m3fn, device=device)
     scales = torch.empty((rows, (cols + 31) // 32), dtype=torch.float8_e8m0fnu, device=device)
-    return Mx8(q[:, :cols], scales)
+    return Mx8(q if pitch == cols else q[:, :cols], scales)
+
+
+_KINDS = {torch.float32: GS_MAT_F32, torch.bfloat16: GS_MAT_BF16}
 
 
 def _matrix(t, name):
     """gs_matrix of a two-dimensional tensor (float32, bfloat16) or Mx8 with adjacent columns."""
     if t is None:
         return None
-    scales, sld, q = None, 0, t
     if isinstance(t, Mx8):
-        q, s = t.q, t.scales
-        if q.dtype != torch.float8_e4m3fn or s.dtype != torch.float8_e8m0fnu or s.dim() != 2 or q.dim() != 2:
+        q, kind = t.q, GS_MAT_MX8
+        if q.dtype != torch.float8_e4m3fn or t.scales.dtype != torch.float8_e8m0fnu:
             raise ValueError(f"{name}: an Mx8 is a float8_e4m3fn matrix with float8_e8m0fnu scales")
-        if s.shape[0] != q.shape[0] or s.shape[1] != (q.shape[1] + 31) // 32 or not _adjacent(s):
-            raise ValueError(f"{name}: scales must be [rows][ceil(cols / 32)] with adjacent columns")
-        scales, sld, kind = s.data_ptr(), _pitch(s), GS_MAT_MX8
-    elif t.dtype == torch.float32:
-        kind = GS_MAT_F32
-    elif t.dtype == torch.bfloat16:
-        kind = GS_MAT_BF16
+        blocks, scales, scales_ld = _rows(t.scales, f"{name} (scales)")
     else:
-        raise ValueError(f"{name}: expected float32, bfloat16 or an Mx8, got {t.dtype}")
-    if q.dim() != 2 or not _adjacent(q):
+        q, kind, blocks, scales, scales_ld = t, _KINDS.get(t.dtype), None, None, 0
+        if kind is None:
+            raise ValueError(f"{name}: expected float32, bfloat16 or an Mx8, got {t.dtype}")
+    (rows, cols), data, ld = _rows(q, name)
+    if blocks is not None and blocks != (rows, (cols + 31) // 32):
+        raise ValueError(f"{name}: scales must be [rows][ceil(cols / 32)]")
+    return C.byref(GsMatrix(data, scales, rows, cols, ld, scales_ld, kind))
+
+
+def _rows(t, name):
+    """(shape, address, elements between rows) of a device matrix with adjacent columns; a
+    single row's (or an empty matrix's) stride says nothing."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
         raise ValueError(f"{name}: expected a matrix with adjacent columns")
-    if not q.is_cuda or (scales is not None and not t.scales.is_cuda):
+    if not t.is_cuda:
         raise ValueError(f"{name}: expected device memory")
-    return C.byref(GsMatrix(q.data_ptr(), scales, q.shape[0], q.shape[1], _pitch(q), sld, kind))
-
-
-def _adjacent(t):
-    return t.shape[1] <= 1 or t.stride(1) == 1
-
-
-def _pitch(t):
-    """Elements between rows; a single row's (or an empty matrix's) stride says nothing."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return shape, t.data_ptr(), stride[0] if shape[0] > 1 else shape[1]
 
 
 def _floats(t, n, name):
