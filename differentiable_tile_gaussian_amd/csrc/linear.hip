@@ -169,33 +169,57 @@ __global__ void __launch_bounds__(WP* WQ * 64) gemm_tn_kernel(MatArg P, MatArg Q
 // ------------------------------------------------------------- dz, db and W^T
 
 // dz = dy act'(z) to bfloat16 (unless dz is absent) and part[slice] = the column sums of dz
-// before its rounding.  lanes (a power of two in [4, 64]) take 8 columns each of a row.
+// before its rounding.  lanes (a power of two in [4, 64]) take 8 columns each of a row (held as
+// matrix.h has it; NARROW: fewer than 8 columns), kRows rows at a time.
+constexpr int kRows = 2;
+
+template <bool NARROW>
 __global__ void __launch_bounds__(kThreads) dz_kernel(MatArg dy, MatArg z, int act, MatArg dz, float* part,
                                                        int64_t rows, int cols, int64_t per_slice, int lanes) {
   const int lane = threadIdx.x & (lanes - 1), slot = threadIdx.x / lanes, per = kThreads / lanes;
-  const int col = int(blockIdx.y) * lanes * 8 + lane * 8, n = cols - col;
+  const int col = (int(blockIdx.y) * lanes + lane) * 8;
+  const Held c = held_at(col, cols);
   const int64_t first = int64_t(blockIdx.x) * per_slice;
   const int64_t last = first + per_slice < rows ? first + per_slice : rows;
   float acc[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
-  for (int64_t row = first + slot; row < last; row += per) {
-    float v[8];
-    const Raw8 a = load_raw8(dy, row, col, n);
-    if (act != GS_ACT_NONE) {
-      const Raw8 b = load_raw8(z, row, col, n);
-      float t[8];
-      raw8_to_float(a, dy.type, v);
-      raw8_to_float(b, z.type, t);
+  for (int64_t row0 = first + slot; row0 < last; row0 += per * kRows) {
+    Raw8 a[kRows], b[kRows];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= act_slope(t[i], act);
-    } else {
-      raw8_to_float(a, dy.type, v);
+    for (int u = 0; u < kRows; ++u) {
+      const int64_t row = row0 + u * per < last ? row0 + u * per : last - 1;
+      a[u] = NARROW ? load_raw8(dy, row, col, cols - col) : load_held(dy, row, c);
     }
-    if (dz.p && n > 0) store_bf16x8(dz.p + (row * dz.ld + col) * 2, v, n);
+    if (act != GS_ACT_NONE) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] += v[i];
+      for (int u = 0; u < kRows; ++u) {
+        const int64_t row = row0 + u * per < last ? row0 + u * per : last - 1;
+        b[u] = NARROW ? load_raw8(z, row, col, cols - col) : load_held(z, row, c);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int64_t row = row0 + u * per;
+      float v[8];
+      raw8_to_float(a[u], dy.type, v);
+      if (act != GS_ACT_NONE) {
+        float t[8];
+        if (NARROW)
+          raw8_to_float(b[u], z.type, t);
+        else
+          held_to_float(b[u], z.type, c, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= act_slope(t[i], act);
+      }
+      const bool in = row < last;
+      if (dz.p && in && c.skip < 8)
+        store_bf16x8(dz.p + (row * dz.ld + (NARROW ? col : c.at)) * 2, v, NARROW ? cols - col : 8);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] += in && (NARROW || i >= c.skip) ? v[i] : 0.0f;
+    }
   }
+  if (!NARROW) move_down(c, acc);
   if (!part) return;
   __shared__ float sums[kThreads * 8];
 #pragma unroll
@@ -209,20 +233,27 @@ __global__ void __launch_bounds__(kThreads) dz_kernel(MatArg dy, MatArg z, int a
   }
 }
 
-// wt[k][n] = w[n][k], tiles of 64 x 64.
+// wt[k][n] = w[n][k], tiles of 64 x 64, 8 values to a thread on both sides (wt's rows are
+// padded to multiples of 8).
 __global__ void __launch_bounds__(kThreads) transpose_kernel(MatArg w, MatArg wt, int n, int k) {
-  __shared__ uint16_t tile[64][66];
+  __shared__ uint16_t tile[64][66];   // [k][n]
   const int k0 = blockIdx.x * 64, n0 = blockIdx.y * 64;
-  for (int i = threadIdx.x; i < 4096; i += kThreads) {
-    const int r = i / 64, c = i % 64;
-    if (n0 + r < n && k0 + c < k)
-      tile[r][c] = reinterpret_cast<const uint16_t*>(w.p)[int64_t(n0 + r) * w.ld + k0 + c];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int r = threadIdx.x / 8 + u * 32, c = threadIdx.x % 8 * 8;
+    const u32x4 v = load_raw8(w, n0 + r, k0 + c, n0 + r < n ? k - k0 - c : 0).lo;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) tile[c + i][r] = uint16_t(v[i / 2] >> (16 * (i & 1)));
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 4096; i += kThreads) {
-    const int r = i / 64, c = i % 64;
-    if (k0 + r < k && n0 + c < n)
-      reinterpret_cast<uint16_t*>(wt.p)[int64_t(k0 + r) * wt.ld + n0 + c] = tile[c][r];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int r = threadIdx.x / 8 + u * 32, c = threadIdx.x % 8 * 8;
+    if (k0 + r >= k || n0 + c >= n) continue;
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint32_t*>(&tile[r][c + 2 * i]);
+    *reinterpret_cast<u32x4*>(wt.p + (int64_t(k0 + r) * wt.ld + n0 + c) * 2) = v;
   }
 }
 
@@ -305,8 +336,12 @@ hipError_t launch_linear_bwd(const MatArg& dy, const MatArg& z, int act, const M
     const int64_t per = (rows + slices - 1) / slices;
     {
       GSK_PROF("linear_dz", s);
-      dz_kernel<<<dim3(slices, div_up(n, lanes * 8)), kThreads, 0, s>>>(dy, z, act, own_dz ? dz : none,
-                                                                        dbias ? b.db : nullptr, rows, n, per, lanes);
+      const dim3 grid(slices, div_up(n, lanes * 8));
+      float* part = dbias ? b.db : nullptr;
+      if (n < 8)
+        dz_kernel<true><<<grid, kThreads, 0, s>>>(dy, z, act, own_dz ? dz : none, part, rows, n, per, lanes);
+      else
+        dz_kernel<false><<<grid, kThreads, 0, s>>>(dy, z, act, own_dz ? dz : none, part, rows, n, per, lanes);
     }
     if (dbias) {
       if ((e = launch_sum_parts(b.db, slices, n, 0, 1, MatArg{}, dbias, s)) != hipSuccess) return e;

@@ -153,6 +153,75 @@ __device__ inline u32x4 raw8_to_bf16(const Raw8& r, int type) {
   return u32x4{a[0], a[1], b[0], b[1]};
 }
 
+// ---- rows of at least 8 columns, 8 to a lane, without branches
+//
+// A row is held by neighbouring lanes, lane l's chunk starting at column 8 l.  A chunk that
+// would pass the row's end is held from column cols - 8 instead: its first `skip` values are
+// columns that the lane before it holds too (from 8 on: the whole chunk is another's).  So
+// every load is a full one, inside the row.  Sums leave the repeated values out; float32 and
+// bfloat16 results are written from where they are held, the repeated ones twice with the
+// same bits; MX8 results, whose blocks have their places, are moved down first.
+struct Held {
+  int at, skip;
+};
+
+__device__ inline Held held_at(int col, int cols) {
+  const int at = col < cols - 8 ? col : cols - 8;
+  return {at, col - at};
+}
+
+// The chunk's columns at .. at + 7 (any alignment).  MX8: a chunk at a block's end takes two
+// scales, in the low and the second byte.
+__device__ inline Raw8 load_held(const MatArg& m, int64_t row, const Held& c) {
+  Raw8 r;
+  r.hi = u32x4{0, 0, 0, 0};
+  r.scale = 0;
+  if (m.type == GS_MAT_BF16) {
+    __builtin_memcpy(&r.lo, __builtin_assume_aligned(m.p + (row * m.ld + c.at) * 2, 2), 16);
+  } else if (m.type == GS_MAT_F32) {
+    const char* p = m.p + (row * m.ld + c.at) * 4;
+    __builtin_memcpy(&r.lo, __builtin_assume_aligned(p, 4), 16);
+    __builtin_memcpy(&r.hi, __builtin_assume_aligned(p + 16, 4), 16);
+  } else {
+    u32x2 v;
+    __builtin_memcpy(&v, m.p + row * m.ld + c.at, 8);
+    r.lo = u32x4{v[0], v[1], 0, 0};
+    const uint8_t* s = m.s + row * m.lds;
+    r.scale = s[c.at >> 5] | uint32_t(s[(c.at + 7) >> 5]) << 8;
+  }
+  return r;
+}
+
+__device__ inline void held_to_float(const Raw8& r, int type, const Held& c, float v[8]) {
+  if (type != GS_MAT_MX8) {
+    raw8_to_float(r, type, v);
+    return;
+  }
+  Raw8 one = r;
+  one.scale = r.scale & 255u;
+  raw8_to_float(one, type, v);
+  if (c.skip > 0) {   // only such a chunk can lie across a block's end
+    one.scale = r.scale >> 8;
+    float w[8];
+    raw8_to_float(one, type, w);
+    const int left = 32 - (c.at & 31);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < left ? v[i] : w[i];
+  }
+}
+
+// Moves a held chunk's own values to its front, zeros behind them.
+__device__ inline void move_down(const Held& c, float v[8]) {
+#pragma unroll
+  for (int b = 4; b > 0; b /= 2)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c.skip & b ? (i + b < 8 ? v[i + b] : 0.0f) : v[i];
+  if (c.skip >= 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+  }
+}
+
 // ---- buffer access
 //
 // The row kernels' fast paths load and store through buffer descriptors, whose range check

@@ -12,50 +12,56 @@ namespace gsk {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 4;
+constexpr int kRows = 2;
 
-// lanes: lanes per row, a power of two in [4, 64].
+// lanes: lanes per row, a power of two in [4, 64].  NARROW: fewer than 8 columns.
+template <bool NARROW>
 __global__ void __launch_bounds__(kThreads) mx8_pack_kernel(MatArg x, MatArg q, int64_t rows, int cols, int lanes) {
   const int lane = threadIdx.x & (lanes - 1);
   const int per = kThreads / lanes;   // rows a block takes at a time
   const int64_t row0 = int64_t(blockIdx.x) * (per * kRows) + threadIdx.x / lanes;
-  for (int c0 = 0; c0 < cols; c0 += lanes * 8) {
-    const int col = c0 + lane * 8;
-    Raw8 raw[kRows];
+  const int col = (int(blockIdx.y) * lanes + lane) * 8;
+  const Held c = held_at(col, cols);
+  Raw8 raw[kRows];
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      const int64_t row = row0 + int64_t(u) * per;
-      raw[u] = load_raw8(x, row, col, row < rows ? cols - col : 0);
-    }
+  for (int u = 0; u < kRows; ++u) {
+    const int64_t row = row0 + int64_t(u) * per;
+    raw[u] = NARROW ? load_raw8(x, row, col, row < rows ? cols - col : 0)
+                    : load_held(x, row < rows ? row : rows - 1, c);
+  }
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      const int64_t row = row0 + int64_t(u) * per;
-      float v[8];
-      raw8_to_float(raw[u], x.type, v);
-      store_mx8_quad(q, row, col, v, row < rows ? cols - col : 0);
-    }
+  for (int u = 0; u < kRows; ++u) {
+    const int64_t row = row0 + int64_t(u) * per;
+    float v[8];
+    raw8_to_float(raw[u], x.type, v);
+    if (!NARROW) move_down(c, v);
+    store_mx8_quad(q, row, col, v, row < rows ? cols - col : 0);
   }
 }
 
+template <bool NARROW>
 __global__ void __launch_bounds__(kThreads) mx8_unpack_kernel(MatArg q, MatArg x, int64_t rows, int cols, int lanes) {
   const int lane = threadIdx.x & (lanes - 1);
   const int per = kThreads / lanes;
   const int64_t row0 = int64_t(blockIdx.x) * (per * kRows) + threadIdx.x / lanes;
-  for (int c0 = 0; c0 < cols; c0 += lanes * 8) {
-    const int col = c0 + lane * 8;
-    Raw8 raw[kRows];
+  const int col = (int(blockIdx.y) * lanes + lane) * 8;
+  const Held c = held_at(col, cols);
+  Raw8 raw[kRows];
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      const int64_t row = row0 + int64_t(u) * per;
-      raw[u] = load_raw8(q, row, col, row < rows ? cols - col : 0);
-    }
+  for (int u = 0; u < kRows; ++u) {
+    const int64_t row = row0 + int64_t(u) * per;
+    raw[u] = NARROW ? load_raw8(q, row, col, row < rows ? cols - col : 0)
+                    : load_held(q, row < rows ? row : rows - 1, c);
+  }
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      const int64_t row = row0 + int64_t(u) * per;
-      float v[8];
+  for (int u = 0; u < kRows; ++u) {
+    const int64_t row = row0 + int64_t(u) * per;
+    float v[8];
+    if (NARROW)
       raw8_to_float(raw[u], GS_MAT_MX8, v);
-      if (row < rows && col < cols) store8(x, row, col, v, cols - col);
-    }
+    else
+      held_to_float(raw[u], GS_MAT_MX8, c, v);
+    if (row < rows && c.skip < 8) store8(x, row, NARROW ? col : c.at, v, NARROW ? cols - col : 8);
   }
 }
 
@@ -65,21 +71,29 @@ int lanes_for(int cols) {
   return lanes;
 }
 
-unsigned blocks_for(int64_t rows, int lanes) { return div_up(rows, int64_t(kThreads / lanes) * kRows); }
+dim3 blocks_for(int64_t rows, int cols, int lanes) {
+  return dim3(div_up(rows, int64_t(kThreads / lanes) * kRows), div_up(cols, lanes * 8));
+}
 
 }  // namespace
 
 hipError_t launch_mx8_pack(const MatArg& x, const MatArg& q, int64_t rows, int cols, hipStream_t s) {
   const int lanes = lanes_for(cols);
   GSK_PROF("mx8_pack", s);
-  mx8_pack_kernel<<<blocks_for(rows, lanes), kThreads, 0, s>>>(x, q, rows, cols, lanes);
+  if (cols < 8)
+    mx8_pack_kernel<true><<<blocks_for(rows, cols, lanes), kThreads, 0, s>>>(x, q, rows, cols, lanes);
+  else
+    mx8_pack_kernel<false><<<blocks_for(rows, cols, lanes), kThreads, 0, s>>>(x, q, rows, cols, lanes);
   return hipGetLastError();
 }
 
 hipError_t launch_mx8_unpack(const MatArg& q, const MatArg& x, int64_t rows, int cols, hipStream_t s) {
   const int lanes = lanes_for(cols);
   GSK_PROF("mx8_unpack", s);
-  mx8_unpack_kernel<<<blocks_for(rows, lanes), kThreads, 0, s>>>(q, x, rows, cols, lanes);
+  if (cols < 8)
+    mx8_unpack_kernel<true><<<blocks_for(rows, cols, lanes), kThreads, 0, s>>>(q, x, rows, cols, lanes);
+  else
+    mx8_unpack_kernel<false><<<blocks_for(rows, cols, lanes), kThreads, 0, s>>>(q, x, rows, cols, lanes);
   return hipGetLastError();
 }
 

@@ -2,10 +2,10 @@
 // and its gradients dh = rstd (u - xhat mean(u xhat)) + dres, dw = sum_rows dy xhat, where
 // u = dy w and xhat = h rstd.
 //
-// Streams bounded by HBM.  A row is held by 4 to 64 lanes, 8 columns a lane at a time (so an
+// Streams bounded by HBM.  A row is held by 4 to 256 lanes, 8 columns a lane at a time (so an
 // MX8 block is four neighbouring lanes), in registers from its load to its store: each input
-// is read once and each output written once, up to kMaxHeld columns.  Wider rows are walked
-// twice by one wave, the second time from the caches.
+// is read once and each output written once, from 8 to kMaxHeld columns.  Other rows are
+// walked twice by one wave, the second time from the caches.
 #include "matrix.h"
 #include "profile.h"
 
@@ -13,12 +13,20 @@ namespace gsk {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxHeld = 4096;   // 64 lanes x 8 chunks x 8 columns
+constexpr int kMaxHeld = 4096;   // 256 lanes x 2 chunks x 8 columns
 
+// The sum over a row's lanes; LANES == 256: over the block's waves in order, with `turn` (how
+// many sums came before) alternating two places, so that one barrier a sum is enough.
 template <int LANES>
-__device__ inline float row_sum(float v) {
+__device__ inline float row_sum(float v, int turn = 0) {
 #pragma unroll
-  for (int o = LANES / 2; o > 0; o /= 2) v += __shfl_xor(v, o);
+  for (int o = (LANES < 64 ? LANES : 64) / 2; o > 0; o /= 2) v += __shfl_xor(v, o);
+  if constexpr (LANES == 256) {
+    __shared__ float sums[2][4];
+    if (threadIdx.x % 64 == 0) sums[turn & 1][threadIdx.x / 64] = v;
+    __syncthreads();
+    v = sums[turn & 1][0] + sums[turn & 1][1] + sums[turn & 1][2] + sums[turn & 1][3];
+  }
   return v;
 }
 
@@ -43,60 +51,80 @@ __device__ inline void store_chunk(const MatArg& m, int64_t row, int col, const 
     store8(m, row, col, v, n);
 }
 
-// LANES lanes hold a row, CHUNKS chunks each.
-template <int LANES, int CHUNKS>
+// LANES lanes hold a row, CHUNKS chunks each (matrix.h has how), and take ROWS rows side by
+// side: their loads are all issued before the first is used.
+template <int LANES, int CHUNKS, int ROWS>
 __global__ void __launch_bounds__(kThreads) rmsnorm_fwd_kernel(NormFwdArgs a) {
   constexpr int kPer = kThreads / LANES;
   const int lane = threadIdx.x % LANES;
+  const int64_t first = int64_t(blockIdx.x) * (kPer * ROWS) + threadIdx.x / LANES;
+  Raw8 xr[ROWS][CHUNKS], rr[ROWS][CHUNKS];
+#pragma unroll
+  for (int u = 0; u < ROWS; ++u) {
+    const int64_t row = first + u * kPer < a.rows ? first + u * kPer : a.rows - 1;
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) xr[u][c] = load_held(a.x, row, held_at((c * LANES + lane) * 8, a.cols));
+  }
+  if (a.r.p) {
+#pragma unroll
+    for (int u = 0; u < ROWS; ++u) {
+      const int64_t row = first + u * kPer < a.rows ? first + u * kPer : a.rows - 1;
+#pragma unroll
+      for (int c = 0; c < CHUNKS; ++c) rr[u][c] = load_held(a.r, row, held_at((c * LANES + lane) * 8, a.cols));
+    }
+  }
   float w[CHUNKS][8];
 #pragma unroll
-  for (int c = 0; c < CHUNKS; ++c) load_weight(a.w, (c * LANES + lane) * 8, a.cols - (c * LANES + lane) * 8, w[c]);
-  for (int64_t row0 = int64_t(blockIdx.x) * kPer; row0 < a.rows; row0 += int64_t(gridDim.x) * kPer) {
-    const int64_t row = row0 + threadIdx.x / LANES;
-    const bool in = row < a.rows;
-    Raw8 xr[CHUNKS], rr[CHUNKS];
+  for (int c = 0; c < CHUNKS; ++c) {
+    const Held t = held_at((c * LANES + lane) * 8, a.cols);
 #pragma unroll
-    for (int c = 0; c < CHUNKS; ++c) {
-      const int col = (c * LANES + lane) * 8;
-      xr[c] = load_raw8(a.x, row, col, in ? a.cols - col : 0);
-    }
-    if (a.r.p) {
+    for (int i = 0; i < 8; ++i) w[c][i] = a.w[t.at + i];
+  }
 #pragma unroll
-      for (int c = 0; c < CHUNKS; ++c) {
-        const int col = (c * LANES + lane) * 8;
-        rr[c] = load_raw8(a.r, row, col, in ? a.cols - col : 0);
-      }
-    }
+  for (int u = 0; u < ROWS; ++u) {
+    const int64_t row = first + u * kPer;
     float h[CHUNKS][8], sum = 0.0f;
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
-      raw8_to_float(xr[c], a.x.type, h[c]);
+      const Held t = held_at((c * LANES + lane) * 8, a.cols);
+      raw8_to_float(xr[u][c], a.x.type, h[c]);
       if (a.r.p) {
-        float t[8];
-        raw8_to_float(rr[c], a.r.type, t);
+        float r[8];
+        raw8_to_float(rr[u][c], a.r.type, r);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[c][i] += t[i];
+        for (int i = 0; i < 8; ++i) h[c][i] += r[i];
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum += h[c][i] * h[c][i];
+      for (int i = 0; i < 8; ++i) sum += i >= t.skip ? h[c][i] * h[c][i] : 0.0f;
     }
-    sum = row_sum<LANES>(sum);
+    sum = row_sum<LANES>(sum, u);
     const float rstd = 1.0f / sqrtf(sum * a.inv_cols + a.eps);
+    const bool in = row < a.rows;
     if (in && lane == 0 && a.rstd) a.rstd[row] = rstd;
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
-      const int col = (c * LANES + lane) * 8, n = in ? a.cols - col : 0;
-      if (a.h.p) store_chunk(a.h, row, col, h[c], n);
-      if (a.ckpt.p) store_mx8_quad(a.ckpt, row, col, h[c], n);
+      const int col = (c * LANES + lane) * 8;
+      const Held t = held_at(col, a.cols);
       float y[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] = h[c][i] * rstd * w[c][i];
-      store_chunk(a.y, row, col, y, n);
+      const bool mine = in && t.skip < 8;
+      if (a.h.p && mine) store8(a.h, row, t.at, h[c], 8);
+      if (a.y.type == GS_MAT_MX8) {
+        move_down(t, y);
+        store_mx8_quad(a.y, row, col, y, in ? a.cols - col : 0);
+      } else if (mine) {
+        store8(a.y, row, t.at, y, 8);
+      }
+      if (a.ckpt.p) {
+        move_down(t, h[c]);
+        store_mx8_quad(a.ckpt, row, col, h[c], in ? a.cols - col : 0);
+      }
     }
   }
 }
 
-// Rows of more than kMaxHeld columns: a wave a row, walked twice.
+// Rows of fewer than 8 or more than kMaxHeld columns: a wave a row, walked twice.
 __global__ void __launch_bounds__(kThreads) rmsnorm_fwd_wide_kernel(NormFwdArgs a) {
   const int lane = threadIdx.x % 64;
   const int64_t row = int64_t(blockIdx.x) * (kThreads / 64) + threadIdx.x / 64;
@@ -151,45 +179,48 @@ __global__ void __launch_bounds__(kThreads) rmsnorm_bwd_kernel(NormBwdArgs a) {
   float w[CHUNKS][8], acc[CHUNKS][8];
 #pragma unroll
   for (int c = 0; c < CHUNKS; ++c) {
-    load_weight(a.w, (c * LANES + lane) * 8, a.cols - (c * LANES + lane) * 8, w[c]);
+    const Held t = held_at((c * LANES + lane) * 8, a.cols);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[c][i] = 0.0f;
+    for (int i = 0; i < 8; ++i) {
+      w[c][i] = a.w[t.at + i];
+      acc[c][i] = 0.0f;
+    }
   }
+  int turn = 0;
   for (int64_t row0 = int64_t(blockIdx.x) * kPer; row0 < a.rows; row0 += int64_t(gridDim.x) * kPer) {
-    const int64_t row = row0 + threadIdx.x / LANES;
-    const bool in = row < a.rows;
+    const int64_t own = row0 + threadIdx.x / LANES, row = own < a.rows ? own : a.rows - 1;
+    const bool in = own < a.rows;
     Raw8 dr[CHUNKS], hr[CHUNKS], rr[CHUNKS];
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
-      const int col = (c * LANES + lane) * 8, n = in ? a.cols - col : 0;
-      dr[c] = load_raw8(a.dy, row, col, n);
-      hr[c] = load_raw8(a.h, row, col, n);
+      const Held t = held_at((c * LANES + lane) * 8, a.cols);
+      dr[c] = load_held(a.dy, row, t);
+      hr[c] = load_held(a.h, row, t);
     }
     if (a.dres.p) {
 #pragma unroll
-      for (int c = 0; c < CHUNKS; ++c) {
-        const int col = (c * LANES + lane) * 8;
-        rr[c] = load_raw8(a.dres, row, col, in ? a.cols - col : 0);
-      }
+      for (int c = 0; c < CHUNKS; ++c) rr[c] = load_held(a.dres, row, held_at((c * LANES + lane) * 8, a.cols));
     }
-    const float rstd = in ? a.rstd[row] : 0.0f;
+    const float rstd = a.rstd[row];
     float dy[CHUNKS][8], xh[CHUNKS][8], dot = 0.0f;
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
+      const Held t = held_at((c * LANES + lane) * 8, a.cols);
+      const int skip = in ? t.skip : 8;
       raw8_to_float(dr[c], a.dy.type, dy[c]);
-      raw8_to_float(hr[c], a.h.type, xh[c]);
+      held_to_float(hr[c], a.h.type, t, xh[c]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         xh[c][i] *= rstd;
-        const float p = dy[c][i] * xh[c][i];
+        const float p = i >= skip ? dy[c][i] * xh[c][i] : 0.0f;
         acc[c][i] += p;
         dot += p * w[c][i];
       }
     }
-    const float mean = row_sum<LANES>(dot) * a.inv_cols;
+    const float mean = row_sum<LANES>(dot, turn++) * a.inv_cols;
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
-      const int col = (c * LANES + lane) * 8, n = in ? a.cols - col : 0;
+      const Held t = held_at((c * LANES + lane) * 8, a.cols);
       float o[8];
       if (a.dres.p) {
         raw8_to_float(rr[c], a.dres.type, o);
@@ -199,16 +230,16 @@ __global__ void __launch_bounds__(kThreads) rmsnorm_bwd_kernel(NormBwdArgs a) {
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[i] += rstd * (dy[c][i] * w[c][i] - xh[c][i] * mean);
-      if (n > 0) store8(a.dh, row, col, o, n);
+      if (in && t.skip < 8) store8(a.dh, row, t.at, o, 8);
     }
   }
   if (!a.part) return;
   // the block's sum of each column, in the order of its row slots
-  __shared__ float sums[kPer * LANES * 8 <= 2048 ? 2048 : 1];
-  static_assert(kPer * LANES * 8 == 2048, "one chunk of every thread at a time");
+  __shared__ float sums[kThreads * 8];   // one chunk of every thread at a time
   float* out = a.part + int64_t(blockIdx.x) * a.cols;
 #pragma unroll
   for (int c = 0; c < CHUNKS; ++c) {
+    move_down(held_at((c * LANES + lane) * 8, a.cols), acc[c]);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) sums[threadIdx.x * 8 + i] = acc[c][i];
@@ -222,8 +253,8 @@ __global__ void __launch_bounds__(kThreads) rmsnorm_bwd_kernel(NormBwdArgs a) {
   }
 }
 
-// Rows of more than kMaxHeld columns: a wave a row, walked twice; the weight's gradient has
-// its own kernel.
+// Rows of fewer than 8 or more than kMaxHeld columns: a wave a row, walked twice; the
+// weight's gradient has its own kernel.
 __global__ void __launch_bounds__(kThreads) rmsnorm_bwd_wide_kernel(NormBwdArgs a) {
   const int lane = threadIdx.x % 64;
   const int64_t row = int64_t(blockIdx.x) * (kThreads / 64) + threadIdx.x / 64;
@@ -284,41 +315,49 @@ __global__ void __launch_bounds__(kThreads) rmsnorm_dw_wide_kernel(NormBwdArgs a
   }
 }
 
+// Lanes of a row: the smallest power of two that holds it in one chunk up to a wave, a wave
+// with two chunks, and the whole block beyond (8160 rows of 4096 columns by one wave each, eight
+// chunks in its registers: forward 57 us and backward 85, by the block 47 and 46).
 int lanes_for(int cols) {
   int lanes = 4;
   while (lanes < 64 && lanes * 8 < cols) lanes *= 2;
-  return lanes;
+  return cols > 1024 ? 256 : lanes;
 }
 
-// Blocks of the backward: enough to fill the card, few enough that their partial sums stay
-// small beside the rows.
+// Whether the kernels that do not hold a row take it.
+bool wide(int cols) { return cols < 8 || cols > kMaxHeld; }
+
+// Blocks of the backward: as many as the kernel's registers let reside at once (five waves a
+// SIMD; 1M rows of 128: 161 us, with 1024 blocks 178, with 2048 183).
 int bwd_blocks(int64_t rows, int cols) {
-  if (cols > kMaxHeld) return int(rows < 256 ? (rows < 1 ? 1 : rows) : 256);
+  if (wide(cols)) return int(rows < 256 ? (rows < 1 ? 1 : rows) : 256);
   const int64_t per = kThreads / lanes_for(cols);
   const int64_t want = (rows + per - 1) / per;
-  return int(want < 1 ? 1 : (want > 1024 ? 1024 : want));
+  return int(want < 1 ? 1 : (want > 1280 ? 1280 : want));
 }
 
 template <template <int, int> class Launch, typename Args>
 void by_width(int cols, const Args& a, unsigned blocks, hipStream_t s) {
-  const int chunks = (cols + 511) / 512;
   switch (lanes_for(cols)) {
     case 4: Launch<4, 1>::go(a, blocks, s); break;
     case 8: Launch<8, 1>::go(a, blocks, s); break;
     case 16: Launch<16, 1>::go(a, blocks, s); break;
     case 32: Launch<32, 1>::go(a, blocks, s); break;
+    case 64:
+      if (cols <= 512) Launch<64, 1>::go(a, blocks, s);
+      else Launch<64, 2>::go(a, blocks, s);
+      break;
     default:
-      if (chunks <= 1) Launch<64, 1>::go(a, blocks, s);
-      else if (chunks <= 2) Launch<64, 2>::go(a, blocks, s);
-      else if (chunks <= 4) Launch<64, 4>::go(a, blocks, s);
-      else Launch<64, 8>::go(a, blocks, s);
+      if (cols <= 2048) Launch<256, 1>::go(a, blocks, s);
+      else Launch<256, 2>::go(a, blocks, s);
   }
 }
 
 template <int L, int C>
 struct Fwd {
-  static void go(const NormFwdArgs& a, unsigned blocks, hipStream_t s) {
-    rmsnorm_fwd_kernel<L, C><<<blocks, kThreads, 0, s>>>(a);
+  static void go(const NormFwdArgs& a, unsigned, hipStream_t s) {
+    constexpr int kRows = C == 1 ? 2 : 1;
+    rmsnorm_fwd_kernel<L, C, kRows><<<div_up(a.rows, kThreads / L * kRows), kThreads, 0, s>>>(a);
   }
 };
 template <int L, int C>
@@ -372,11 +411,10 @@ hipError_t launch_rmsnorm_fwd(const MatArg& x, const MatArg& r, const float* w, 
                               hipStream_t s) {
   const NormFwdArgs a{x, r, h, ckpt, y, w, rstd, eps, 1.0f / float(cols), rows, cols};
   GSK_PROF("rmsnorm_fwd", s);
-  if (cols > kMaxHeld) {
+  if (wide(cols)) {
     rmsnorm_fwd_wide_kernel<<<div_up(rows, kThreads / 64), kThreads, 0, s>>>(a);
   } else {
-    const int64_t want = div_up(rows, kThreads / lanes_for(cols));
-    by_width<Fwd>(cols, a, unsigned(want > 4096 ? 4096 : want), s);
+    by_width<Fwd>(cols, a, 0, s);
   }
   return hipGetLastError();
 }
@@ -391,7 +429,7 @@ hipError_t launch_rmsnorm_bwd(const MatArg& dy, const MatArg& h, const float* w,
   const int blocks = bwd_blocks(rows, cols);
   float* part = dweight ? static_cast<float*>(ws) : nullptr;
   const NormBwdArgs a{dy, h, dres, dh, w, rstd, part, 1.0f / float(cols), rows, cols};
-  if (cols > kMaxHeld) {
+  if (wide(cols)) {
     if (rows > 0) {
       GSK_PROF("rmsnorm_bwd", s);
       rmsnorm_bwd_wide_kernel<<<div_up(rows, kThreads / 64), kThreads, 0, s>>>(a);
