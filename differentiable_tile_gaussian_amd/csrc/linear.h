@@ -107,12 +107,10 @@ hipError_t launch_rows_bwd(const MatArg& dy, const MatArg& z, int act, const Mat
 
 // ---- linear_tiles.hip: products bounded by the matrix cores, in 128-column tiles
 // out(q, p) = sum_k Q(q, k) P(p, k), finished as a forward's result
-bool tile_nt_takes(const MatArg& P, const MatArg& Q, int nk);
 hipError_t launch_tile_nt(const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, const Epilogue& e,
                           hipStream_t s);
 // out(q, p) = sum_m Q(m, q) P(m, p) in `slices` parts of the rows m (part: [slices][nq][np]
 // where there are several)
-bool tile_tn_takes(const MatArg& P, const MatArg& Q, int np, int nq);
 int tile_tn_slices(int64_t rows, int np, int nq);
 hipError_t launch_tile_tn(const MatArg& P, const MatArg& Q, int np, int nq, int64_t rows, int slices, float* part,
                           const MatArg& out, hipStream_t s);

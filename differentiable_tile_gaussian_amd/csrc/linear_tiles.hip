@@ -60,6 +60,17 @@ struct Unit {
     else
       b = buffer_load16(data, off + 16);
   }
+  // n: columns of the 16 that exist.
+  __device__ void load_any(const MatArg& m, int64_t row, int col, int n) {
+    const Raw8 lo = load_raw8(m, row, col, n), hi = load_raw8(m, row, col + 8, n - 8);
+    scale = lo.scale;
+    if constexpr (TYPE == GS_MAT_MX8) {
+      a = u32x4{lo.lo[0], lo.lo[1], hi.lo[0], hi.lo[1]};
+    } else {
+      a = lo.lo;
+      b = hi.lo;
+    }
+  }
   __device__ void operands(u32x4& p, u32x4& q) const {
     if constexpr (TYPE == GS_MAT_MX8) {
       const float s = mx8_scale(scale);
@@ -77,10 +88,10 @@ struct Unit {
 // ------------------------------------------------- contraction contiguous in both operands
 
 // out(q, p) = sum_k Q(q, k) P(p, k) for the rows q of Q (bfloat16 or MX8) and p of P
-// (bfloat16); nk a multiple of 16.  An LDS row is 64 k, 128 bytes, whose 16-byte pieces are
+// (bfloat16).  WHOLE: nk is a multiple of 16 and both are in buffers' reach.  An LDS row is 64 k, 128 bytes, whose 16-byte pieces are
 // permuted by the row's number so that a fragment read's 16 rows fall into different banks;
 // P's rows are stored so that a lane's four result tiles are 16 consecutive columns.
-template <int QTYPE, int QT, int D>
+template <int QTYPE, int QT, int D, bool WHOLE>
 __global__ void __launch_bounds__(kThreads) tile_nt_kernel(MatArg P, MatArg Q, int np, int64_t nq, int nk, Epilogue e,
                                                             int ptiles, int tiles) {
   constexpr int BP = 128, BQ = 32 * QT, kStep = (BP + BQ) * 128;
@@ -109,6 +120,16 @@ __global__ void __launch_bounds__(kThreads) tile_nt_kernel(MatArg P, MatArg Q, i
   Unit<QTYPE> qr[D][BQ / 64];
   auto fetch = [&](int d, int k0) {
     const bool in = k0 + piece * 16 < nk;
+    if constexpr (!WHOLE) {
+      const int k = k0 + piece * 16;
+#pragma unroll
+      for (int u = 0; u < BP / 64; ++u)
+        pr[d][u].load_any(P, p0 + u * 64 + row, k, p0 + u * 64 + row < np ? nk - k : 0);
+#pragma unroll
+      for (int u = 0; u < BQ / 64; ++u)
+        qr[d][u].load_any(Q, q0 + u * 64 + row, k, q0 + u * 64 + row < nq ? nk - k : 0);
+      return;
+    }
 #pragma unroll
     for (int u = 0; u < BP / 64; ++u) pr[d][u].load(pb, pb, in ? poff[u] + k0 * 2 : kAbsent, 0);
 #pragma unroll
@@ -193,10 +214,11 @@ __global__ void __launch_bounds__(kThreads) tile_nt_kernel(MatArg P, MatArg Q, i
 // ------------------------------------------------- contraction over the operands' rows
 
 // out(q, p) = sum_m Q(m, q) P(m, p) for m in the block's slice: the weight's gradient (Q =
-// dz, bfloat16; P = x, bfloat16 or MX8); np and nq multiples of 16.  LDS holds 64 rows m
+// dz, bfloat16; P = x, bfloat16 or MX8).  WHOLE: np and nq are multiples of 16 and both
+// matrices in buffers' reach.  LDS holds 64 rows m
 // as they are in memory (plus 32 bytes a row, so that eight rows fall into different banks),
 // read transposed.
-template <int PTYPE, int QT, int D>
+template <int PTYPE, int QT, int D, bool WHOLE>
 __global__ void __launch_bounds__(kThreads) tile_tn_kernel(MatArg P, MatArg Q, int np, int nq, int64_t rows,
                                                             int64_t per_slice, float* part, MatArg out, int ptiles,
                                                             int tiles) {
@@ -219,6 +241,19 @@ __global__ void __launch_bounds__(kThreads) tile_tn_kernel(MatArg P, MatArg Q, i
     const Buffer pb = buffer_at(P.p + (m0 * P.ld + p0) * kP), qb = buffer_at(Q.p + (m0 * Q.ld + q0) * 2);
     const Buffer sb = buffer_at(PTYPE == GS_MAT_MX8 ? P.s + m0 * P.lds + p0 / 32 : nullptr);
     const int left = last - m0 < 64 ? int(last - m0) : 64;
+    if constexpr (!WHOLE) {
+#pragma unroll
+      for (int u = 0; u < kUP; ++u) {
+        const int m = pm + u * (kThreads * 16 / BP);
+        pr[d][u].load_any(P, m0 + m, p0 + pc, m < left ? np - p0 - pc : 0);
+      }
+#pragma unroll
+      for (int u = 0; u < kUQ; ++u) {
+        const int m = qm + u * (kThreads * 16 / BQ);
+        qr[d][u].load_any(Q, m0 + m, q0 + qc, m < left ? nq - q0 - qc : 0);
+      }
+      return;
+    }
 #pragma unroll
     for (int u = 0; u < kUP; ++u) {
       const int m = pm + u * (kThreads * 16 / BP);
@@ -295,8 +330,19 @@ __global__ void __launch_bounds__(kThreads) tile_tn_kernel(MatArg P, MatArg Q, i
       const int p = p0 + wp * 64 + t * 16 + lane / 16 * 4;
       if (q >= nq || p >= np) continue;
       const f32x4 v = acc[i][t];
+      if (!WHOLE && p + 4 > np) {   // the last columns of an odd width
+        for (int j = 0; p + j < np; ++j) {
+          if (part)
+            part[(int64_t(blockIdx.y) * nq + q) * np + p + j] = v[j];
+          else if (out.type == GS_MAT_F32)
+            reinterpret_cast<float*>(out.p)[int64_t(q) * out.ld + p + j] = v[j];
+          else
+            reinterpret_cast<uint16_t*>(out.p)[int64_t(q) * out.ld + p + j] = uint16_t(pack_bf16(v[j], 0.0f));
+        }
+        continue;
+      }
       if (part) {
-        __builtin_memcpy(part + (int64_t(blockIdx.y) * nq + q) * np + p, &v, 16);
+        __builtin_memcpy(__builtin_assume_aligned(part + (int64_t(blockIdx.y) * nq + q) * np + p, 4), &v, 16);
       } else if (out.type == GS_MAT_F32) {
         __builtin_memcpy(__builtin_assume_aligned(reinterpret_cast<float*>(out.p) + int64_t(q) * out.ld + p, 4), &v, 16);
       } else {
@@ -307,10 +353,10 @@ __global__ void __launch_bounds__(kThreads) tile_tn_kernel(MatArg P, MatArg Q, i
   }
 }
 
-template <int QTYPE, int QT, int D>
+template <int QTYPE, int QT, int D, bool WHOLE>
 hipError_t go_nt(const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, const Epilogue& e, hipStream_t s) {
   constexpr int kLds = 2 * (128 + 32 * QT) * 128;
-  const auto kernel = &tile_nt_kernel<QTYPE, QT, D>;
+  const auto kernel = &tile_nt_kernel<QTYPE, QT, D, WHOLE>;
   static const hipError_t allowed =
       hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
   if (allowed != hipSuccess) return allowed;
@@ -319,11 +365,11 @@ hipError_t go_nt(const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, c
   return hipGetLastError();
 }
 
-template <int PTYPE, int QT, int D>
+template <int PTYPE, int QT, int D, bool WHOLE>
 hipError_t go_tn(const MatArg& P, const MatArg& Q, int np, int nq, int64_t rows, int slices, float* part,
                  const MatArg& out, hipStream_t s) {
   constexpr int kLds = 2 * 64 * (128 * 2 + 32 + 32 * QT * 2 + 32);
-  const auto kernel = &tile_tn_kernel<PTYPE, QT, D>;
+  const auto kernel = &tile_tn_kernel<PTYPE, QT, D, WHOLE>;
   static const hipError_t allowed =
       hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
   if (allowed != hipSuccess) return allowed;
@@ -336,10 +382,6 @@ hipError_t go_tn(const MatArg& P, const MatArg& Q, int np, int nq, int64_t rows,
 
 }  // namespace
 
-bool tile_nt_takes(const MatArg& P, const MatArg& Q, int nk) {
-  return P.type == GS_MAT_BF16 && Q.type != GS_MAT_F32 && nk % 16 == 0 && buffer_ok(P) && buffer_ok(Q);
-}
-
 hipError_t launch_tile_nt(const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, const Epilogue& e,
                           hipStream_t s) {
   // One 128 x 256 block a compute unit or two of 128 x 128: a long contraction runs better on
@@ -347,12 +389,13 @@ hipError_t launch_tile_nt(const MatArg& P, const MatArg& Q, int np, int64_t nq, 
   // 93), but two blocks hide each other's epilogue (8160 x 1024 to 4096: 110 us and 106; with
   // gelu and a kept z 138 and 118).
   const bool big = nk >= 2048 && int64_t(div_up(np, 128)) * div_up(nq, 256) >= 192;
-  if (Q.type == GS_MAT_MX8) return go_nt<GS_MAT_MX8, 4, 2>(P, Q, np, nq, nk, e, s);
-  return big ? go_nt<GS_MAT_BF16, 8, 3>(P, Q, np, nq, nk, e, s) : go_nt<GS_MAT_BF16, 4, 2>(P, Q, np, nq, nk, e, s);
-}
-
-bool tile_tn_takes(const MatArg& P, const MatArg& Q, int np, int nq) {
-  return Q.type == GS_MAT_BF16 && P.type != GS_MAT_F32 && np % 16 == 0 && nq % 16 == 0 && buffer_ok(P) && buffer_ok(Q);
+  const bool whole = nk % 16 == 0 && buffer_ok(P) && buffer_ok(Q);
+  if (Q.type == GS_MAT_MX8)
+    return whole ? go_nt<GS_MAT_MX8, 4, 2, true>(P, Q, np, nq, nk, e, s)
+                 : go_nt<GS_MAT_MX8, 4, 1, false>(P, Q, np, nq, nk, e, s);
+  if (!whole) return go_nt<GS_MAT_BF16, 4, 1, false>(P, Q, np, nq, nk, e, s);
+  return big ? go_nt<GS_MAT_BF16, 8, 3, true>(P, Q, np, nq, nk, e, s)
+             : go_nt<GS_MAT_BF16, 4, 2, true>(P, Q, np, nq, nk, e, s);
 }
 
 int tile_tn_slices(int64_t rows, int np, int nq) {
@@ -363,8 +406,12 @@ int tile_tn_slices(int64_t rows, int np, int nq) {
 
 hipError_t launch_tile_tn(const MatArg& P, const MatArg& Q, int np, int nq, int64_t rows, int slices, float* part,
                           const MatArg& out, hipStream_t s) {
-  return P.type == GS_MAT_MX8 ? go_tn<GS_MAT_MX8, 4, 4>(P, Q, np, nq, rows, slices, part, out, s)
-                              : go_tn<GS_MAT_BF16, 4, 4>(P, Q, np, nq, rows, slices, part, out, s);
+  const bool whole = np % 16 == 0 && nq % 16 == 0 && buffer_ok(P) && buffer_ok(Q);
+  if (P.type == GS_MAT_MX8)
+    return whole ? go_tn<GS_MAT_MX8, 4, 4, true>(P, Q, np, nq, rows, slices, part, out, s)
+                 : go_tn<GS_MAT_MX8, 4, 1, false>(P, Q, np, nq, rows, slices, part, out, s);
+  return whole ? go_tn<GS_MAT_BF16, 4, 4, true>(P, Q, np, nq, rows, slices, part, out, s)
+               : go_tn<GS_MAT_BF16, 4, 1, false>(P, Q, np, nq, rows, slices, part, out, s);
 }
 
 }  // namespace gsk
