@@ -17,6 +17,10 @@ struct Epilogue {
 constexpr int kAny = -1;    // a matrix type that the arguments tell
 constexpr int kNone = -2;   // no such matrix
 
+// How a kernel reaches its operands: through buffers in whole 16-column pieces, or pieces held
+// within the row or one by one (matrix.h's Raw16).
+enum Reach { kWhole, kHeldIn, kNarrow };
+
 // 16 columns of a row in MX8; the lanes 16 apart hold the two halves of a 32-column block
 // (all lanes active).  Values of absent columns are zero.
 struct Mx8x16 {

@@ -25,9 +25,10 @@ struct Piece<false> {
     a = buffer_load16(data, off + kc * 128);
     b = buffer_load16(data, off + kc * 128 + 16);
   }
-  __device__ void load_any(const MatArg& x, int64_t row, int k, int cols) {
-    a = load_raw8(x, row, k, cols - k).lo;
-    b = load_raw8(x, row, k + 8, cols - k - 8).lo;
+  template <class R>
+  __device__ void set(const R& r) {
+    a = u32x4{r.w[0], r.w[1], r.w[2], r.w[3]};
+    b = u32x4{r.w[4], r.w[5], r.w[6], r.w[7]};
   }
   __device__ void operands(bf16x8& p, bf16x8& q) const {
     p = __builtin_bit_cast(bf16x8, a);
@@ -43,10 +44,10 @@ struct Piece<true> {
     a = buffer_load16(data, off + kc * 64);
     scale = buffer_load1(scales, soff + kc * 2);
   }
-  __device__ void load_any(const MatArg& x, int64_t row, int k, int cols) {
-    const Raw8 lo = load_raw8(x, row, k, cols - k), hi = load_raw8(x, row, k + 8, cols - k - 8);
-    a = u32x4{lo.lo[0], lo.lo[1], hi.lo[0], hi.lo[1]};
-    scale = lo.scale;
+  template <class R>
+  __device__ void set(const R& r) {
+    a = u32x4{r.w[0], r.w[1], r.w[2], r.w[3]};
+    scale = r.scale;
   }
   __device__ void operands(bf16x8& p, bf16x8& q) const {
     const float s = mx8_scale(scale);
@@ -258,10 +259,11 @@ __global__ void __launch_bounds__(S::kThreads, S::kWaves) rows_fwd_kernel(RowsAr
   }
 }
 
-// Any width, alignment and types: the same products with loads and stores piece by piece.
+// Any width, alignment and types: the same products, the pieces moved into place and the
+// stores piece by piece.
 constexpr int kAnyThreads = 256;
 
-template <int KC, bool MX>
+template <int KC, bool MX, bool NARROW>
 __global__ void __launch_bounds__(kAnyThreads) rows_fwd_any_kernel(RowsArgs a, int groups) {
   extern __shared__ __align__(16) uint8_t lds[];
   float* bl = reinterpret_cast<float*>(lds + size_t(groups) * KC * 8192);
@@ -271,14 +273,26 @@ __global__ void __launch_bounds__(kAnyThreads) rows_fwd_any_kernel(RowsArgs a, i
   __syncthreads();
   const int lane = threadIdx.x % 64, g = lane / 16, r = lane % 16;
   const int64_t step = int64_t(gridDim.x) * (kAnyThreads / 64) * 16;
-  for (int64_t row0 = (int64_t(blockIdx.x) * (kAnyThreads / 64) + threadIdx.x / 64) * 16; row0 < a.rows; row0 += step) {
+  int64_t row0 = (int64_t(blockIdx.x) * (kAnyThreads / 64) + threadIdx.x / 64) * 16;
+  Raw16<MX ? GS_MAT_MX8 : GS_MAT_BF16, NARROW> next[KC];
+  auto fetch = [&](int64_t from) {
+    const int64_t row = from + r;
+#pragma unroll
+    for (int kc = 0; kc < KC; ++kc)
+      next[kc].load(a.x, row < a.rows ? row : a.rows - 1, kc * 64 + g * 16, a.k, row < a.rows);
+  };
+  fetch(row0);
+  for (; row0 < a.rows; row0 += step) {
     const int64_t row = row0 + r;
-    Piece<MX> piece[KC];
     bf16x8 xf[1][KC][2];
 #pragma unroll
-    for (int kc = 0; kc < KC; ++kc) piece[kc].load_any(a.x, row, kc * 64 + g * 16, row < a.rows ? a.k : 0);
-#pragma unroll
-    for (int kc = 0; kc < KC; ++kc) piece[kc].operands(xf[0][kc][0], xf[0][kc][1]);
+    for (int kc = 0; kc < KC; ++kc) {
+      Piece<MX> piece;
+      next[kc].settle();
+      piece.set(next[kc]);
+      piece.operands(xf[0][kc][0], xf[0][kc][1]);
+    }
+    fetch(row0 + step);
     for (int c = 0; c < nc; ++c) {
       f32x4 acc[1][4];
       products<KC, 1, false>(lds, bl, c, lane, xf, acc);
@@ -336,10 +350,10 @@ hipError_t by_columns(const RowsArgs& a, hipStream_t s) {
   return groups <= 2 ? by_input<KC, 2>(a, s) : by_input<KC, 4>(a, s);
 }
 
-template <int KC, bool MX>
+template <int KC, bool MX, bool NARROW>
 hipError_t go_any(const RowsArgs& a, hipStream_t s) {
   static const hipError_t allowed =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(&rows_fwd_any_kernel<KC, MX>),
+      hipFuncSetAttribute(reinterpret_cast<const void*>(&rows_fwd_any_kernel<KC, MX, NARROW>),
                           hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLds);
   if (allowed != hipSuccess) return allowed;
   const int all = (a.n + 63) / 64;
@@ -347,7 +361,7 @@ hipError_t go_any(const RowsArgs& a, hipStream_t s) {
   const int split = split_for(turns, all), groups = (all + split - 1) / split;
   const size_t lds = size_t(groups) * (KC * 8192 + 256);
   GSK_PROF("linear_rows_fwd_any", s);
-  rows_fwd_any_kernel<KC, MX>
+  rows_fwd_any_kernel<KC, MX, NARROW>
       <<<dim3(unsigned(blocks_for(turns, lds, 4)), split), kAnyThreads, lds, s>>>(a, groups);
   return hipGetLastError();
 }
@@ -370,10 +384,11 @@ hipError_t launch_rows_fwd(const MatArg& x, const MatArg& w, const Epilogue& e, 
   const RowsArgs a{x, w, e, rows, k, n};
   const bool mx = x.type == GS_MAT_MX8;
   if (fast(a)) return k <= 64 ? by_columns<1>(a, s) : k <= 128 ? by_columns<2>(a, s) : by_columns<4>(a, s);
+  if (k < 16) return mx ? go_any<1, true, true>(a, s) : go_any<1, false, true>(a, s);
   switch ((k + 63) / 64) {
-    case 1: return mx ? go_any<1, true>(a, s) : go_any<1, false>(a, s);
-    case 2: return mx ? go_any<2, true>(a, s) : go_any<2, false>(a, s);
-    default: return mx ? go_any<4, true>(a, s) : go_any<4, false>(a, s);
+    case 1: return mx ? go_any<1, true, false>(a, s) : go_any<1, false, false>(a, s);
+    case 2: return mx ? go_any<2, true, false>(a, s) : go_any<2, false, false>(a, s);
+    default: return mx ? go_any<4, true, false>(a, s) : go_any<4, false, false>(a, s);
   }
 }
 

@@ -22,24 +22,49 @@ constexpr int kRows = 128;
 // 16 columns of a row as loaded, of any type.
 struct Piece {
   u32x4 v[4];
-  uint32_t scale;
+  uint32_t scale, skip;
 };
 
-// Columns col .. col + 15 of a row of any matrix (cols: 0 for an absent row).
-__device__ inline void load_piece_any(Piece& p, const MatArg& m, int64_t row, int col, int cols) {
-  const Raw8 lo = load_raw8(m, row, col, cols - col), hi = load_raw8(m, row, col + 8, cols - col - 8);
-  p.scale = lo.scale;
-  if (m.type == GS_MAT_MX8) {
-    p.v[0] = u32x4{lo.lo[0], lo.lo[1], hi.lo[0], hi.lo[1]};
-  } else if (m.type == GS_MAT_BF16) {
-    p.v[0] = lo.lo;
-    p.v[1] = hi.lo;
-  } else {
-    p.v[0] = lo.lo;
-    p.v[1] = lo.hi;
-    p.v[2] = hi.lo;
-    p.v[3] = hi.hi;
-  }
+// Columns col .. col + 15 of a row of any matrix, as matrix.h's Raw16 holds them until they
+// are settled.
+template <int TYPE, bool NARROW>
+__device__ inline void load_piece_as(Piece& p, const MatArg& m, int64_t row, int col, int cols, bool live) {
+  Raw16<TYPE, NARROW> r;
+  r.load(m, row, col, cols, live);
+#pragma unroll
+  for (int i = 0; i < r.kWords; ++i) p.v[i / 4][i % 4] = r.w[i];
+  p.scale = TYPE == GS_MAT_MX8 ? r.scale : 0;
+  p.skip = r.skip;
+}
+
+template <bool NARROW>
+__device__ inline void load_piece_any(Piece& p, const MatArg& m, int64_t row, int col, int cols, bool live) {
+  if (m.type == GS_MAT_MX8)
+    load_piece_as<GS_MAT_MX8, NARROW>(p, m, row, col, cols, live);
+  else if (m.type == GS_MAT_BF16)
+    load_piece_as<GS_MAT_BF16, NARROW>(p, m, row, col, cols, live);
+  else
+    load_piece_as<GS_MAT_F32, NARROW>(p, m, row, col, cols, live);
+}
+
+template <int TYPE>
+__device__ inline void settle_piece_as(Piece& p) {
+  Raw16<TYPE, false> r;
+#pragma unroll
+  for (int i = 0; i < r.kWords; ++i) r.w[i] = p.v[i / 4][i % 4];
+  r.skip = p.skip;
+  r.settle();
+#pragma unroll
+  for (int i = 0; i < r.kWords; ++i) p.v[i / 4][i % 4] = r.w[i];
+}
+
+__device__ inline void settle_piece(Piece& p, int type) {
+  if (type == GS_MAT_MX8)
+    settle_piece_as<GS_MAT_MX8>(p);
+  else if (type == GS_MAT_BF16)
+    settle_piece_as<GS_MAT_BF16>(p);
+  else
+    settle_piece_as<GS_MAT_F32>(p);
 }
 
 // The pieces of a lane's row through buffers: rows row0 + row, columns 64 c + 16 g.
@@ -118,12 +143,14 @@ struct Share {
   static constexpr int kQT = NC * KC == 4 ? 2 : 1, kWP = KC, kWQ = NC * 4 / kQT, kMS = 8 / (kWP * kWQ);
 };
 
+constexpr int kAnyNarrow = -3;   // as kAny, a width being below 16
+
 // NC, KC: groups of 64 columns of dz and of x.  DY, Z, X: the types of dy, z (GS_MAT_F32: no
-// activation) and x, widths being multiples of 16; or all kAny.
+// activation) and x, widths being multiples of 16; or all kAny or kAnyNarrow.
 template <int NC, int KC, int DY, int Z, int X>
 __global__ void __launch_bounds__(kThreads) rows_bwd_kernel(RowsBwdArgs a) {
   using S = Share<NC, KC>;
-  constexpr bool kWhole = DY != kAny;
+  constexpr bool kWhole = DY >= 0, kFew = DY == kAnyNarrow;
   const int dyt = kWhole ? DY : a.dy.type, zt_ = kWhole ? Z : a.z.type, xt_ = kWhole ? X : a.x.type;
   const int act = Z == GS_MAT_F32 ? GS_ACT_NONE : a.act;
   constexpr int kPitchQ = NC * 128 + 32, kPitchP = KC * 128 + 32;
@@ -165,13 +192,15 @@ __global__ void __launch_bounds__(kThreads) rows_bwd_kernel(RowsBwdArgs a) {
       if constexpr (Z != GS_MAT_F32) load_pieces<Z>(z, a.z, row0, row, in, g, a.n);
       load_pieces<X>(x, a.x, row0, row, in, g, a.k);
     } else {
+      const int64_t at = in ? row0 + row : a.rows - 1;
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        load_piece_any(dy[c], a.dy, row0 + row, c * 64 + g * 16, in ? a.n : 0);
-        if (act != GS_ACT_NONE) load_piece_any(z[c], a.z, row0 + row, c * 64 + g * 16, in ? a.n : 0);
+      for (int c = 0; c < NC; ++c) load_piece_any<kFew>(dy[c], a.dy, at, c * 64 + g * 16, a.n, in);
+      if (act != GS_ACT_NONE) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) load_piece_any<kFew>(z[c], a.z, at, c * 64 + g * 16, a.n, in);
       }
 #pragma unroll
-      for (int c = 0; c < KC; ++c) load_piece_any(x[c], a.x, row0 + row, c * 64 + g * 16, in ? a.k : 0);
+      for (int c = 0; c < KC; ++c) load_piece_any<kFew>(x[c], a.x, at, c * 64 + g * 16, a.k, in);
     }
   };
   u32x4 dz[NC][2], xb[KC][2];
@@ -179,9 +208,11 @@ __global__ void __launch_bounds__(kThreads) rows_bwd_kernel(RowsBwdArgs a) {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       float v[16];
+      if constexpr (!kWhole) settle_piece(dy[c], dyt);
       piece_to_float(dy[c], dyt, v);
       if (act != GS_ACT_NONE) {
         float t[16];
+        if constexpr (!kWhole) settle_piece(z[c], zt_);
         piece_to_float(z[c], zt_, t);
         if (act == GS_ACT_SILU) {
 #pragma unroll
@@ -200,11 +231,16 @@ __global__ void __launch_bounds__(kThreads) rows_bwd_kernel(RowsBwdArgs a) {
       for (int i = 0; i < 8; ++i) dz[c][i / 4][i % 4] = pack_bf16(v[2 * i], v[2 * i + 1]);
     }
 #pragma unroll
-    for (int c = 0; c < KC; ++c) piece_to_bf16(x[c], xt_, xb[c][0], xb[c][1]);
+    for (int c = 0; c < KC; ++c) {
+      if constexpr (!kWhole) settle_piece(x[c], xt_);
+      piece_to_bf16(x[c], xt_, xb[c][0], xb[c][1]);
+    }
   };
   const int turns = int((a.rows + kRows - 1) / kRows);
-  fetch(blockIdx.x);
-  convert();
+  if (int64_t(blockIdx.x) < turns) {
+    fetch(blockIdx.x);
+    convert();
+  }
   for (int turn = blockIdx.x; turn < turns; turn += gridDim.x) {
     lds_barrier();   // the last turn's readers are done (and, at first, W^T is written)
 #pragma unroll
@@ -357,7 +393,8 @@ template <int NC, int KC>
 hipError_t by_type(const RowsBwdArgs& a, int blocks, hipStream_t s) {
   if (a.k % 16 || a.n % 16 || (a.act != GS_ACT_NONE && a.z.type == GS_MAT_F32) || !buffer_ok(a.dy) ||
       !buffer_ok(a.x) || !buffer_ok(a.dx) || (a.act != GS_ACT_NONE && !buffer_ok(a.z)))
-    return go<NC, KC, kAny, kAny, kAny>(a, blocks, s);
+    return a.k < 16 || a.n < 16 ? go<NC, KC, kAnyNarrow, kAnyNarrow, kAnyNarrow>(a, blocks, s)
+                                : go<NC, KC, kAny, kAny, kAny>(a, blocks, s);
   return a.dy.type == GS_MAT_F32 ? by_z<NC, KC, GS_MAT_F32>(a, blocks, s) : by_z<NC, KC, GS_MAT_BF16>(a, blocks, s);
 }
 

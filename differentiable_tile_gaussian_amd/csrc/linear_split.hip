@@ -13,14 +13,14 @@ struct Operands {
   bf16x8 a, b;
 };
 
-// As loaded: bfloat16 (two words) or MX8 (one, and the scale).  WHOLE: nk is a multiple of 16
+// As loaded: bfloat16 (two words) or MX8 (one, and the scale).  kWhole: nk is a multiple of 16
 // and the matrix in buffers' reach.
-template <int TYPE, bool WHOLE>
+template <int TYPE, Reach HOW>
 struct Share {
   u32x4 a, b;
-  uint32_t scale;
+  uint32_t scale, skip;
   __device__ void load(const MatArg& m, Buffer data, Buffer scales, int64_t row0, int row, bool in, int k, int nk) {
-    if constexpr (WHOLE) {
+    if constexpr (HOW == kWhole) {
       const bool there = in && k < nk;
       const uint32_t off = there ? (row * uint32_t(m.ld) + k) * element_bytes(TYPE) : kAbsent;
       a = buffer_load16(data, off);
@@ -29,15 +29,23 @@ struct Share {
       else
         b = buffer_load16(data, off + 16);
     } else {
-      const int n = in ? nk - k : 0;
-      const Raw8 lo = load_raw8(m, row0 + row, k, n), hi = load_raw8(m, row0 + row, k + 8, n - 8);
-      scale = lo.scale;
-      if constexpr (TYPE == GS_MAT_MX8) {
-        a = u32x4{lo.lo[0], lo.lo[1], hi.lo[0], hi.lo[1]};
-      } else {
-        a = lo.lo;
-        b = hi.lo;
-      }
+      Raw16<TYPE, HOW == kNarrow> r;
+      r.load(m, in ? row0 + row : row0, k, nk, in);
+      a = u32x4{r.w[0], r.w[1], r.w[2], r.w[3]};
+      if constexpr (TYPE != GS_MAT_MX8) b = u32x4{r.w[4], r.w[5], r.w[6], r.w[7]};
+      scale = TYPE == GS_MAT_MX8 ? r.scale : 0;
+      skip = r.skip;
+    }
+  }
+  __device__ void settle() {
+    if constexpr (HOW != kWhole) {
+      Raw16<TYPE, false> r;
+#pragma unroll
+      for (int i = 0; i < r.kWords; ++i) r.w[i] = i < 4 ? a[i] : b[i % 4];
+      r.skip = skip;
+      r.settle();
+      a = u32x4{r.w[0], r.w[1], r.w[2], r.w[3]};
+      if constexpr (TYPE != GS_MAT_MX8) b = u32x4{r.w[4], r.w[5], r.w[6], r.w[7]};
     }
   }
   __device__ Operands operands() const {
@@ -57,7 +65,7 @@ struct Share {
 __host__ __device__ constexpr int waves_for(int qt) { return qt == 4 ? 4 : 8; }
 
 // out(q, p) = sum_k Q(q, k) P(p, k), P bfloat16, Q bfloat16 or MX8.
-template <int QTYPE, int QT, bool WHOLE>
+template <int QTYPE, int QT, Reach HOW>
 __global__ void __launch_bounds__(waves_for(QT) * 64) split_nt_kernel(MatArg P, MatArg Q, int np, int64_t nq, int nk, Epilogue e) {
   constexpr int kWaves = waves_for(QT);
   extern __shared__ __align__(16) uint8_t lds[];
@@ -68,8 +76,8 @@ __global__ void __launch_bounds__(waves_for(QT) * 64) split_nt_kernel(MatArg P, 
   const int64_t q0 = int64_t(blockIdx.x) * (16 * QT);
   const Buffer pb = buffer_at(P.p + int64_t(p0) * P.ld * 2), qb = buffer_at(Q.p + q0 * Q.ld * element_bytes(QTYPE));
   const Buffer sb = buffer_at(QTYPE == GS_MAT_MX8 ? Q.s + q0 * Q.lds : nullptr);
-  Share<GS_MAT_BF16, WHOLE> ps[4];
-  Share<QTYPE, WHOLE> qs[QT];
+  Share<GS_MAT_BF16, HOW> ps[4];
+  Share<QTYPE, HOW> qs[QT];
   auto fetch = [&](int step) {
     const int k = step * 64 + g * 16;
 #pragma unroll
@@ -90,9 +98,15 @@ __global__ void __launch_bounds__(waves_for(QT) * 64) split_nt_kernel(MatArg P, 
   for (int s = wave; s < steps; s += kWaves) {
     Operands po[4], qo[QT];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) po[t] = ps[t].operands();
+    for (int t = 0; t < 4; ++t) {
+      ps[t].settle();
+      po[t] = ps[t].operands();
+    }
 #pragma unroll
-    for (int i = 0; i < QT; ++i) qo[i] = qs[i].operands();
+    for (int i = 0; i < QT; ++i) {
+      qs[i].settle();
+      qo[i] = qs[i].operands();
+    }
     fetch(s + kWaves);   // past the end: all absent
 #pragma unroll
     for (int i = 0; i < QT; ++i)
@@ -123,19 +137,19 @@ __global__ void __launch_bounds__(waves_for(QT) * 64) split_nt_kernel(MatArg P, 
   finish16<false, kAny, kAny>(e, row, col, v, row < nq ? n : 0);
 }
 
-template <int QTYPE, int QT, bool WHOLE>
+template <int QTYPE, int QT, Reach HOW>
 hipError_t go(const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, const Epilogue& e, hipStream_t s) {
   constexpr int kWaves = waves_for(QT), kLds = kWaves * QT * 4096;
-  split_nt_kernel<QTYPE, QT, WHOLE>
+  split_nt_kernel<QTYPE, QT, HOW>
       <<<dim3(div_up(nq, 16 * QT), div_up(np, 64)), kWaves * 64, kLds, s>>>(P, Q, np, nq, nk, e);
   return hipGetLastError();
 }
 
-template <int QTYPE, bool WHOLE>
+template <int QTYPE, Reach HOW>
 hipError_t by_rows(const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, const Epilogue& e, hipStream_t s) {
-  return nq <= 16   ? go<QTYPE, 1, WHOLE>(P, Q, np, nq, nk, e, s)
-         : nq <= 32 ? go<QTYPE, 2, WHOLE>(P, Q, np, nq, nk, e, s)
-                    : go<QTYPE, 4, WHOLE>(P, Q, np, nq, nk, e, s);
+  return nq <= 16   ? go<QTYPE, 1, HOW>(P, Q, np, nq, nk, e, s)
+         : nq <= 32 ? go<QTYPE, 2, HOW>(P, Q, np, nq, nk, e, s)
+                    : go<QTYPE, 4, HOW>(P, Q, np, nq, nk, e, s);
 }
 
 }  // namespace
@@ -146,10 +160,14 @@ bool split_nt_takes(const MatArg& P, const MatArg& Q, int np, int64_t nq) {
 
 hipError_t launch_split_nt(const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, const Epilogue& e,
                            hipStream_t s) {
-  const bool whole = nk % 16 == 0 && buffer_ok(P) && buffer_ok(Q);
+  const Reach how = nk < 16 ? kNarrow : nk % 16 == 0 && buffer_ok(P) && buffer_ok(Q) ? kWhole : kHeldIn;
   if (Q.type == GS_MAT_MX8)
-    return whole ? by_rows<GS_MAT_MX8, true>(P, Q, np, nq, nk, e, s) : by_rows<GS_MAT_MX8, false>(P, Q, np, nq, nk, e, s);
-  return whole ? by_rows<GS_MAT_BF16, true>(P, Q, np, nq, nk, e, s) : by_rows<GS_MAT_BF16, false>(P, Q, np, nq, nk, e, s);
+    return how == kWhole    ? by_rows<GS_MAT_MX8, kWhole>(P, Q, np, nq, nk, e, s)
+           : how == kHeldIn ? by_rows<GS_MAT_MX8, kHeldIn>(P, Q, np, nq, nk, e, s)
+                            : by_rows<GS_MAT_MX8, kNarrow>(P, Q, np, nq, nk, e, s);
+  return how == kWhole    ? by_rows<GS_MAT_BF16, kWhole>(P, Q, np, nq, nk, e, s)
+         : how == kHeldIn ? by_rows<GS_MAT_BF16, kHeldIn>(P, Q, np, nq, nk, e, s)
+                          : by_rows<GS_MAT_BF16, kNarrow>(P, Q, np, nq, nk, e, s);
 }
 
 }  // namespace gsk

@@ -60,16 +60,25 @@ struct Unit {
     else
       b = buffer_load16(data, off + 16);
   }
-  // n: columns of the 16 that exist.
-  __device__ void load_any(const MatArg& m, int64_t row, int col, int n) {
-    const Raw8 lo = load_raw8(m, row, col, n), hi = load_raw8(m, row, col + 8, n - 8);
-    scale = lo.scale;
-    if constexpr (TYPE == GS_MAT_MX8) {
-      a = u32x4{lo.lo[0], lo.lo[1], hi.lo[0], hi.lo[1]};
-    } else {
-      a = lo.lo;
-      b = hi.lo;
-    }
+  // Any width and alignment (matrix.h): to be settled before its use.
+  uint32_t skip;
+  template <bool NARROW>
+  __device__ void load_any(const MatArg& m, int64_t row, int col, int cols, bool live) {
+    Raw16<TYPE, NARROW> r;
+    r.load(m, row, col, cols, live);
+    a = u32x4{r.w[0], r.w[1], r.w[2], r.w[3]};
+    if constexpr (TYPE != GS_MAT_MX8) b = u32x4{r.w[4], r.w[5], r.w[6], r.w[7]};
+    scale = TYPE == GS_MAT_MX8 ? r.scale : 0;
+    skip = r.skip;
+  }
+  __device__ void settle() {
+    Raw16<TYPE, false> r;
+#pragma unroll
+    for (int i = 0; i < r.kWords; ++i) r.w[i] = i < 4 ? a[i] : b[i % 4];
+    r.skip = skip;
+    r.settle();
+    a = u32x4{r.w[0], r.w[1], r.w[2], r.w[3]};
+    if constexpr (TYPE != GS_MAT_MX8) b = u32x4{r.w[4], r.w[5], r.w[6], r.w[7]};
   }
   __device__ void operands(u32x4& p, u32x4& q) const {
     if constexpr (TYPE == GS_MAT_MX8) {
@@ -88,12 +97,13 @@ struct Unit {
 // ------------------------------------------------- contraction contiguous in both operands
 
 // out(q, p) = sum_k Q(q, k) P(p, k) for the rows q of Q (bfloat16 or MX8) and p of P
-// (bfloat16).  WHOLE: nk is a multiple of 16 and both are in buffers' reach.  An LDS row is 64 k, 128 bytes, whose 16-byte pieces are
+// (bfloat16).  kWhole: nk is a multiple of 16 and both are in buffers' reach.  An LDS row is 64 k, 128 bytes, whose 16-byte pieces are
 // permuted by the row's number so that a fragment read's 16 rows fall into different banks;
 // P's rows are stored so that a lane's four result tiles are 16 consecutive columns.
-template <int QTYPE, int QT, int D, bool WHOLE>
+template <int QTYPE, int QT, int D, Reach HOW>
 __global__ void __launch_bounds__(kThreads) tile_nt_kernel(MatArg P, MatArg Q, int np, int64_t nq, int nk, Epilogue e,
                                                             int ptiles, int tiles) {
+  constexpr bool WHOLE = HOW == kWhole, kFew = HOW == kNarrow;
   constexpr int BP = 128, BQ = 32 * QT, kStep = (BP + BQ) * 128;
   extern __shared__ __align__(16) uint8_t lds[];
   const int tile = tile_of(blockIdx.x, tiles);
@@ -123,11 +133,15 @@ __global__ void __launch_bounds__(kThreads) tile_nt_kernel(MatArg P, MatArg Q, i
     if constexpr (!WHOLE) {
       const int k = k0 + piece * 16;
 #pragma unroll
-      for (int u = 0; u < BP / 64; ++u)
-        pr[d][u].load_any(P, p0 + u * 64 + row, k, p0 + u * 64 + row < np ? nk - k : 0);
+      for (int u = 0; u < BP / 64; ++u) {
+        const int at = p0 + u * 64 + row;
+        pr[d][u].template load_any<kFew>(P, at < np ? at : np - 1, k, nk, at < np);
+      }
 #pragma unroll
-      for (int u = 0; u < BQ / 64; ++u)
-        qr[d][u].load_any(Q, q0 + u * 64 + row, k, q0 + u * 64 + row < nq ? nk - k : 0);
+      for (int u = 0; u < BQ / 64; ++u) {
+        const int64_t at = q0 + u * 64 + row;
+        qr[d][u].template load_any<kFew>(Q, at < nq ? at : nq - 1, k, nk, at < nq);
+      }
       return;
     }
 #pragma unroll
@@ -146,11 +160,13 @@ __global__ void __launch_bounds__(kThreads) tile_nt_kernel(MatArg P, MatArg Q, i
 #pragma unroll
     for (int u = 0; u < BP / 64; ++u) {
       const int r = u * 64 + row;
+      if constexpr (!WHOLE) pr[d][u].settle();
       pr[d][u].operands(a, b);
       put(at, (r & ~63) | ((r & 12) << 2) | ((r & 48) >> 2) | (r & 3), a, b);
     }
 #pragma unroll
     for (int u = 0; u < BQ / 64; ++u) {
+      if constexpr (!WHOLE) qr[d][u].settle();
       qr[d][u].operands(a, b);
       put(at + BP * 128, u * 64 + row, a, b);
     }
@@ -214,22 +230,25 @@ __global__ void __launch_bounds__(kThreads) tile_nt_kernel(MatArg P, MatArg Q, i
 // ------------------------------------------------- contraction over the operands' rows
 
 // out(q, p) = sum_m Q(m, q) P(m, p) for m in the block's slice: the weight's gradient (Q =
-// dz, bfloat16; P = x, bfloat16 or MX8).  WHOLE: np and nq are multiples of 16 and both
-// matrices in buffers' reach.  LDS holds 64 rows m
+// dz, bfloat16; P = x, bfloat16 or MX8).  kWhole: np and nq are multiples of 16 and
+// both matrices in buffers' reach.  LDS holds 64 rows m
 // as they are in memory (plus 32 bytes a row, so that eight rows fall into different banks),
 // read transposed.
-template <int PTYPE, int QT, int D, bool WHOLE>
+template <int PTYPE, int QT, int D, Reach HOW>
 __global__ void __launch_bounds__(kThreads) tile_tn_kernel(MatArg P, MatArg Q, int np, int nq, int64_t rows,
                                                             int64_t per_slice, float* part, MatArg out, int ptiles,
-                                                            int tiles) {
+                                                            int tiles, int slices) {
+  constexpr bool WHOLE = HOW == kWhole, kFew = HOW == kNarrow;
   constexpr int BP = 128, BQ = 32 * QT, kPitchP = BP * 2 + 32, kPitchQ = BQ * 2 + 32;
   constexpr int kStep = 64 * (kPitchP + kPitchQ), kUP = BP / 64, kUQ = BQ / 64;
   extern __shared__ __align__(16) uint8_t lds[];
-  const int tile = tile_of(blockIdx.x, tiles);
-  if (tile >= tiles) return;
+  // an XCD is given all the tiles of a slice, which share its rows; a few slices: neighbouring tiles
+  const int slice = slices < 8 ? blockIdx.x / ((tiles + 7) / 8 * 8) : blockIdx.x / 8 / tiles * 8 + blockIdx.x % 8;
+  const int tile = slices < 8 ? tile_of(blockIdx.x % ((tiles + 7) / 8 * 8), tiles) : blockIdx.x / 8 % tiles;
+  if (tile >= tiles || slice >= slices) return;
   const int p0 = tile % ptiles * BP, q0 = tile / ptiles * BQ;
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, wp = wave % 2, wq = wave / 2;
-  const int64_t first = int64_t(blockIdx.y) * per_slice;
+  const int64_t first = int64_t(slice) * per_slice;
   const int64_t last = first + per_slice < rows ? first + per_slice : rows;
   // a thread stages 16 columns of kUP + kUQ row pieces: P's rows hold BP / 16 of them, Q's BQ / 16
   constexpr uint32_t kP = element_bytes(PTYPE);
@@ -245,12 +264,14 @@ __global__ void __launch_bounds__(kThreads) tile_tn_kernel(MatArg P, MatArg Q, i
 #pragma unroll
       for (int u = 0; u < kUP; ++u) {
         const int m = pm + u * (kThreads * 16 / BP);
-        pr[d][u].load_any(P, m0 + m, p0 + pc, m < left ? np - p0 - pc : 0);
+        const int64_t at = m0 + m < rows ? m0 + m : rows - 1;
+        pr[d][u].template load_any<kFew>(P, at, p0 + pc, np, m < left);
       }
 #pragma unroll
       for (int u = 0; u < kUQ; ++u) {
         const int m = qm + u * (kThreads * 16 / BQ);
-        qr[d][u].load_any(Q, m0 + m, q0 + qc, m < left ? nq - q0 - qc : 0);
+        const int64_t at = m0 + m < rows ? m0 + m : rows - 1;
+        qr[d][u].template load_any<kFew>(Q, at, q0 + qc, nq, m < left);
       }
       return;
     }
@@ -271,6 +292,7 @@ __global__ void __launch_bounds__(kThreads) tile_tn_kernel(MatArg P, MatArg Q, i
 #pragma unroll
     for (int u = 0; u < kUP; ++u) {
       uint8_t* o = at + (pm + u * (kThreads * 16 / BP)) * kPitchP + pc * 2;
+      if constexpr (!WHOLE) pr[d][u].settle();
       pr[d][u].operands(a, b);
       *reinterpret_cast<u32x4*>(o) = a;
       *reinterpret_cast<u32x4*>(o + 16) = b;
@@ -278,6 +300,7 @@ __global__ void __launch_bounds__(kThreads) tile_tn_kernel(MatArg P, MatArg Q, i
 #pragma unroll
     for (int u = 0; u < kUQ; ++u) {
       uint8_t* o = at + 64 * kPitchP + (qm + u * (kThreads * 16 / BQ)) * kPitchQ + qc * 2;
+      if constexpr (!WHOLE) qr[d][u].settle();
       qr[d][u].operands(a, b);
       *reinterpret_cast<u32x4*>(o) = a;
       *reinterpret_cast<u32x4*>(o + 16) = b;
@@ -290,11 +313,13 @@ __global__ void __launch_bounds__(kThreads) tile_tn_kernel(MatArg P, MatArg Q, i
     for (int t = 0; t < 4; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
   const int m = lane / 16 * 8 + lane % 16 / 4, c = lane % 4 * 4;
   const int pat = m * kPitchP + (wp * 64 + c) * 2, qat = 64 * kPitchP + m * kPitchQ + (wq * QT * 16 + c) * 2;
-  fetch(0, first);
-  stage(0, lds);
-#pragma unroll
-  for (int d = 0; d < D; ++d) fetch(d, first + (d + 1) * 64);
   const int steps = last > first ? int((last - first + 63) / 64) : 0;
+  if (steps > 0) {
+    fetch(0, first);
+    stage(0, lds);
+#pragma unroll
+    for (int d = 0; d < D; ++d) fetch(d, first + (d + 1) * 64);
+  }
   for (int s0 = 0; s0 < steps; s0 += D) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
@@ -333,7 +358,7 @@ __global__ void __launch_bounds__(kThreads) tile_tn_kernel(MatArg P, MatArg Q, i
       if (!WHOLE && p + 4 > np) {   // the last columns of an odd width
         for (int j = 0; p + j < np; ++j) {
           if (part)
-            part[(int64_t(blockIdx.y) * nq + q) * np + p + j] = v[j];
+            part[(int64_t(slice) * nq + q) * np + p + j] = v[j];
           else if (out.type == GS_MAT_F32)
             reinterpret_cast<float*>(out.p)[int64_t(q) * out.ld + p + j] = v[j];
           else
@@ -342,7 +367,7 @@ __global__ void __launch_bounds__(kThreads) tile_tn_kernel(MatArg P, MatArg Q, i
         continue;
       }
       if (part) {
-        __builtin_memcpy(__builtin_assume_aligned(part + (int64_t(blockIdx.y) * nq + q) * np + p, 4), &v, 16);
+        __builtin_memcpy(__builtin_assume_aligned(part + (int64_t(slice) * nq + q) * np + p, 4), &v, 16);
       } else if (out.type == GS_MAT_F32) {
         __builtin_memcpy(__builtin_assume_aligned(reinterpret_cast<float*>(out.p) + int64_t(q) * out.ld + p, 4), &v, 16);
       } else {
@@ -353,10 +378,10 @@ __global__ void __launch_bounds__(kThreads) tile_tn_kernel(MatArg P, MatArg Q, i
   }
 }
 
-template <int QTYPE, int QT, int D, bool WHOLE>
+template <int QTYPE, int QT, int D, Reach HOW>
 hipError_t go_nt(const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, const Epilogue& e, hipStream_t s) {
   constexpr int kLds = 2 * (128 + 32 * QT) * 128;
-  const auto kernel = &tile_nt_kernel<QTYPE, QT, D, WHOLE>;
+  const auto kernel = &tile_nt_kernel<QTYPE, QT, D, HOW>;
   static const hipError_t allowed =
       hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
   if (allowed != hipSuccess) return allowed;
@@ -365,18 +390,18 @@ hipError_t go_nt(const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, c
   return hipGetLastError();
 }
 
-template <int PTYPE, int QT, int D, bool WHOLE>
+template <int PTYPE, int QT, int D, Reach HOW>
 hipError_t go_tn(const MatArg& P, const MatArg& Q, int np, int nq, int64_t rows, int slices, float* part,
                  const MatArg& out, hipStream_t s) {
   constexpr int kLds = 2 * 64 * (128 * 2 + 32 + 32 * QT * 2 + 32);
-  const auto kernel = &tile_tn_kernel<PTYPE, QT, D, WHOLE>;
+  const auto kernel = &tile_tn_kernel<PTYPE, QT, D, HOW>;
   static const hipError_t allowed =
       hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
   if (allowed != hipSuccess) return allowed;
   const int ptiles = int(div_up(np, 128)), tiles = ptiles * int(div_up(nq, 32 * QT));
   const int64_t per = ((rows + slices - 1) / slices + 63) / 64 * 64;
-  kernel<<<dim3((tiles + 7) / 8 * 8, slices), kThreads, kLds, s>>>(P, Q, np, nq, rows, per, slices > 1 ? part : nullptr,
-                                                                  out, ptiles, tiles);
+  const unsigned blocks = unsigned(slices < 8 ? (tiles + 7) / 8 * 8 * slices : (slices + 7) / 8 * 8 * tiles);
+  kernel<<<blocks, kThreads, kLds, s>>>(P, Q, np, nq, rows, per, slices > 1 ? part : nullptr, out, ptiles, tiles, slices);
   return hipGetLastError();
 }
 
@@ -389,13 +414,15 @@ hipError_t launch_tile_nt(const MatArg& P, const MatArg& Q, int np, int64_t nq, 
   // 93), but two blocks hide each other's epilogue (8160 x 1024 to 4096: 110 us and 106; with
   // gelu and a kept z 138 and 118).
   const bool big = nk >= 2048 && int64_t(div_up(np, 128)) * div_up(nq, 256) >= 192;
-  const bool whole = nk % 16 == 0 && buffer_ok(P) && buffer_ok(Q);
+  const Reach how = nk < 16 ? kNarrow : nk % 16 == 0 && buffer_ok(P) && buffer_ok(Q) ? kWhole : kHeldIn;
   if (Q.type == GS_MAT_MX8)
-    return whole ? go_nt<GS_MAT_MX8, 4, 2, true>(P, Q, np, nq, nk, e, s)
-                 : go_nt<GS_MAT_MX8, 4, 1, false>(P, Q, np, nq, nk, e, s);
-  if (!whole) return go_nt<GS_MAT_BF16, 4, 1, false>(P, Q, np, nq, nk, e, s);
-  return big ? go_nt<GS_MAT_BF16, 8, 3, true>(P, Q, np, nq, nk, e, s)
-             : go_nt<GS_MAT_BF16, 4, 2, true>(P, Q, np, nq, nk, e, s);
+    return how == kWhole    ? go_nt<GS_MAT_MX8, 4, 2, kWhole>(P, Q, np, nq, nk, e, s)
+           : how == kHeldIn ? go_nt<GS_MAT_MX8, 4, 2, kHeldIn>(P, Q, np, nq, nk, e, s)
+                            : go_nt<GS_MAT_MX8, 4, 1, kNarrow>(P, Q, np, nq, nk, e, s);
+  if (how == kHeldIn) return go_nt<GS_MAT_BF16, 4, 2, kHeldIn>(P, Q, np, nq, nk, e, s);
+  if (how == kNarrow) return go_nt<GS_MAT_BF16, 4, 1, kNarrow>(P, Q, np, nq, nk, e, s);
+  return big ? go_nt<GS_MAT_BF16, 8, 3, kWhole>(P, Q, np, nq, nk, e, s)
+             : go_nt<GS_MAT_BF16, 4, 2, kWhole>(P, Q, np, nq, nk, e, s);
 }
 
 int tile_tn_slices(int64_t rows, int np, int nq) {
@@ -407,11 +434,14 @@ int tile_tn_slices(int64_t rows, int np, int nq) {
 hipError_t launch_tile_tn(const MatArg& P, const MatArg& Q, int np, int nq, int64_t rows, int slices, float* part,
                           const MatArg& out, hipStream_t s) {
   const bool whole = np % 16 == 0 && nq % 16 == 0 && buffer_ok(P) && buffer_ok(Q);
+  const Reach how = np < 16 || nq < 16 ? kNarrow : whole ? kWhole : kHeldIn;
   if (P.type == GS_MAT_MX8)
-    return whole ? go_tn<GS_MAT_MX8, 4, 4, true>(P, Q, np, nq, rows, slices, part, out, s)
-                 : go_tn<GS_MAT_MX8, 4, 1, false>(P, Q, np, nq, rows, slices, part, out, s);
-  return whole ? go_tn<GS_MAT_BF16, 4, 4, true>(P, Q, np, nq, rows, slices, part, out, s)
-               : go_tn<GS_MAT_BF16, 4, 1, false>(P, Q, np, nq, rows, slices, part, out, s);
+    return how == kWhole    ? go_tn<GS_MAT_MX8, 4, 4, kWhole>(P, Q, np, nq, rows, slices, part, out, s)
+           : how == kHeldIn ? go_tn<GS_MAT_MX8, 4, 2, kHeldIn>(P, Q, np, nq, rows, slices, part, out, s)
+                            : go_tn<GS_MAT_MX8, 4, 1, kNarrow>(P, Q, np, nq, rows, slices, part, out, s);
+  return how == kWhole    ? go_tn<GS_MAT_BF16, 4, 4, kWhole>(P, Q, np, nq, rows, slices, part, out, s)
+         : how == kHeldIn ? go_tn<GS_MAT_BF16, 4, 2, kHeldIn>(P, Q, np, nq, rows, slices, part, out, s)
+                          : go_tn<GS_MAT_BF16, 4, 1, kNarrow>(P, Q, np, nq, rows, slices, part, out, s);
 }
 
 }  // namespace gsk

@@ -222,6 +222,61 @@ __device__ inline void move_down(const Held& c, float v[8]) {
   }
 }
 
+// ---- 16 columns of a row of any width and alignment, without branches
+//
+// A piece that would pass the row's end is loaded from column cols - 16 instead and moved
+// down when it is used; what is behind the row's end, and an absent row, reads as zero.
+// NARROW: for rows of fewer than 16 columns, loaded one by one (a kernel of its own: the other
+// loads would wait where the two ways join).
+template <int TYPE, bool NARROW>
+struct Raw16 {
+  static constexpr int kWords = TYPE == GS_MAT_F32 ? 16 : TYPE == GS_MAT_BF16 ? 8 : 4;
+  uint32_t w[kWords];
+  uint32_t scale, skip;
+
+  // row: a row of the matrix, also where the piece is absent (live false).
+  __device__ void load(const MatArg& m, int64_t row, int col, int cols, bool live) {
+    constexpr int kE = 4 * kWords / 16;
+    if constexpr (!NARROW) {
+      const int at = col < cols - 16 ? col : cols - 16;
+      const char* p = m.p + (row * m.ld + at) * kE;
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i) {
+        u32x4 v;
+        __builtin_memcpy(&v, __builtin_assume_aligned(p + 16 * i, kE), 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[4 * i + j] = v[j];
+      }
+      if constexpr (TYPE == GS_MAT_MX8) scale = m.s[row * m.lds + ((col < cols ? col : cols - 1) >> 5)];
+      skip = live ? (col - at < 16 ? col - at : 16) : 16;
+    } else {
+      const int n = live ? cols - col : 0;
+      const Raw8 lo = load_raw8(m, row, col, n), hi = load_raw8(m, row, col + 8, n - 8);
+#pragma unroll
+      for (int i = 0; i < kWords / 2; ++i) {
+        w[i] = i < 4 ? lo.lo[i] : lo.hi[i % 4];
+        w[kWords / 2 + i] = i < 4 ? hi.lo[i] : hi.hi[i % 4];
+      }
+      scale = lo.scale;
+      skip = 0;
+    }
+  }
+  // Moves the piece's own columns to its front, zeros behind them.
+  __device__ void settle() {
+    constexpr int kE = 4 * kWords / 16;
+    const uint32_t bytes = skip * kE;
+#pragma unroll
+    for (int b = kWords; b > 0; b /= 2)
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = bytes & (4 * b) ? (i + b < kWords ? w[i + b] : 0u) : w[i];
+    if constexpr (kE < 4) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i)
+        w[i] = __builtin_amdgcn_alignbyte(i + 1 < kWords ? w[i + 1] : 0u, w[i], bytes & 3);
+    }
+  }
+};
+
 // ---- buffer access
 //
 // The row kernels' fast paths load and store through buffer descriptors, whose range check

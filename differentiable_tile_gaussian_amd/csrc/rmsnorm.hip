@@ -396,12 +396,53 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float* __restrict
   }
 }
 
+// Few parts of many entries: a thread sums 4 entries over the parts in order.
+__global__ void __launch_bounds__(kThreads) sum_few_parts_kernel(const float* __restrict__ part, int parts,
+                                                                  int64_t size, int64_t first, int64_t last,
+                                                                  int64_t split, int cols, MatArg out, float* tail) {
+  const int64_t c0 = first + (int64_t(blockIdx.x) * kThreads + threadIdx.x) * 4;
+  if (c0 >= last) return;
+  const int n = last - c0 < 4 ? int(last - c0) : 4;
+  float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (n == 4) {
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) {
+      f32x4 v;
+      __builtin_memcpy(&v, __builtin_assume_aligned(part + p * size + c0, 4), 16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t[i] += v[i];
+    }
+  } else {
+    for (int p = 0; p < parts; ++p)
+      for (int i = 0; i < n; ++i) t[i] += part[p * size + c0 + i];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t c = c0 + i;
+    if (i >= n) break;
+    if (c >= split) {
+      tail[c - split] = t[i];
+    } else {
+      const int64_t at = (c / cols) * out.ld + c % cols;
+      if (out.type == GS_MAT_F32)
+        reinterpret_cast<float*>(out.p)[at] = t[i];
+      else
+        reinterpret_cast<uint16_t*>(out.p)[at] = uint16_t(pack_bf16(t[i], 0.0f));
+    }
+  }
+}
+
 }  // namespace
 
 hipError_t launch_sum_parts(const float* part, int parts, int64_t size, int64_t split, int cols, const MatArg& out,
                             float* tail, hipStream_t s) {
   const int64_t first = out.p ? 0 : split, last = tail ? size : split;
   GSK_PROF("sum_parts", s);
+  if (parts <= 32 && last - first >= 16384) {
+    sum_few_parts_kernel<<<div_up(last - first, kThreads * 4), kThreads, 0, s>>>(part, parts, size, first, last, split,
+                                                                                cols, out, tail);
+    return hipGetLastError();
+  }
   sum_parts_kernel<<<div_up(last - first, 16), 1024, 0, s>>>(part, parts, size, first, last, split, cols, out, tail);
   return hipGetLastError();
 }
