@@ -61,16 +61,24 @@ struct Piece<true> {
 // The block's part of W (nc groups of 64 columns from group c0) as operands, 1 KiB for each
 // (column group, tile, piece, half), so that a read is 64 consecutive 16-byte words; and the
 // bias, from which the sums start.
+// held: the last 16-column piece is taken from inside the row (as matrix.h's Raw16), so that
+// its lanes compute, and write, 16 columns like all others.
 template <int KC>
 __device__ inline void stage_weight(const MatArg& w, const float* bias, int k, int n, int c0, int nc, uint8_t* wl,
-                                    float* bl) {
+                                    float* bl, bool held) {
   for (int f = threadIdx.x; f < nc * KC * 512; f += blockDim.x) {
     const int l = f % 64, frag = f / 64, half = frag % 2, kc = frag / 2 % KC, t = frag / (2 * KC) % 4;
     const int c = frag / (8 * KC);
-    const int row = (c0 + c) * 64 + l % 16 / 4 * 16 + t * 4 + l % 4, col = kc * 64 + l / 16 * 16 + half * 8;
+    int first = (c0 + c) * 64 + l % 16 / 4 * 16;
+    if (held && first > n - 16) first = n - 16;
+    const int row = first + t * 4 + l % 4, col = kc * 64 + l / 16 * 16 + half * 8;
     *reinterpret_cast<u32x4*>(wl + size_t(f) * 16) = load_raw8(w, row, col, row < n ? k - col : 0).lo;
   }
-  for (int j = threadIdx.x; j < nc * 64; j += blockDim.x) bl[j] = bias && c0 * 64 + j < n ? bias[c0 * 64 + j] : 0.0f;
+  for (int j = threadIdx.x; j < nc * 64; j += blockDim.x) {
+    int first = (c0 * 64 + j) / 16 * 16;
+    if (held && first > n - 16) first = n - 16;
+    bl[j] = bias && first + j % 16 < n ? bias[first + j % 16] : 0.0f;
+  }
 }
 
 // One column group's sums for 16 MT rows.  The weight does not change from turn to turn; the
@@ -142,7 +150,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kWaves) rows_fwd_kernel(RowsAr
   float* bl = reinterpret_cast<float*>(lds + NC * KC * 8192);
   const int c0 = blockIdx.y * NC, col0 = c0 * 64;
   const int nc = (a.n + 63) / 64 - c0 < NC ? (a.n + 63) / 64 - c0 : NC;
-  stage_weight<KC>(a.w, a.e.bias, a.k, a.n, c0, nc, lds, bl);
+  stage_weight<KC>(a.w, a.e.bias, a.k, a.n, c0, nc, lds, bl, false);
   __syncthreads();
   const int lane = threadIdx.x % 64, g = lane / 16, r = lane % 16;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -269,7 +277,8 @@ __global__ void __launch_bounds__(kAnyThreads) rows_fwd_any_kernel(RowsArgs a, i
   float* bl = reinterpret_cast<float*>(lds + size_t(groups) * KC * 8192);
   const int c0 = blockIdx.y * groups;
   const int nc = (a.n + 63) / 64 - c0 < groups ? (a.n + 63) / 64 - c0 : groups;
-  stage_weight<KC>(a.w, a.e.bias, a.k, a.n, c0, nc, lds, bl);
+  const bool held = a.n >= 16;
+  stage_weight<KC>(a.w, a.e.bias, a.k, a.n, c0, nc, lds, bl, held);
   __syncthreads();
   const int lane = threadIdx.x % 64, g = lane / 16, r = lane % 16;
   const int64_t step = int64_t(gridDim.x) * (kAnyThreads / 64) * 16;
@@ -288,7 +297,9 @@ __global__ void __launch_bounds__(kAnyThreads) rows_fwd_any_kernel(RowsArgs a, i
 #pragma unroll
     for (int kc = 0; kc < KC; ++kc) {
       Piece<MX> piece;
-      next[kc].settle();
+      // the row ends in the last group of 64, or with four groups the one before it; absent
+      // rows' results go nowhere
+      if (kc == KC - 1 || (KC == 4 && kc == 2)) next[kc].settle();
       piece.set(next[kc]);
       piece.operands(xf[0][kc][0], xf[0][kc][1]);
     }
@@ -299,8 +310,30 @@ __global__ void __launch_bounds__(kAnyThreads) rows_fwd_any_kernel(RowsArgs a, i
       float v[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = acc[0][i / 4][i % 4];
-      const int col = (c0 + c) * 64 + g * 16;
-      finish16<false, kAny, kAny>(a.e, row, col, v, row < a.rows ? (a.n - col < 16 ? a.n - col : 16) : 0);
+      const int col = (c0 + c) * 64 + g * 16, n = row < a.rows ? (a.n - col < 16 ? a.n - col : 16) : 0;
+      if (!held) {
+        finish16<false, kAny, kAny>(a.e, row, col, v, n);
+        continue;
+      }
+      const int at = col < a.n - 16 ? col : a.n - 16, skip = col - at;
+      if (a.e.z.p && a.e.z.type == GS_MAT_MX8) {
+        // a block's columns have their places: the piece's own to its front
+        float z[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) z[i] = v[i];
+#pragma unroll
+        for (int b = 8; b > 0; b /= 2)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) z[i] = skip & b ? (i + b < 16 ? z[i + b] : 0.0f) : z[i];
+        if (skip >= 16) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) z[i] = 0.0f;
+        }
+        store_mx8x16<false>(a.e.z, row, col, encode16(z), n);
+      } else if (a.e.z.p && n > 0) {
+        store16<true>(a.e.z, a.e.z.type, row, at, v, 16);
+      }
+      finish16<true, kNone, kAny>(a.e, row, at, v, n > 0 ? 16 : 0);
     }
   }
 }

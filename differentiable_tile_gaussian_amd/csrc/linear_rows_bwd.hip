@@ -37,34 +37,40 @@ __device__ inline void load_piece_as(Piece& p, const MatArg& m, int64_t row, int
   p.skip = r.skip;
 }
 
-template <bool NARROW>
+template <int TYPE, bool NARROW>
 __device__ inline void load_piece_any(Piece& p, const MatArg& m, int64_t row, int col, int cols, bool live) {
-  if (m.type == GS_MAT_MX8)
+  if (TYPE == GS_MAT_MX8 || (TYPE == kAny && m.type == GS_MAT_MX8))
     load_piece_as<GS_MAT_MX8, NARROW>(p, m, row, col, cols, live);
-  else if (m.type == GS_MAT_BF16)
+  else if (TYPE == GS_MAT_BF16 || (TYPE == kAny && m.type == GS_MAT_BF16))
     load_piece_as<GS_MAT_BF16, NARROW>(p, m, row, col, cols, live);
   else
     load_piece_as<GS_MAT_F32, NARROW>(p, m, row, col, cols, live);
 }
 
+// last: the row's last piece, which may have to move.
 template <int TYPE>
-__device__ inline void settle_piece_as(Piece& p) {
+__device__ inline void settle_piece_as(Piece& p, bool last) {
   Raw16<TYPE, false> r;
 #pragma unroll
   for (int i = 0; i < r.kWords; ++i) r.w[i] = p.v[i / 4][i % 4];
   r.skip = p.skip;
-  r.settle();
+  if (last)
+    r.settle();
+  else
+    r.settle_whole();
 #pragma unroll
   for (int i = 0; i < r.kWords; ++i) p.v[i / 4][i % 4] = r.w[i];
 }
 
-__device__ inline void settle_piece(Piece& p, int type) {
-  if (type == GS_MAT_MX8)
-    settle_piece_as<GS_MAT_MX8>(p);
-  else if (type == GS_MAT_BF16)
-    settle_piece_as<GS_MAT_BF16>(p);
+// TYPE: the matrix's, or kAny.
+template <int TYPE>
+__device__ inline void settle_piece(Piece& p, int type, bool last) {
+  if (TYPE == GS_MAT_MX8 || (TYPE == kAny && type == GS_MAT_MX8))
+    settle_piece_as<GS_MAT_MX8>(p, last);
+  else if (TYPE == GS_MAT_BF16 || (TYPE == kAny && type == GS_MAT_BF16))
+    settle_piece_as<GS_MAT_BF16>(p, last);
   else
-    settle_piece_as<GS_MAT_F32>(p);
+    settle_piece_as<GS_MAT_F32>(p, last);
 }
 
 // The pieces of a lane's row through buffers: rows row0 + row, columns 64 c + 16 g.
@@ -143,16 +149,14 @@ struct Share {
   static constexpr int kQT = NC * KC == 4 ? 2 : 1, kWP = KC, kWQ = NC * 4 / kQT, kMS = 8 / (kWP * kWQ);
 };
 
-constexpr int kAnyNarrow = -3;   // as kAny, a width being below 16
-
-// NC, KC: groups of 64 columns of dz and of x.  DY, Z, X: the types of dy, z (GS_MAT_F32: no
-// activation) and x, widths being multiples of 16; or all kAny or kAnyNarrow.
-template <int NC, int KC, int DY, int Z, int X>
-__global__ void __launch_bounds__(kThreads) rows_bwd_kernel(RowsBwdArgs a) {
+// NC, KC: groups of 64 columns of dz and of x.  DY, Z, X: the types of dy, z (kNone: no
+// activation) and x, or all kAny.
+template <int NC, int KC, int DY, int Z, int X, Reach HOW>
+__global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(RowsBwdArgs a) {
   using S = Share<NC, KC>;
-  constexpr bool kWhole = DY >= 0, kFew = DY == kAnyNarrow;
-  const int dyt = kWhole ? DY : a.dy.type, zt_ = kWhole ? Z : a.z.type, xt_ = kWhole ? X : a.x.type;
-  const int act = Z == GS_MAT_F32 ? GS_ACT_NONE : a.act;
+  constexpr bool kFew = HOW == kNarrow;
+  const int dyt = DY == kAny ? a.dy.type : DY, zt_ = Z == kAny ? a.z.type : Z, xt_ = X == kAny ? a.x.type : X;
+  const int act = Z == kNone ? GS_ACT_NONE : a.act;
   constexpr int kPitchQ = NC * 128 + 32, kPitchP = KC * 128 + 32;
   extern __shared__ __align__(16) uint8_t lds[];
   uint8_t* wt = lds;                                  // NC KC 8 KiB of operands
@@ -187,20 +191,20 @@ __global__ void __launch_bounds__(kThreads) rows_bwd_kernel(RowsBwdArgs a) {
     const int64_t row0 = int64_t(turn) * kRows;
     const int row = wave * 16 + r;
     const bool in = row < a.rows - row0;
-    if constexpr (kWhole) {
+    if constexpr (HOW == kWhole) {
       load_pieces<DY>(dy, a.dy, row0, row, in, g, a.n);
-      if constexpr (Z != GS_MAT_F32) load_pieces<Z>(z, a.z, row0, row, in, g, a.n);
+      if constexpr (Z != kNone) load_pieces<Z>(z, a.z, row0, row, in, g, a.n);
       load_pieces<X>(x, a.x, row0, row, in, g, a.k);
     } else {
       const int64_t at = in ? row0 + row : a.rows - 1;
 #pragma unroll
-      for (int c = 0; c < NC; ++c) load_piece_any<kFew>(dy[c], a.dy, at, c * 64 + g * 16, a.n, in);
+      for (int c = 0; c < NC; ++c) load_piece_any<DY, kFew>(dy[c], a.dy, at, c * 64 + g * 16, a.n, in);
       if (act != GS_ACT_NONE) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) load_piece_any<kFew>(z[c], a.z, at, c * 64 + g * 16, a.n, in);
+        for (int c = 0; c < NC; ++c) load_piece_any<Z, kFew>(z[c], a.z, at, c * 64 + g * 16, a.n, in);
       }
 #pragma unroll
-      for (int c = 0; c < KC; ++c) load_piece_any<kFew>(x[c], a.x, at, c * 64 + g * 16, a.k, in);
+      for (int c = 0; c < KC; ++c) load_piece_any<X, kFew>(x[c], a.x, at, c * 64 + g * 16, a.k, in);
     }
   };
   u32x4 dz[NC][2], xb[KC][2];
@@ -208,11 +212,11 @@ __global__ void __launch_bounds__(kThreads) rows_bwd_kernel(RowsBwdArgs a) {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       float v[16];
-      if constexpr (!kWhole) settle_piece(dy[c], dyt);
+      if constexpr (HOW != kWhole) settle_piece<DY>(dy[c], dyt, c == NC - 1);
       piece_to_float(dy[c], dyt, v);
       if (act != GS_ACT_NONE) {
         float t[16];
-        if constexpr (!kWhole) settle_piece(z[c], zt_);
+        if constexpr (HOW != kWhole) settle_piece<Z>(z[c], zt_, c == NC - 1);
         piece_to_float(z[c], zt_, t);
         if (act == GS_ACT_SILU) {
 #pragma unroll
@@ -232,7 +236,7 @@ __global__ void __launch_bounds__(kThreads) rows_bwd_kernel(RowsBwdArgs a) {
     }
 #pragma unroll
     for (int c = 0; c < KC; ++c) {
-      if constexpr (!kWhole) settle_piece(x[c], xt_);
+      if constexpr (HOW != kWhole) settle_piece<X>(x[c], xt_, c == KC - 1);
       piece_to_bf16(x[c], xt_, xb[c][0], xb[c][1]);
     }
   };
@@ -304,7 +308,7 @@ __global__ void __launch_bounds__(kThreads) rows_bwd_kernel(RowsBwdArgs a) {
         float v[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = acc[kc][i / 4][i % 4];
-        if constexpr (kWhole) {
+        if constexpr (HOW == kWhole) {
           const uint32_t off = in && col < a.k ? (row * uint32_t(a.dx.ld) + col) * e : kAbsent;
           if (a.dx.type == GS_MAT_F32) {
 #pragma unroll
@@ -363,39 +367,44 @@ __global__ void __launch_bounds__(kThreads) rows_bwd_kernel(RowsBwdArgs a) {
   }
 }
 
-template <int NC, int KC, int DY, int Z, int X>
+template <int NC, int KC, int DY, int Z, int X, Reach HOW>
 hipError_t go(const RowsBwdArgs& a, int blocks, hipStream_t s) {
   constexpr size_t kLds = NC * KC * 8192 + size_t(kRows) * ((NC + KC) * 128 + 64);
-  static const hipError_t allowed =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(&rows_bwd_kernel<NC, KC, DY, Z, X>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, int(kLds));
+  const auto kernel = &rows_bwd_kernel<NC, KC, DY, Z, X, HOW>;
+  static const hipError_t allowed = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                                        hipFuncAttributeMaxDynamicSharedMemorySize, int(kLds));
   if (allowed != hipSuccess) return allowed;
   GSK_PROF("linear_rows_bwd", s);
-  rows_bwd_kernel<NC, KC, DY, Z, X><<<blocks, kThreads, kLds, s>>>(a);
+  kernel<<<blocks, kThreads, kLds, s>>>(a);
   return hipGetLastError();
 }
 
-template <int NC, int KC, int DY, int Z>
+template <int NC, int KC, int DY, int Z, Reach HOW>
 hipError_t by_x(const RowsBwdArgs& a, int blocks, hipStream_t s) {
-  return a.x.type == GS_MAT_MX8 ? go<NC, KC, DY, Z, GS_MAT_MX8>(a, blocks, s)
-                                : go<NC, KC, DY, Z, GS_MAT_BF16>(a, blocks, s);
+  return a.x.type == GS_MAT_MX8 ? go<NC, KC, DY, Z, GS_MAT_MX8, HOW>(a, blocks, s)
+                                : go<NC, KC, DY, Z, GS_MAT_BF16, HOW>(a, blocks, s);
 }
 
-template <int NC, int KC, int DY>
+template <int NC, int KC, int DY, Reach HOW>
 hipError_t by_z(const RowsBwdArgs& a, int blocks, hipStream_t s) {
-  if (a.act == GS_ACT_NONE) return by_x<NC, KC, DY, GS_MAT_F32>(a, blocks, s);
-  return a.z.type == GS_MAT_MX8 ? by_x<NC, KC, DY, GS_MAT_MX8>(a, blocks, s) : by_x<NC, KC, DY, GS_MAT_BF16>(a, blocks, s);
+  if (a.act == GS_ACT_NONE) return by_x<NC, KC, DY, kNone, HOW>(a, blocks, s);
+  return a.z.type == GS_MAT_MX8 ? by_x<NC, KC, DY, GS_MAT_MX8, HOW>(a, blocks, s)
+                                : by_x<NC, KC, DY, GS_MAT_BF16, HOW>(a, blocks, s);
 }
 
-// The types are compiled in for widths of whole 16-column pieces in buffers' reach; other
-// widths and pitches (and a float32 z) take one kernel that reads its types from the arguments.
+// The types are compiled in (but for a float32 z and for widths below 16, which take one
+// kernel that reads them from the arguments); whole 16-column pieces in buffers' reach have
+// kernels of their own (500k rows 99 to 113 by the kernel for any type: 407 us, with
+// the types compiled in 144).
 template <int NC, int KC>
 hipError_t by_type(const RowsBwdArgs& a, int blocks, hipStream_t s) {
-  if (a.k % 16 || a.n % 16 || (a.act != GS_ACT_NONE && a.z.type == GS_MAT_F32) || !buffer_ok(a.dy) ||
-      !buffer_ok(a.x) || !buffer_ok(a.dx) || (a.act != GS_ACT_NONE && !buffer_ok(a.z)))
-    return a.k < 16 || a.n < 16 ? go<NC, KC, kAnyNarrow, kAnyNarrow, kAnyNarrow>(a, blocks, s)
-                                : go<NC, KC, kAny, kAny, kAny>(a, blocks, s);
-  return a.dy.type == GS_MAT_F32 ? by_z<NC, KC, GS_MAT_F32>(a, blocks, s) : by_z<NC, KC, GS_MAT_BF16>(a, blocks, s);
+  if (a.k < 16 || a.n < 16 || (a.act != GS_ACT_NONE && a.z.type == GS_MAT_F32))
+    return go<NC, KC, kAny, kAny, kAny, kNarrow>(a, blocks, s);
+  const bool whole = a.k % 16 == 0 && a.n % 16 == 0 && buffer_ok(a.dy) && buffer_ok(a.x) && buffer_ok(a.dx) &&
+                     (a.act == GS_ACT_NONE || buffer_ok(a.z));
+  if (a.dy.type == GS_MAT_F32)
+    return whole ? by_z<NC, KC, GS_MAT_F32, kWhole>(a, blocks, s) : by_z<NC, KC, GS_MAT_F32, kHeldIn>(a, blocks, s);
+  return whole ? by_z<NC, KC, GS_MAT_BF16, kWhole>(a, blocks, s) : by_z<NC, KC, GS_MAT_BF16, kHeldIn>(a, blocks, s);
 }
 
 // Blocks: as many as stay resident at once, each of at least two turns where there are

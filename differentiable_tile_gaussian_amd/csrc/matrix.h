@@ -261,6 +261,11 @@ struct Raw16 {
       skip = 0;
     }
   }
+  // For a piece that lies within the row: zeros if its row is absent.
+  __device__ void settle_whole() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = skip >= 16 ? 0u : w[i];
+  }
   // Moves the piece's own columns to its front, zeros behind them.
   __device__ void settle() {
     constexpr int kE = 4 * kWords / 16;
