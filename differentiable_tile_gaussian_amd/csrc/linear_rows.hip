@@ -277,7 +277,8 @@ __global__ void __launch_bounds__(kAnyThreads) rows_fwd_any_kernel(RowsArgs a, i
   float* bl = reinterpret_cast<float*>(lds + size_t(groups) * KC * 8192);
   const int c0 = blockIdx.y * groups;
   const int nc = (a.n + 63) / 64 - c0 < groups ? (a.n + 63) / 64 - c0 : groups;
-  const bool held = a.n >= 16;
+  // (not where y replaces the residual: a repeated column's residual would be gone)
+  const bool held = a.n >= 16 && !(a.e.r.p && a.e.r.p == a.e.y.p);
   stage_weight<KC>(a.w, a.e.bias, a.k, a.n, c0, nc, lds, bl, held);
   __syncthreads();
   const int lane = threadIdx.x % 64, g = lane / 16, r = lane % 16;

@@ -4,8 +4,8 @@
 //
 // Streams bounded by HBM.  A row is held by 4 to 256 lanes, 8 columns a lane at a time (so an
 // MX8 block is four neighbouring lanes), in registers from its load to its store: each input
-// is read once and each output written once, from 8 to kMaxHeld columns.  Other rows are
-// walked twice by one wave, the second time from the caches.
+// is read once and each output written once, up to kMaxHeld columns.  Wider rows are walked
+// twice by one wave, the second time from the caches.
 #include "matrix.h"
 #include "profile.h"
 
@@ -51,9 +51,20 @@ __device__ inline void store_chunk(const MatArg& m, int64_t row, int col, const 
     store8(m, row, col, v, n);
 }
 
-// LANES lanes hold a row, CHUNKS chunks each (matrix.h has how), and take ROWS rows side by
-// side: their loads are all issued before the first is used.
-template <int LANES, int CHUNKS, int ROWS>
+// A lane's chunk of a row: held inside it (matrix.h), or for rows of fewer than 8 columns
+// (NARROW) what there is of them in the first lane.
+template <bool NARROW>
+__device__ inline Held chunk_at(int col, int cols) {
+  return NARROW ? Held{col, col < cols ? 0 : 8} : held_at(col, cols);
+}
+template <bool NARROW>
+__device__ inline Raw8 load_chunk(const MatArg& m, int64_t row, const Held& c, int cols) {
+  return NARROW ? load_raw8(m, row, c.at, cols - c.at) : load_held(m, row, c);
+}
+
+// LANES lanes hold a row, CHUNKS chunks each, and take ROWS rows side by side: their loads are
+// all issued before the first is used.
+template <int LANES, int CHUNKS, int ROWS, bool NARROW>
 __global__ void __launch_bounds__(kThreads) rmsnorm_fwd_kernel(NormFwdArgs a) {
   constexpr int kPer = kThreads / LANES;
   const int lane = threadIdx.x % LANES;
@@ -63,22 +74,22 @@ __global__ void __launch_bounds__(kThreads) rmsnorm_fwd_kernel(NormFwdArgs a) {
   for (int u = 0; u < ROWS; ++u) {
     const int64_t row = first + u * kPer < a.rows ? first + u * kPer : a.rows - 1;
 #pragma unroll
-    for (int c = 0; c < CHUNKS; ++c) xr[u][c] = load_held(a.x, row, held_at((c * LANES + lane) * 8, a.cols));
+    for (int c = 0; c < CHUNKS; ++c) xr[u][c] = load_chunk<NARROW>(a.x, row, chunk_at<NARROW>((c * LANES + lane) * 8, a.cols), a.cols);
   }
   if (a.r.p) {
 #pragma unroll
     for (int u = 0; u < ROWS; ++u) {
       const int64_t row = first + u * kPer < a.rows ? first + u * kPer : a.rows - 1;
 #pragma unroll
-      for (int c = 0; c < CHUNKS; ++c) rr[u][c] = load_held(a.r, row, held_at((c * LANES + lane) * 8, a.cols));
+      for (int c = 0; c < CHUNKS; ++c) rr[u][c] = load_chunk<NARROW>(a.r, row, chunk_at<NARROW>((c * LANES + lane) * 8, a.cols), a.cols);
     }
   }
   float w[CHUNKS][8];
 #pragma unroll
   for (int c = 0; c < CHUNKS; ++c) {
-    const Held t = held_at((c * LANES + lane) * 8, a.cols);
+    const Held t = chunk_at<NARROW>((c * LANES + lane) * 8, a.cols);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[c][i] = a.w[t.at + i];
+    for (int i = 0; i < 8; ++i) w[c][i] = NARROW && t.at + i >= a.cols ? 0.0f : a.w[t.at + i];
   }
 #pragma unroll
   for (int u = 0; u < ROWS; ++u) {
@@ -86,7 +97,7 @@ __global__ void __launch_bounds__(kThreads) rmsnorm_fwd_kernel(NormFwdArgs a) {
     float h[CHUNKS][8], sum = 0.0f;
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
-      const Held t = held_at((c * LANES + lane) * 8, a.cols);
+      const Held t = chunk_at<NARROW>((c * LANES + lane) * 8, a.cols);
       raw8_to_float(xr[u][c], a.x.type, h[c]);
       if (a.r.p) {
         float r[8];
@@ -104,27 +115,27 @@ __global__ void __launch_bounds__(kThreads) rmsnorm_fwd_kernel(NormFwdArgs a) {
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
       const int col = (c * LANES + lane) * 8;
-      const Held t = held_at(col, a.cols);
+      const Held t = chunk_at<NARROW>(col, a.cols);
       float y[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] = h[c][i] * rstd * w[c][i];
       const bool mine = in && t.skip < 8;
-      if (a.h.p && mine) store8(a.h, row, t.at, h[c], 8);
+      if (a.h.p && mine) store8(a.h, row, t.at, h[c], NARROW ? a.cols : 8);
       if (a.y.type == GS_MAT_MX8) {
-        move_down(t, y);
+        if (!NARROW) move_down(t, y);
         store_mx8_quad(a.y, row, col, y, in ? a.cols - col : 0);
       } else if (mine) {
-        store8(a.y, row, t.at, y, 8);
+        store8(a.y, row, t.at, y, NARROW ? a.cols : 8);
       }
       if (a.ckpt.p) {
-        move_down(t, h[c]);
+        if (!NARROW) move_down(t, h[c]);
         store_mx8_quad(a.ckpt, row, col, h[c], in ? a.cols - col : 0);
       }
     }
   }
 }
 
-// Rows of fewer than 8 or more than kMaxHeld columns: a wave a row, walked twice.
+// Rows of more than kMaxHeld columns: a wave a row, walked twice.
 __global__ void __launch_bounds__(kThreads) rmsnorm_fwd_wide_kernel(NormFwdArgs a) {
   const int lane = threadIdx.x % 64;
   const int64_t row = int64_t(blockIdx.x) * (kThreads / 64) + threadIdx.x / 64;
@@ -172,17 +183,17 @@ struct NormBwdArgs {
   int cols;
 };
 
-template <int LANES, int CHUNKS>
+template <int LANES, int CHUNKS, bool NARROW>
 __global__ void __launch_bounds__(kThreads) rmsnorm_bwd_kernel(NormBwdArgs a) {
   constexpr int kPer = kThreads / LANES;
   const int lane = threadIdx.x % LANES;
   float w[CHUNKS][8], acc[CHUNKS][8];
 #pragma unroll
   for (int c = 0; c < CHUNKS; ++c) {
-    const Held t = held_at((c * LANES + lane) * 8, a.cols);
+    const Held t = chunk_at<NARROW>((c * LANES + lane) * 8, a.cols);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      w[c][i] = a.w[t.at + i];
+      w[c][i] = NARROW && t.at + i >= a.cols ? 0.0f : a.w[t.at + i];
       acc[c][i] = 0.0f;
     }
   }
@@ -193,22 +204,25 @@ __global__ void __launch_bounds__(kThreads) rmsnorm_bwd_kernel(NormBwdArgs a) {
     Raw8 dr[CHUNKS], hr[CHUNKS], rr[CHUNKS];
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
-      const Held t = held_at((c * LANES + lane) * 8, a.cols);
-      dr[c] = load_held(a.dy, row, t);
-      hr[c] = load_held(a.h, row, t);
+      const Held t = chunk_at<NARROW>((c * LANES + lane) * 8, a.cols);
+      dr[c] = load_chunk<NARROW>(a.dy, row, t, a.cols);
+      hr[c] = load_chunk<NARROW>(a.h, row, t, a.cols);
     }
     if (a.dres.p) {
 #pragma unroll
-      for (int c = 0; c < CHUNKS; ++c) rr[c] = load_held(a.dres, row, held_at((c * LANES + lane) * 8, a.cols));
+      for (int c = 0; c < CHUNKS; ++c) rr[c] = load_chunk<NARROW>(a.dres, row, chunk_at<NARROW>((c * LANES + lane) * 8, a.cols), a.cols);
     }
     const float rstd = a.rstd[row];
     float dy[CHUNKS][8], xh[CHUNKS][8], dot = 0.0f;
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
-      const Held t = held_at((c * LANES + lane) * 8, a.cols);
+      const Held t = chunk_at<NARROW>((c * LANES + lane) * 8, a.cols);
       const int skip = in ? t.skip : 8;
       raw8_to_float(dr[c], a.dy.type, dy[c]);
-      held_to_float(hr[c], a.h.type, t, xh[c]);
+      if (NARROW)
+        raw8_to_float(hr[c], a.h.type, xh[c]);
+      else
+        held_to_float(hr[c], a.h.type, t, xh[c]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         xh[c][i] *= rstd;
@@ -220,7 +234,7 @@ __global__ void __launch_bounds__(kThreads) rmsnorm_bwd_kernel(NormBwdArgs a) {
     const float mean = row_sum<LANES>(dot, turn++) * a.inv_cols;
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
-      const Held t = held_at((c * LANES + lane) * 8, a.cols);
+      const Held t = chunk_at<NARROW>((c * LANES + lane) * 8, a.cols);
       float o[8];
       if (a.dres.p) {
         raw8_to_float(rr[c], a.dres.type, o);
@@ -230,7 +244,7 @@ __global__ void __launch_bounds__(kThreads) rmsnorm_bwd_kernel(NormBwdArgs a) {
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[i] += rstd * (dy[c][i] * w[c][i] - xh[c][i] * mean);
-      if (in && t.skip < 8) store8(a.dh, row, t.at, o, 8);
+      if (in && t.skip < 8) store8(a.dh, row, t.at, o, NARROW ? a.cols : 8);
     }
   }
   if (!a.part) return;
@@ -239,7 +253,7 @@ __global__ void __launch_bounds__(kThreads) rmsnorm_bwd_kernel(NormBwdArgs a) {
   float* out = a.part + int64_t(blockIdx.x) * a.cols;
 #pragma unroll
   for (int c = 0; c < CHUNKS; ++c) {
-    move_down(held_at((c * LANES + lane) * 8, a.cols), acc[c]);
+    if (!NARROW) move_down(held_at((c * LANES + lane) * 8, a.cols), acc[c]);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) sums[threadIdx.x * 8 + i] = acc[c][i];
@@ -253,8 +267,8 @@ __global__ void __launch_bounds__(kThreads) rmsnorm_bwd_kernel(NormBwdArgs a) {
   }
 }
 
-// Rows of fewer than 8 or more than kMaxHeld columns: a wave a row, walked twice; the
-// weight's gradient has its own kernel.
+// Rows of more than kMaxHeld columns: a wave a row, walked twice; the weight's gradient has
+// its own kernel.
 __global__ void __launch_bounds__(kThreads) rmsnorm_bwd_wide_kernel(NormBwdArgs a) {
   const int lane = threadIdx.x % 64;
   const int64_t row = int64_t(blockIdx.x) * (kThreads / 64) + threadIdx.x / 64;
@@ -325,7 +339,7 @@ int lanes_for(int cols) {
 }
 
 // Whether the kernels that do not hold a row take it.
-bool wide(int cols) { return cols < 8 || cols > kMaxHeld; }
+bool wide(int cols) { return cols > kMaxHeld; }
 
 // Blocks of the backward: as many as the kernel's registers let reside at once (five waves a
 // SIMD; 1M rows of 128: 161 us, with 1024 blocks 178, with 2048 183).
@@ -336,34 +350,38 @@ int bwd_blocks(int64_t rows, int cols) {
   return int(want < 1 ? 1 : (want > 1280 ? 1280 : want));
 }
 
-template <template <int, int> class Launch, typename Args>
+template <template <int, int, bool> class Launch, typename Args>
 void by_width(int cols, const Args& a, unsigned blocks, hipStream_t s) {
+  if (cols < 8) {
+    Launch<4, 1, true>::go(a, blocks, s);
+    return;
+  }
   switch (lanes_for(cols)) {
-    case 4: Launch<4, 1>::go(a, blocks, s); break;
-    case 8: Launch<8, 1>::go(a, blocks, s); break;
-    case 16: Launch<16, 1>::go(a, blocks, s); break;
-    case 32: Launch<32, 1>::go(a, blocks, s); break;
+    case 4: Launch<4, 1, false>::go(a, blocks, s); break;
+    case 8: Launch<8, 1, false>::go(a, blocks, s); break;
+    case 16: Launch<16, 1, false>::go(a, blocks, s); break;
+    case 32: Launch<32, 1, false>::go(a, blocks, s); break;
     case 64:
-      if (cols <= 512) Launch<64, 1>::go(a, blocks, s);
-      else Launch<64, 2>::go(a, blocks, s);
+      if (cols <= 512) Launch<64, 1, false>::go(a, blocks, s);
+      else Launch<64, 2, false>::go(a, blocks, s);
       break;
     default:
-      if (cols <= 2048) Launch<256, 1>::go(a, blocks, s);
-      else Launch<256, 2>::go(a, blocks, s);
+      if (cols <= 2048) Launch<256, 1, false>::go(a, blocks, s);
+      else Launch<256, 2, false>::go(a, blocks, s);
   }
 }
 
-template <int L, int C>
+template <int L, int C, bool NARROW>
 struct Fwd {
   static void go(const NormFwdArgs& a, unsigned, hipStream_t s) {
     constexpr int kRows = C == 1 ? 2 : 1;
-    rmsnorm_fwd_kernel<L, C, kRows><<<div_up(a.rows, kThreads / L * kRows), kThreads, 0, s>>>(a);
+    rmsnorm_fwd_kernel<L, C, kRows, NARROW><<<div_up(a.rows, kThreads / L * kRows), kThreads, 0, s>>>(a);
   }
 };
-template <int L, int C>
+template <int L, int C, bool NARROW>
 struct Bwd {
   static void go(const NormBwdArgs& a, unsigned blocks, hipStream_t s) {
-    rmsnorm_bwd_kernel<L, C><<<blocks, kThreads, 0, s>>>(a);
+    rmsnorm_bwd_kernel<L, C, NARROW><<<blocks, kThreads, 0, s>>>(a);
   }
 };
 

@@ -346,6 +346,22 @@ def test_linear_backward(gs, rows, k, n, dk, xk, zk, act, dxk, dwk, pitch):
         assert torch.equal(one[want], (dx, dw, db)[want]), want
 
 
+@pytest.mark.parametrize("n", [7, 16, 40, 65, 67, 79, 80, 130, 200, 300])
+@pytest.mark.parametrize("rows", [100, 20000])
+def test_linear_in_place_of_the_residual(gs, rows, n):
+    """The same bits with y in place of the residual, at widths whose last columns are taken
+    from inside the row, with the column groups in one block and in several."""
+    print("linear in place", rows, n, flush=True)
+    g = rng("inplacelinear", rows, n)
+    x, w = normal(g, rows, 20).bfloat16().cuda(), normal(g, n, 20).bfloat16().cuda()
+    for dt in (torch.bfloat16, torch.float32):
+        r = normal(g, rows, n).to(dt).cuda()
+        y = torch.empty_like(r)
+        gs.gs_linear_fwd(x, w, y, act="silu", residual=r)
+        gs.gs_linear_fwd(x, w, r, act="silu", residual=r)
+        assert torch.equal(r, y)
+
+
 def test_linear_gradient_against_differences(gs):
     g = rng("lineardiff")
     rows, k, n = 3, 7, 5
