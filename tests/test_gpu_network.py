@@ -209,11 +209,12 @@ def test_rmsnorm_forward(gs, rows, cols, pad, offset, xk, rk, hk, ck, yk):
         assert untouched(y, rows, cols)
 
 
-def test_rmsnorm_forward_in_place(gs):
-    g = rng("inplace")
-    x, r = (normal(g, 50, 96).bfloat16().cuda() for _ in range(2))
-    w = torch.ones(96, device="cuda")
-    y, h = (torch.empty(50, 96, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+@pytest.mark.parametrize("cols", [3, 9, 59, 96, 513, 1000, 1025, 2047, 4095, 4097])
+def test_rmsnorm_forward_in_place(gs, cols):
+    g = rng("inplace", cols)
+    x, r = (normal(g, 50, cols).bfloat16().cuda() for _ in range(2))
+    w = torch.ones(cols, device="cuda")
+    y, h = (torch.empty(50, cols, dtype=torch.bfloat16, device="cuda") for _ in range(2))
     gs.gs_rmsnorm_fwd(x, w, EPS, y, residual=r, h=h)
     r2, y2 = r.clone(), torch.empty_like(y)
     gs.gs_rmsnorm_fwd(x, w, EPS, y2, residual=r2, h=r2)
