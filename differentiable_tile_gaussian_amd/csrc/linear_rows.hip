@@ -63,16 +63,31 @@ struct Piece<true> {
 // bias, from which the sums start.
 // held: the last 16-column piece is taken from inside the row (as matrix.h's Raw16), so that
 // its lanes compute, and write, 16 columns like all others.
-template <int KC>
+template <int KC, int NC, int THREADS, bool NARROW>
 __device__ inline void stage_weight(const MatArg& w, const float* bias, int k, int n, int c0, int nc, uint8_t* wl,
                                     float* bl, bool held) {
-  for (int f = threadIdx.x; f < nc * KC * 512; f += blockDim.x) {
-    const int l = f % 64, frag = f / 64, half = frag % 2, kc = frag / 2 % KC, t = frag / (2 * KC) % 4;
-    const int c = frag / (8 * KC);
-    int first = (c0 + c) * 64 + l % 16 / 4 * 16;
-    if (held && first > n - 16) first = n - 16;
-    const int row = first + t * 4 + l % 4, col = kc * 64 + l / 16 * 16 + half * 8;
-    *reinterpret_cast<u32x4*>(wl + size_t(f) * 16) = load_raw8(w, row, col, row < n ? k - col : 0).lo;
+  // a unit: the 16 k of a lane's two operands; four of a thread's units in flight
+  constexpr int kUnits = NC * KC * 256 / THREADS, kBatch = kUnits < 4 ? kUnits : 4;
+  for (int f0 = threadIdx.x; f0 < nc * KC * 256; f0 += THREADS * kBatch) {
+    Raw16<GS_MAT_BF16, NARROW> raw[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int f = f0 + u * THREADS, l = f % 64, kc = f / 64 % KC, t = f / (64 * KC) % 4, c = f / (256 * KC);
+      int first = (c0 + c) * 64 + l % 16 / 4 * 16;
+      if (held && first > n - 16) first = n - 16;
+      const int row = first + t * 4 + l % 4;
+      raw[u].load(w, row < n ? row : n - 1, kc * 64 + l / 16 * 16, k, row < n);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int f = f0 + u * THREADS, l = f % 64, kc = f / 64 % KC, t = f / (64 * KC) % 4, c = f / (256 * KC);
+      if (f >= nc * KC * 256) break;
+      raw[u].settle();
+      uint8_t* at = wl + (((c * 4 + t) * KC + kc) * 2) * 1024 + l * 16;
+      const uint32_t* v = raw[u].w;
+      *reinterpret_cast<u32x4*>(at) = u32x4{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<u32x4*>(at + 1024) = u32x4{v[4], v[5], v[6], v[7]};
+    }
   }
   for (int j = threadIdx.x; j < nc * 64; j += blockDim.x) {
     int first = (c0 * 64 + j) / 16 * 16;
@@ -150,8 +165,6 @@ __global__ void __launch_bounds__(S::kThreads, S::kWaves) rows_fwd_kernel(RowsAr
   float* bl = reinterpret_cast<float*>(lds + NC * KC * 8192);
   const int c0 = blockIdx.y * NC, col0 = c0 * 64;
   const int nc = (a.n + 63) / 64 - c0 < NC ? (a.n + 63) / 64 - c0 : NC;
-  stage_weight<KC>(a.w, a.e.bias, a.k, a.n, c0, nc, lds, bl, false);
-  __syncthreads();
   const int lane = threadIdx.x % 64, g = lane / 16, r = lane % 16;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int turns = int((a.rows + 16 * MT - 1) / (16 * MT)), step = gridDim.x * (S::kThreads / 64);
@@ -176,6 +189,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kWaves) rows_fwd_kernel(RowsAr
     }
   };
   fetch(turn);
+  stage_weight<KC, NC, S::kThreads, false>(a.w, a.e.bias, a.k, a.n, c0, nc, lds, bl, false);
+  __syncthreads();
   bf16x8 xf[MT][KC][2];
   auto convert = [&]() {
 #pragma unroll
@@ -279,8 +294,6 @@ __global__ void __launch_bounds__(kAnyThreads) rows_fwd_any_kernel(RowsArgs a, i
   const int nc = (a.n + 63) / 64 - c0 < groups ? (a.n + 63) / 64 - c0 : groups;
   // (not where y replaces the residual: a repeated column's residual would be gone)
   const bool held = a.n >= 16 && !(a.e.r.p && a.e.r.p == a.e.y.p);
-  stage_weight<KC>(a.w, a.e.bias, a.k, a.n, c0, nc, lds, bl, held);
-  __syncthreads();
   const int lane = threadIdx.x % 64, g = lane / 16, r = lane % 16;
   const int64_t step = int64_t(gridDim.x) * (kAnyThreads / 64) * 16;
   int64_t row0 = (int64_t(blockIdx.x) * (kAnyThreads / 64) + threadIdx.x / 64) * 16;
@@ -292,6 +305,8 @@ __global__ void __launch_bounds__(kAnyThreads) rows_fwd_any_kernel(RowsArgs a, i
       next[kc].load(a.x, row < a.rows ? row : a.rows - 1, kc * 64 + g * 16, a.k, row < a.rows);
   };
   fetch(row0);
+  stage_weight<KC, 4, kAnyThreads, NARROW>(a.w, a.e.bias, a.k, a.n, c0, nc, lds, bl, held);
+  __syncthreads();
   for (; row0 < a.rows; row0 += step) {
     const int64_t row = row0 + r;
     bf16x8 xf[1][KC][2];

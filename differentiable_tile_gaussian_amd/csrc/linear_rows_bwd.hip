@@ -126,6 +126,15 @@ __device__ inline void piece_to_bf16(const Piece& p, int type, u32x4& a, u32x4& 
   }
 }
 
+template <int ROTATION>
+__device__ inline float add_rotated(float v) {
+  return v + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x120 + ROTATION, 0xf, 0xf, true));
+}
+// The sum over the 16 lanes of a row of the wave, by rotations within it.
+__device__ inline float sum_over16(float v) {
+  return add_rotated<1>(add_rotated<2>(add_rotated<4>(add_rotated<8>(v))));
+}
+
 // Orders LDS accesses around a barrier; global loads stay in flight across it.
 __device__ inline void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
@@ -164,16 +173,6 @@ __global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(RowsBwdArgs a) {
   uint8_t* xt = zt + kRows * kPitchQ;                 // x rows
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, g = lane / 16, r = lane % 16;
   const int wp = wave % S::kWP, wq = wave / S::kWP % S::kWQ, ms = wave / (S::kWP * S::kWQ);
-
-  // W^T as operands of tile (kc, t), piece (nc, half): lane (g, r) holds rows n = 64 nc + 16 g
-  // + 8 half .. + 7 of column k = 64 kc + 16 (r / 4) + 4 t + r % 4.
-  for (int i = threadIdx.x; i < NC * KC * 4096; i += kThreads) {
-    const int n = i / (KC * 64), k = i % (KC * 64);
-    const uint16_t v = n < a.n && k < a.k ? reinterpret_cast<const uint16_t*>(a.w.p)[int64_t(n) * a.w.ld + k] : 0;
-    const int frag = ((k / 64 * 4 + k / 4 % 4) * NC + n / 64) * 2 + n / 8 % 2;
-    const int l = n / 16 % 4 * 16 + k / 16 % 4 * 4 + k % 4;
-    *reinterpret_cast<uint16_t*>(wt + frag * 1024 + l * 16 + n % 8 * 2) = v;
-  }
 
   float db[NC][16];
   f32x4 dw[S::kQT][4];
@@ -241,10 +240,28 @@ __global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(RowsBwdArgs a) {
     }
   };
   const int turns = int((a.rows + kRows - 1) / kRows);
-  if (int64_t(blockIdx.x) < turns) {
-    fetch(blockIdx.x);
-    convert();
+  const bool any = int64_t(blockIdx.x) < turns;
+  if (any) fetch(blockIdx.x);
+  // W^T as operands of tile (kc, t), piece (nc, half): lane (g, r) holds rows n = 64 nc + 16 g
+  // + 8 half .. + 7 of column k = 64 kc + 16 (r / 4) + 4 t + r % 4.
+  constexpr int kChunks = NC * KC;   // of 8 k, for each thread
+  u32x4 wr[kChunks];
+#pragma unroll
+  for (int u = 0; u < kChunks; ++u) {
+    const int i = u * kThreads + threadIdx.x, n = i / (KC * 8), k = i % (KC * 8) * 8;
+    wr[u] = load_raw8(a.w, n, k, n < a.n ? a.k - k : 0).lo;
   }
+#pragma unroll
+  for (int u = 0; u < kChunks; ++u) {
+    const int i = u * kThreads + threadIdx.x, n = i / (KC * 8), k0 = i % (KC * 8) * 8;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int k = k0 + j, frag = ((k / 64 * 4 + k / 4 % 4) * NC + n / 64) * 2 + n / 8 % 2;
+      const int l = n / 16 % 4 * 16 + k / 16 % 4 * 4 + k % 4;
+      *reinterpret_cast<uint16_t*>(wt + frag * 1024 + l * 16 + n % 8 * 2) = uint16_t(wr[u][j / 2] >> (16 * (j & 1)));
+    }
+  }
+  if (any) convert();
   for (int turn = blockIdx.x; turn < turns; turn += gridDim.x) {
     lds_barrier();   // the last turn's readers are done (and, at first, W^T is written)
 #pragma unroll
@@ -335,12 +352,16 @@ __global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(RowsBwdArgs a) {
     for (int q = 0; q < S::kQT; ++q) {
       const int n = (wq * S::kQT + q) * 16 + r;
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = wp * 64 + t * 16 + g * 4 + i;
-          if (n < a.n && k < a.k) out[n * a.k + k] = dw[q][t][i];
+      for (int t = 0; t < 4; ++t) {
+        const int k = wp * 64 + t * 16 + g * 4;
+        if (n >= a.n || k >= a.k) continue;
+        float* o = out + n * a.k + k;
+        if (k + 4 <= a.k) {
+          __builtin_memcpy(__builtin_assume_aligned(o, 4), &dw[q][t], 16);
+        } else {
+          for (int i = 0; k + i < a.k; ++i) o[i] = dw[q][t][i];
         }
+      }
     }
   }
   if (a.want_db) {
@@ -351,9 +372,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(RowsBwdArgs a) {
     for (int c = 0; c < NC; ++c)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        float t = db[c][i];
-#pragma unroll
-        for (int o = 1; o < 16; o *= 2) t += __shfl_xor(t, o);
+        const float t = sum_over16(db[c][i]);
         if (r == 0) sums[wave * NC * 64 + c * 64 + g * 16 + i] = t;
       }
     __syncthreads();
@@ -407,11 +426,12 @@ hipError_t by_type(const RowsBwdArgs& a, int blocks, hipStream_t s) {
   return whole ? by_z<NC, KC, GS_MAT_BF16, kWhole>(a, blocks, s) : by_z<NC, KC, GS_MAT_BF16, kHeldIn>(a, blocks, s);
 }
 
-// Blocks: as many as stay resident at once, each of at least two turns where there are
-// enough rows (a block's sums of dW cost about as much traffic as a turn).
+// Blocks: one a turn with few rows; else as many as stay resident at once, each of at least
+// two turns (a block's sums of dW cost about as much traffic as a turn).
 int blocks_for(int64_t rows, int k, int n) {
   const int resident = k <= 64 && n <= 64 ? 512 : 256;
-  const int64_t turns = (rows + kRows - 1) / kRows, want = turns < 2 * resident ? (turns + 1) / 2 : resident;
+  const int64_t turns = (rows + kRows - 1) / kRows;
+  const int64_t want = turns <= 128 ? turns : turns < 2 * resident ? (turns + 1) / 2 : resident;
   return int(want < 1 ? 1 : want);
 }
 
