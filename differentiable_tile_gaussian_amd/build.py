@@ -19,8 +19,8 @@ OUT = os.path.join(PKG, "libgs.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["preprocess.hip", "chain.hip", "scan.hip", "sort.hip", "render.hip", "loss.hip", "adam.hip", "layout.hip",
-           "densify.hip", "mx8.hip", "rmsnorm.hip", "linear.hip", "linear_rows.hip", "linear_rows_bwd.hip", "linear_tiles.hip", "linear_split.hip",
-           "profile.hip", "gs_api.hip"]
+           "densify.hip", "mx8.hip", "rmsnorm.hip", "linear.hip", "linear_rows.hip", "linear_rows_bwd.hip",
+           "linear_tiles.hip", "linear_split.hip", "profile.hip", "gs_api.hip"]
 PER_FILE_FLAGS = {"preprocess.hip": ["-ffp-contract=off"], "chain.hip": ["-ffp-contract=off"],
                   "densify.hip": ["-ffp-contract=off"]}
 ARCH = os.environ.get("GS_OFFLOAD_ARCH", "gfx950")

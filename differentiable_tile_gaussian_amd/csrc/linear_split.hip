@@ -2,6 +2,8 @@
 // the card, and what there is to do is reading the weight.  A block takes 16 PT columns by 16
 // QT rows and its waves share the contraction, each loading its operands from memory
 // straight into registers one step ahead; the waves' sums are joined through LDS in order.
+// Bounded by latency (a launch, the weight's and the bias's loads, the join): one row 1024 to
+// 1024 in 5.4 us, 4096 to 4096 in 11 us (33.5 MB of weight, 3.0 TB/s).
 #include "linear.h"
 #include "profile.h"
 
@@ -167,7 +169,7 @@ hipError_t go(const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, cons
 
 template <int QTYPE, Reach HOW>
 hipError_t by_rows(const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, const Epilogue& e, hipStream_t s) {
-  // one row 1024 to 1024 by 32 columns a block: 5.6 us, by 64 7.5
+  // one row 1024 to 1024 by 32 columns a block: 5.4 us, by 64 7.5
   if (nq <= 16) return go<QTYPE, 1, 2, HOW>(P, Q, np, nq, nk, e, s);
   return nq <= 32 ? go<QTYPE, 2, 4, HOW>(P, Q, np, nq, nk, e, s) : go<QTYPE, 4, 4, HOW>(P, Q, np, nq, nk, e, s);
 }

@@ -5,6 +5,10 @@
 // float32), so a block of 32 columns is four neighbouring lanes and its largest magnitude
 // two lane exchanges; 4 to 64 lanes take a row (the smallest power of two that covers it,
 // so narrow rows leave few lanes idle), and each keeps kRows rows in flight.
+//
+// 1M rows of 59 float32 columns: pack 59 us (5.0 TB/s), unpack to bfloat16 29 us (its input
+// still in the last-level cache in part); 8160 rows of 4096 bfloat16: 23 and 18 us (4.4 and
+// 5.5 TB/s).  A copy of 256 MB reaches 5.4 TB/s.
 #include "matrix.h"
 #include "profile.h"
 

@@ -281,10 +281,13 @@ def test_rmsnorm_gradient_against_differences(gs):
 LINEAR_SHAPES = [(1, 1, 1), (1, 1024, 1024), (2, 64, 48), (17, 35, 59), (64, 32, 64), (1000, 128, 128), (513, 64, 48),
                  (300, 257, 130), (129, 1024, 384), (4097, 96, 200), (64, 300, 2000), (33, 256, 256), (2050, 3, 3),
                  (5, 4096, 40), (700, 512, 640), (257, 129, 65), (1, 5000, 7)]
+# widths of more than two column groups against one, and results of 65 to 128 and of more tiles
+LINEAR_SHAPES += [(300, 200, 33), (300, 33, 200), (513, 256, 64), (513, 64, 256), (300, 7, 200), (300, 200, 7),
+                  (1100, 80, 1000), (1030, 83, 1001), (2100, 48, 1104), (2100, 45, 1101)]
 PITCHES = [(0, 0), (3, 1), (8, 0)]
 
 
-@pytest.mark.parametrize("rows,k,n", LINEAR_SHAPES)
+@pytest.mark.parametrize("rows,k,n", LINEAR_SHAPES + [(3200, 2048, 2048)])
 @pytest.mark.parametrize("xk,act,rk,zk,yk,pitch", [("bf16", "none", None, None, "f32", 0), ("mx8", "silu", None, "mx8", "bf16", 0),
                                                    ("mx8", "gelu", "bf16", "bf16", "bf16", 1),
                                                    ("bf16", "relu", "f32", "mx8", "f32", 2),
