@@ -9,8 +9,9 @@
 // columns 16 g + 4 t + i, so that a lane's four tiles are 16 consecutive columns of one row:
 // wide stores, and half an MX8 block.
 //
-// 1M rows 128 to 128 from MX8, silu, z kept in MX8: 126 us (520 MB, 4.1 TB/s; the same reads and
-// writes alone 105 us: two write streams and a read stream, where a copy has one of each).
+// 1M rows 128 to 128 from MX8, silu, z kept in MX8: 116-130 us over runs (520 MB, 4.0-4.5
+// TB/s; the same reads and writes alone 105 us: two write streams and a read stream, where a
+// copy has one of each).
 #include "linear.h"
 #include "profile.h"
 

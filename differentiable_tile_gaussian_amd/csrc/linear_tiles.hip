@@ -4,8 +4,8 @@
 // memory and the next step's are written to LDS while the present one is computed, so that
 // one barrier a step suffices and nothing waits for memory.
 //
-// 8160 rows, 4096 to 1024 (68 GFLOP): from bfloat16 82 us (830 TFLOP/s), from MX8 86 us with a
-// residual; the contraction over the rows for dW (4096 x 1024): 111 us (620 TFLOP/s).  What is left
+// 8160 rows, 4096 to 1024 (68 GFLOP): from bfloat16 82 us (830 TFLOP/s), from MX8 with a
+// residual 82 too; the contraction over the rows for dW (4096 x 1024): 107 us (640 TFLOP/s).  What is left
 // is LDS: a step's operands are written once and read twice by the waves beside its matrix
 // instructions.
 #include "linear.h"
