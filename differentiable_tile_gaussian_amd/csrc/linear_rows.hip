@@ -175,7 +175,6 @@ __global__ void __launch_bounds__(S::kThreads, S::kWaves) rows_fwd_kernel(RowsAr
   int turn = blockIdx.x * (S::kThreads / 64) + wave;
 
   const uint32_t xp = uint32_t(a.x.ld) * (MX ? 1 : 2), xs = uint32_t(a.x.lds);
-  const bool last_piece = (KC - 1) * 64 + g * 16 < a.k;
   Piece<MX> next[MT][KC];
   auto fetch = [&](int t) {
     const int64_t from = int64_t(__builtin_amdgcn_readfirstlane(t)) * (16 * MT);
@@ -187,7 +186,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kWaves) rows_fwd_kernel(RowsAr
       const uint32_t off = (m * 16 + r) * xp + g * (MX ? 16 : 32), soff = (m * 16 + r) * xs + g / 2;
 #pragma unroll
       for (int kc = 0; kc < KC; ++kc) {
-        const bool there = in && (kc < KC - 1 || last_piece);
+        // the row ends in the last group of 64, or with four groups the one before it
+        const bool there = in && (kc < KC / 2 || kc * 64 + g * 16 < a.k);
         next[m][kc].load(data, scales, there ? off : kAbsent, there ? soff : kAbsent, kc);
       }
     }
