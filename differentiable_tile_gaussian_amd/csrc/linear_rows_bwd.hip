@@ -451,8 +451,10 @@ bool rows_bwd_takes(int k, int n) {
   return (k <= 128 && n <= 128) || (k <= 256 && n <= 64) || (k >= 16 && k <= 64 && n <= 256);
 }
 
+// No less than fewer rows take: the blocks are up to 128 for 128 turns and fall to 65 for one more.
 size_t rows_bwd_ws_bytes(int64_t rows, int k, int n) {
-  return size_t(blocks_for(rows, k, n)) * shares(k, n) * (size_t(n) * k + n) * 4;
+  const int most = rows > 128 * kRows ? 128 : 0, blocks = blocks_for(rows, k, n);
+  return size_t(blocks > most ? blocks : most) * shares(k, n) * (size_t(n) * k + n) * 4;
 }
 
 hipError_t launch_rows_bwd(const MatArg& dy, const MatArg& z, int act, const MatArg& x, const MatArg& w,

@@ -513,8 +513,9 @@ enum { GS_WS_PREPROCESS = 0, GS_WS_BIN_SORT = 1, GS_WS_LOSS = 2, GS_WS_RENDER = 
 /* Workspace size in bytes for the call `which_call` (GS_WS_*) with n Gaussians (rows, for the
  * network operators), `pairs` pairs and a W x H image (for the network operators W is the input
  * width and H the output width of a linear layer, W the width of a norm); cfg as the call will
- * receive it (NULL: defaults).  The render workspace
- * (GS_WS_RENDER) depends on cfg's split sizes and gradient-sum mode; the others do not. */
+ * receive it (NULL: defaults).  A network operator's workspace for n rows also serves fewer rows
+ * of the same widths.  The render workspace (GS_WS_RENDER) depends on cfg's split sizes and
+ * gradient-sum mode; the others do not. */
 size_t gs_workspace_bytes(int32_t which_call, int64_t n, uint32_t pairs, int32_t W, int32_t H, const gs_config* cfg);
 
 /* Optional per-kernel timing (instrumentation, not part of the method).  gs_profile_enable(1, only)

@@ -158,3 +158,13 @@ def test_the_reference_encoding_pins():
     assert codes[0, 32] == 0x76                                         # 449 / 2 = 224.5 -> 224
     assert ref.mx8_decode(codes, s)[0, 32] == 448.0
     assert list(ref.mx8_encode(np.zeros((1, 1)))[1][0]) == [1]
+
+
+@pytest.mark.parametrize("k,n", [(64, 48), (128, 128), (256, 64), (64, 256), (99, 113), (200, 200), (1024, 4096), (4096, 40)])
+def test_a_workspace_serves_fewer_rows(gs, k, n):
+    """Sizes do not fall as rows are added, so that one made for the most rows serves all calls."""
+    rows = sorted({r + d for r in (0, 128, 512, 1280, 16384, 20480, 32768, 65536, 131072, 1 << 20) for d in (-1, 0, 1, 127, 128)
+                   if r + d >= 0} | set(range(0, 140_000, 997)))
+    for call, kw in ((gs.GS_WS_LINEAR_BWD, dict(W=k, H=n)), (gs.GS_WS_RMSNORM_BWD, dict(W=k))):
+        sizes = [gs.gs_workspace_bytes(call, r, **kw) for r in rows]
+        assert all(a <= b for a, b in zip(sizes, sizes[1:])), [(r, a, b) for r, a, b in zip(rows, sizes, sizes[1:]) if a > b][:3]
