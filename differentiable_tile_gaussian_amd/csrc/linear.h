@@ -2,9 +2,35 @@
 // variants, among which linear.hip chooses.
 #pragma once
 
+#include <atomic>
+
 #include "matrix.h"
 
 namespace gsk {
+
+// A kernel's leave to take more than the default of dynamic LDS, which belongs to a device: asked
+// for on each device that launches the kernel, and again after a refusal.
+class LdsLimit {
+ public:
+  template <class Kernel>
+  hipError_t allow(Kernel* kernel, size_t bytes) {
+    int device = 0;
+    hipError_t e = hipGetDevice(&device);
+    if (e != hipSuccess) return e;
+    const uint64_t bit = device < 64 ? uint64_t(1) << device : 0;
+    if (given_.load(std::memory_order_acquire) & bit) return hipSuccess;
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                            int(bytes));
+    if (e == hipSuccess)
+      given_.fetch_or(bit, std::memory_order_release);
+    else
+      (void)hipGetLastError();   // returned here, and not to be found by the next launch
+    return e;
+  }
+
+ private:
+  std::atomic<uint64_t> given_{0};
+};
 
 // ------------------------------------------------------------- epilogue of the forward
 

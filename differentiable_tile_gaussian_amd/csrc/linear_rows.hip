@@ -372,9 +372,8 @@ template <int KC, int NC, bool MX, int Z, int Y, int R>
 hipError_t go(const RowsArgs& a, hipStream_t s) {
   using S = Shape<KC, NC, MX, Z, Y, R>;
   const auto kernel = &rows_fwd_kernel<S>;
-  static const hipError_t allowed = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                                        hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLds);
-  if (allowed != hipSuccess) return allowed;
+  static LdsLimit limit;
+  if (const hipError_t no = limit.allow(kernel, kMaxLds); no != hipSuccess) return no;
   const int64_t turns = div_up(a.rows, 16 * S::kMT * (S::kThreads / 64));
   GSK_PROF("linear_rows_fwd", s);
   kernel<<<dim3(unsigned(blocks_for(turns, S::kLds, S::kWaves * 256 / S::kThreads)), div_up(a.n, NC * 64)), S::kThreads,
@@ -405,10 +404,8 @@ hipError_t by_columns(const RowsArgs& a, hipStream_t s) {
 
 template <int KC, bool MX, bool NARROW>
 hipError_t go_any(const RowsArgs& a, hipStream_t s) {
-  static const hipError_t allowed =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(&rows_fwd_any_kernel<KC, MX, NARROW>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLds);
-  if (allowed != hipSuccess) return allowed;
+  static LdsLimit limit;
+  if (const hipError_t no = limit.allow(&rows_fwd_any_kernel<KC, MX, NARROW>, kMaxLds); no != hipSuccess) return no;
   const int all = (a.n + 63) / 64;
   const int64_t turns = div_up(a.rows, 16 * (kAnyThreads / 64));
   const int split = split_for(turns, all), groups = (all + split - 1) / split;

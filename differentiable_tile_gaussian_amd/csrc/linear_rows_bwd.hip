@@ -395,9 +395,8 @@ template <int NC, int KC, int DY, int Z, int X, Reach HOW>
 hipError_t go(const RowsBwdArgs& a, int blocks, hipStream_t s) {
   constexpr size_t kLds = NC * KC * 8192 + size_t(kRows) * ((NC + KC) * 128 + 64);
   const auto kernel = &rows_bwd_kernel<NC, KC, DY, Z, X, HOW>;
-  static const hipError_t allowed = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                                        hipFuncAttributeMaxDynamicSharedMemorySize, int(kLds));
-  if (allowed != hipSuccess) return allowed;
+  static LdsLimit limit;
+  if (const hipError_t no = limit.allow(kernel, kLds); no != hipSuccess) return no;
   GSK_PROF("linear_rows_bwd", s);
   kernel<<<blocks, kThreads, kLds, s>>>(a);
   return hipGetLastError();

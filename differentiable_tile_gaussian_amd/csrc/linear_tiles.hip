@@ -386,9 +386,8 @@ template <int QTYPE, int QT, int D, Reach HOW>
 hipError_t go_nt(const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, const Epilogue& e, hipStream_t s) {
   constexpr int kLds = 2 * (128 + 32 * QT) * 128;
   const auto kernel = &tile_nt_kernel<QTYPE, QT, D, HOW>;
-  static const hipError_t allowed =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
-  if (allowed != hipSuccess) return allowed;
+  static LdsLimit limit;
+  if (const hipError_t no = limit.allow(kernel, kLds); no != hipSuccess) return no;
   const int ptiles = int(div_up(np, 128)), tiles = int(ptiles * int64_t(div_up(nq, 32 * QT)));
   kernel<<<(tiles + 7) / 8 * 8, kThreads, kLds, s>>>(P, Q, np, nq, nk, e, ptiles, tiles);
   return hipGetLastError();
@@ -399,9 +398,8 @@ hipError_t go_tn(const MatArg& P, const MatArg& Q, int np, int nq, int64_t rows,
                  const MatArg& out, hipStream_t s) {
   constexpr int kLds = 2 * 64 * (128 * 2 + 32 + 32 * QT * 2 + 32);
   const auto kernel = &tile_tn_kernel<PTYPE, QT, D, HOW>;
-  static const hipError_t allowed =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
-  if (allowed != hipSuccess) return allowed;
+  static LdsLimit limit;
+  if (const hipError_t no = limit.allow(kernel, kLds); no != hipSuccess) return no;
   const int ptiles = int(div_up(np, 128)), tiles = ptiles * int(div_up(nq, 32 * QT));
   const int64_t per = ((rows + slices - 1) / slices + 63) / 64 * 64;
   const unsigned blocks = unsigned(slices < 8 ? (tiles + 7) / 8 * 8 * slices : (slices + 7) / 8 * 8 * tiles);

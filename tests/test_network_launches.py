@@ -1,0 +1,86 @@
+"""Which kernels the network operators launch, on which device and with which grids, by a
+stand-in for the HIP runtime (recording_runtime.cpp) in a process of its own: no GPU is used."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+LIB = os.path.join(os.path.dirname(HERE), "differentiable_tile_gaussian_amd", "libgs.so")
+
+PRELUDE = '''
+import ctypes as C, sys
+rec = C.CDLL(sys.argv[1], mode=C.RTLD_GLOBAL)
+gs = C.CDLL(sys.argv[2])
+rec.recorder_name.restype = C.c_char_p
+gs.gs_last_error.restype = C.c_char_p
+gs.gs_workspace_bytes.argtypes = [C.c_int32, C.c_int64, C.c_uint32, C.c_int32, C.c_int32, C.c_void_p]
+gs.gs_workspace_bytes.restype = C.c_size_t
+F32, BF16, MX8 = 0, 1, 2
+
+class Matrix(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("scales", C.c_void_p), ("rows", C.c_int64), ("cols", C.c_int64), ("ld", C.c_int64),
+                ("scales_ld", C.c_int64), ("type", C.c_int32)]
+
+at = [1 << 40]
+def m(rows, cols, kind=BF16):
+    at[0] += 1 << 44
+    return C.byref(Matrix(at[0], at[0] + (1 << 43) if kind == MX8 else None, rows, cols, (cols + 15) // 16 * 16, (cols + 31) // 32, kind))
+
+def kernels(status=0):
+    """The launches since the last look: (mangled name, blocks along x, device)."""
+    out = [(rec.recorder_name(i).decode(), rec.recorder_blocks(i) & 0xffffffff, rec.recorder_launch_device(i))
+           for i in range(rec.recorder_launches())]
+    rec.recorder_clear()
+    return out
+
+def fwd(rows, k, n, xk=BF16, z=None, y=BF16):
+    return gs.gs_linear_fwd(m(rows, k, xk), m(n, k), None, 2, None, z and m(rows, n, z), m(rows, n, y), None)
+
+def bwd(rows, k, n, z=None, act=0, xk=BF16):
+    need = gs.gs_workspace_bytes(9, rows, 0, k, n, None)
+    return gs.gs_linear_bwd(m(rows, n), m(rows, n, z) if z is not None else None, act, m(rows, k, xk), m(n, k), m(rows, k), m(n, k, F32), C.c_void_p(1 << 50),
+                            C.c_void_p(1 << 51), C.c_size_t(need), None)
+
+def ok(status):
+    assert status == 0, gs.gs_last_error()
+    return kernels()
+'''
+
+
+@pytest.fixture(scope="module")
+def recorder(tmp_path_factory):
+    if not os.path.exists(LIB):
+        pytest.skip("libgs.so is not built")
+    out = str(tmp_path_factory.mktemp("recorder") / "recorder.so")
+    subprocess.run(["g++", "-O1", "-std=c++17", "-shared", "-fPIC", os.path.join(HERE, "recording_runtime.cpp"), "-o", out], check=True)
+
+    def run(script):
+        r = subprocess.run([sys.executable, "-c", PRELUDE + script, out, LIB], capture_output=True, text=True, timeout=60)
+        assert r.returncode == 0, r.stdout + r.stderr
+        return r.stdout
+    return run
+
+
+def test_every_device_is_allowed_the_lds(recorder):
+    """Each kernel that takes more than 64 KiB of LDS is allowed it on every device that calls,
+    once, and a refusal is an error of that call alone."""
+    recorder('''
+calls = {"rows_fwd_kernel": lambda: fwd(100000, 256, 256), "rows_fwd_any_kernel": lambda: fwd(100000, 255, 255),
+         "rows_bwd_kernel": lambda: bwd(1000, 128, 128), "tile_nt_kernel": lambda: fwd(8160, 1024, 4096),
+         "tile_tn_kernel": lambda: bwd(8160, 1024, 4096)}
+for name, call in calls.items():
+    for device in (0, 1, 7):
+        rec.recorder_device(device)
+        launched = ok(call())
+        assert any(name in k for k, _, _ in launched) and all(d == device for _, _, d in launched), (name, launched)
+        before = rec.recorder_attributes()
+        ok(call())
+        assert rec.recorder_attributes() == before, name
+    rec.recorder_device(3)
+    rec.recorder_refuse_attributes(1)
+    assert call() == -4 and gs.gs_last_error(), name
+    kernels()
+    ok(call())
+''')
