@@ -323,6 +323,27 @@ __host__ __device__ constexpr uint32_t element_bytes(int type) {
   return type == GS_MAT_F32 ? 4 : type == GS_MAT_BF16 ? 2 : 1;
 }
 
+// The matrix's rows from `row` on.
+inline MatArg rows_from(MatArg m, int64_t row) {
+  if (m.p) m.p += row * m.ld * element_bytes(m.type);
+  if (m.s) m.s += row * m.lds;
+  return m;
+}
+
+// A launch has fewer than 2^32 threads along x: the most blocks of 256, beyond which the rows
+// are taken by several launches.
+constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;
+
+// launch(first, count, blocks) for parts of the rows, per_block of them to a block.
+template <class Launch>
+inline void for_row_parts(int64_t rows, int64_t per_block, Launch launch) {
+  const int64_t most = kMaxBlocks * per_block;
+  for (int64_t first = 0; first < rows; first += most) {
+    const int64_t count = rows - first < most ? rows - first : most;
+    launch(first, count, div_up(count, per_block));
+  }
+}
+
 // Whether a matrix can be taken through buffers: rows start at multiples of 4 bytes, and 256
 // rows (at most what a block spans from its base) stay within the descriptor's range.
 inline bool buffer_ok(const MatArg& m) {

@@ -75,29 +75,27 @@ int lanes_for(int cols) {
   return lanes;
 }
 
-dim3 blocks_for(int64_t rows, int cols, int lanes) {
-  return dim3(div_up(rows, int64_t(kThreads / lanes) * kRows), div_up(cols, lanes * 8));
-}
-
 }  // namespace
 
 hipError_t launch_mx8_pack(const MatArg& x, const MatArg& q, int64_t rows, int cols, hipStream_t s) {
   const int lanes = lanes_for(cols);
   GSK_PROF("mx8_pack", s);
-  if (cols < 8)
-    mx8_pack_kernel<true><<<blocks_for(rows, cols, lanes), kThreads, 0, s>>>(x, q, rows, cols, lanes);
-  else
-    mx8_pack_kernel<false><<<blocks_for(rows, cols, lanes), kThreads, 0, s>>>(x, q, rows, cols, lanes);
+  for_row_parts(rows, kThreads / lanes * kRows, [&](int64_t first, int64_t count, unsigned blocks) {
+    const auto kernel = cols < 8 ? &mx8_pack_kernel<true> : &mx8_pack_kernel<false>;
+    kernel<<<dim3(blocks, div_up(cols, lanes * 8)), kThreads, 0, s>>>(rows_from(x, first), rows_from(q, first), count, cols,
+                                                                     lanes);
+  });
   return hipGetLastError();
 }
 
 hipError_t launch_mx8_unpack(const MatArg& q, const MatArg& x, int64_t rows, int cols, hipStream_t s) {
   const int lanes = lanes_for(cols);
   GSK_PROF("mx8_unpack", s);
-  if (cols < 8)
-    mx8_unpack_kernel<true><<<blocks_for(rows, cols, lanes), kThreads, 0, s>>>(q, x, rows, cols, lanes);
-  else
-    mx8_unpack_kernel<false><<<blocks_for(rows, cols, lanes), kThreads, 0, s>>>(q, x, rows, cols, lanes);
+  for_row_parts(rows, kThreads / lanes * kRows, [&](int64_t first, int64_t count, unsigned blocks) {
+    const auto kernel = cols < 8 ? &mx8_unpack_kernel<true> : &mx8_unpack_kernel<false>;
+    kernel<<<dim3(blocks, div_up(cols, lanes * 8)), kThreads, 0, s>>>(rows_from(q, first), rows_from(x, first), count, cols,
+                                                                     lanes);
+  });
   return hipGetLastError();
 }
 

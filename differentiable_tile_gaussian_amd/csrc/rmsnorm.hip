@@ -376,11 +376,23 @@ void by_width(int cols, const Args& a, unsigned blocks, hipStream_t s) {
   }
 }
 
+template <class Kernel>
+void launch_fwd(Kernel* kernel, int64_t per_block, const NormFwdArgs& a, hipStream_t s) {
+  for_row_parts(a.rows, per_block, [&](int64_t first, int64_t count, unsigned blocks) {
+    NormFwdArgs p = a;
+    for (MatArg NormFwdArgs::*m : {&NormFwdArgs::x, &NormFwdArgs::r, &NormFwdArgs::h, &NormFwdArgs::ckpt, &NormFwdArgs::y})
+      p.*m = rows_from(a.*m, first);
+    if (a.rstd) p.rstd = a.rstd + first;
+    p.rows = count;
+    kernel<<<blocks, kThreads, 0, s>>>(p);
+  });
+}
+
 template <int L, int C, bool NARROW>
 struct Fwd {
   static void go(const NormFwdArgs& a, unsigned, hipStream_t s) {
     constexpr int kRows = C == 1 ? 2 : 1;
-    rmsnorm_fwd_kernel<L, C, kRows, NARROW><<<div_up(a.rows, kThreads / L * kRows), kThreads, 0, s>>>(a);
+    launch_fwd(&rmsnorm_fwd_kernel<L, C, kRows, NARROW>, kThreads / L * kRows, a, s);
   }
 };
 template <int L, int C, bool NARROW>
@@ -476,7 +488,7 @@ hipError_t launch_rmsnorm_fwd(const MatArg& x, const MatArg& r, const float* w, 
   const NormFwdArgs a{x, r, h, ckpt, y, w, rstd, eps, 1.0f / float(cols), rows, cols};
   GSK_PROF("rmsnorm_fwd", s);
   if (wide(cols)) {
-    rmsnorm_fwd_wide_kernel<<<div_up(rows, kThreads / 64), kThreads, 0, s>>>(a);
+    launch_fwd(&rmsnorm_fwd_wide_kernel, kThreads / 64, a, s);
   } else {
     by_width<Fwd>(cols, a, 0, s);
   }
@@ -496,7 +508,14 @@ hipError_t launch_rmsnorm_bwd(const MatArg& dy, const MatArg& h, const float* w,
   if (wide(cols)) {
     if (rows > 0) {
       GSK_PROF("rmsnorm_bwd", s);
-      rmsnorm_bwd_wide_kernel<<<div_up(rows, kThreads / 64), kThreads, 0, s>>>(a);
+      for_row_parts(rows, kThreads / 64, [&](int64_t first, int64_t count, unsigned n) {
+        NormBwdArgs p = a;
+        for (MatArg NormBwdArgs::*m : {&NormBwdArgs::dy, &NormBwdArgs::h, &NormBwdArgs::dres, &NormBwdArgs::dh})
+          p.*m = rows_from(a.*m, first);
+        p.rstd = a.rstd + first;
+        p.rows = count;
+        rmsnorm_bwd_wide_kernel<<<n, kThreads, 0, s>>>(p);
+      });
     }
     if (dweight) {
       GSK_PROF("rmsnorm_dw", s);

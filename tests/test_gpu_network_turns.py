@@ -174,3 +174,34 @@ def test_rmsnorm_forward_and_packing(gs, rows, cols):
     b2 = torch.empty_like(back)
     gs.gs_mx8_unpack(again, b2)
     assert torch.equal(back, b2)
+
+
+def test_rows_of_several_launches(gs):
+    """The most rows there are, of one column: more than one launch takes, in place and not."""
+    rows, step = (1 << 31) - 1, 1 << 28
+    x = torch.empty((rows, 1), dtype=torch.bfloat16, device="cuda")
+    for a in range(0, rows, step):
+        x[a:a + step].normal_(generator=device_rng("launches", a))
+
+    def eight(n):
+        return gs.Mx8(torch.empty((n, 1), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn),
+                      torch.empty((n, 1), dtype=torch.uint8, device="cuda").view(torch.float8_e8m0fnu))
+    q, w = eight(rows), torch.full((1,), 1.5, device="cuda")
+    gs.gs_mx8_pack(x, q)
+    back, h, rstd = torch.empty_like(x), torch.empty_like(x), torch.empty(rows, device="cuda")
+    gs.gs_mx8_unpack(q, back)
+    y = torch.empty_like(x)
+    gs.gs_rmsnorm_fwd(x, w, EPS, y, rstd, residual=back, h=h)
+    for a in range(0, rows, step):
+        n = min(step, rows - a)
+        print("rows", a, n, flush=True)
+        part, b, hh, yy, r = eight(n), *(torch.empty((n, 1), dtype=torch.bfloat16, device="cuda") for _ in range(3)), \
+            torch.empty(n, device="cuda")
+        gs.gs_mx8_pack(x[a:a + n], part)
+        gs.gs_mx8_unpack(part, b)
+        gs.gs_rmsnorm_fwd(x[a:a + n], w, EPS, yy, r, residual=b, h=hh)
+        for whole, own in ((q.q.view(torch.uint8), part.q.view(torch.uint8)), (q.scales.view(torch.uint8), part.scales.view(torch.uint8)),
+                           (back, b), (h, hh), (y, yy), (rstd, r)):
+            assert torch.equal(whole[a:a + n], own), a
+    gs.gs_rmsnorm_fwd(x, w, EPS, y, residual=back, h=back)
+    assert torch.equal(back, h)

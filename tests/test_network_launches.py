@@ -84,3 +84,29 @@ for name, call in calls.items():
     kernels()
     ok(call())
 ''')
+
+
+def test_grids_for_the_most_rows(recorder):
+    """Rows up to 2^31 - 1, the range that the header gives: no launch of 2^32 threads, and as
+    many blocks as the rows take."""
+    recorder('''
+ROWS = (1 << 31) - 1
+def norm(rows, cols, yk, ckpt, residual):
+    return gs.gs_rmsnorm_fwd(m(rows, cols), m(rows, cols) if residual else None, C.c_void_p(1 << 50), C.c_float(1e-6), None,
+                             m(rows, cols, MX8) if ckpt else None, m(rows, cols, yk), C.c_void_p(1 << 51), None)
+# columns and rows a block: 4 to 64 lanes a row and the whole block, one and two chunks a lane
+for cols, pack_rows, norm_rows in ((1, 128, 128), (7, 128, 128), (32, 128, 128), (64, 64, 64), (128, 32, 32), (256, 16, 16),
+                                   (512, 8, 8), (1024, 8, 4), (2048, 8, 2), (4096, 8, 1), (4097, 8, 4)):
+    for call, per in ((lambda: gs.gs_mx8_pack(m(ROWS, cols), m(ROWS, cols, MX8), None), pack_rows),
+                      (lambda: gs.gs_mx8_unpack(m(ROWS, cols, MX8), m(ROWS, cols), None), pack_rows),
+                      (lambda: norm(ROWS, cols, BF16, False, False), norm_rows),
+                      (lambda: norm(ROWS, cols, MX8, True, True), norm_rows)):
+        launched = ok(call())
+        assert sum(b for _, b, _ in launched) * per >= ROWS, (cols, launched)
+    norm_bwd = gs.gs_rmsnorm_bwd(m(ROWS, cols), m(ROWS, cols, MX8), C.c_void_p(1 << 50), C.c_void_p(1 << 51), None, m(ROWS, cols), C.c_void_p(1 << 52),
+                                 C.c_void_p(1 << 53), C.c_size_t(1 << 40), None)
+    ok(norm_bwd)
+for k, n in ((1, 1), (16, 16), (64, 64), (128, 128), (256, 256), (5, 200)):
+    ok(fwd(ROWS, k, n))
+    ok(bwd(ROWS, k, n))
+''')
