@@ -129,7 +129,8 @@ hipError_t launch_rows_fwd(const MatArg& x, const MatArg& w, const Epilogue& e, 
                            hipStream_t s);
 
 // ---- linear_rows_bwd.hip: the gradients of the narrowest of them in one pass
-bool rows_bwd_takes(int k, int n);
+bool rows_bwd_takes(int k, int n);   // by the widths alone
+bool rows_bwd_runs(const MatArg& dy, const MatArg& z, int act, const MatArg& x, const MatArg& dx, int k, int n);
 size_t rows_bwd_ws_bytes(int64_t rows, int k, int n);
 hipError_t launch_rows_bwd(const MatArg& dy, const MatArg& z, int act, const MatArg& x, const MatArg& w,
                            const MatArg& dx, const MatArg& dw, float* dbias, int64_t rows, int k, int n, void* ws,

@@ -168,14 +168,19 @@ hipError_t launch_linear_fwd(const MatArg& x, const MatArg& w, const float* bias
   return launch_nt("linear_fwd", w, x, n, rows, k, e, s);
 }
 
+// Where the types and addresses decide between the two ways, for either.
 size_t linear_bwd_ws_bytes(int64_t rows, int k, int n) {
-  return rows_bwd_takes(k, n) ? rows_bwd_ws_bytes(rows, k, n) : carve_bwd(nullptr, rows, k, n).bytes;
+  const size_t one = rows_bwd_takes(k, n) ? rows_bwd_ws_bytes(rows, k, n) : 0;
+  if (one && n <= 128) return one;
+  const size_t steps = carve_bwd(nullptr, rows, k, n).bytes;
+  return one > steps ? one : steps;
 }
 
 hipError_t launch_linear_bwd(const MatArg& dy, const MatArg& z, int act, const MatArg& x, const MatArg& w,
                              const MatArg& dx, const MatArg& dw, float* dbias, int64_t rows, int k, int n, void* ws,
                              hipStream_t s) {
-  if (rows_bwd_takes(k, n)) return launch_rows_bwd(dy, z, act, x, w, dx, dw, dbias, rows, k, n, ws, s);
+  if (rows_bwd_runs(dy, z, act, x, dx, k, n))
+    return launch_rows_bwd(dy, z, act, x, w, dx, dw, dbias, rows, k, n, ws, s);
   const BwdWs b = carve_bwd(ws, rows, k, n);
   // dz in memory: as the activation makes it, or a float32 dy rounded once for both products
   const bool own_dz = (act != GS_ACT_NONE || dy.type == GS_MAT_F32) && (dx.p || dw.p);

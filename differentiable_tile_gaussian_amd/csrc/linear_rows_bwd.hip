@@ -415,19 +415,28 @@ hipError_t by_z(const RowsBwdArgs& a, int blocks, hipStream_t s) {
                                 : by_x<NC, KC, DY, GS_MAT_BF16, HOW>(a, blocks, s);
 }
 
+// Whole 16-column pieces in buffers' reach.
+bool whole(const MatArg& dy, const MatArg& z, int act, const MatArg& x, const MatArg& dx, int k, int n) {
+  return k % 16 == 0 && n % 16 == 0 && buffer_ok(dy) && buffer_ok(x) && buffer_ok(dx) &&
+         (act == GS_ACT_NONE || buffer_ok(z));
+}
+
 // The types are compiled in (but for a float32 z and for widths below 16, which take one
-// kernel that reads them from the arguments); whole 16-column pieces in buffers' reach have
-// kernels of their own (500k rows 99 to 113 by the kernel for any type: 407 us, with
-// the types compiled in 144).
+// kernel that reads them from the arguments); whole pieces have kernels of their own (500k
+// rows 99 to 113 by the kernel for any type: 407 us, with the types compiled in 144).
 template <int NC, int KC>
 hipError_t by_type(const RowsBwdArgs& a, int blocks, hipStream_t s) {
-  if (a.k < 16 || a.n < 16 || (a.act != GS_ACT_NONE && a.z.type == GS_MAT_F32))
-    return go<NC, KC, kAny, kAny, kAny, kNarrow>(a, blocks, s);
-  const bool whole = a.k % 16 == 0 && a.n % 16 == 0 && buffer_ok(a.dy) && buffer_ok(a.x) && buffer_ok(a.dx) &&
-                     (a.act == GS_ACT_NONE || buffer_ok(a.z));
-  if (a.dy.type == GS_MAT_F32)
-    return whole ? by_z<NC, KC, GS_MAT_F32, kWhole>(a, blocks, s) : by_z<NC, KC, GS_MAT_F32, kHeldIn>(a, blocks, s);
-  return whole ? by_z<NC, KC, GS_MAT_BF16, kWhole>(a, blocks, s) : by_z<NC, KC, GS_MAT_BF16, kHeldIn>(a, blocks, s);
+  const bool f32 = a.dy.type == GS_MAT_F32;
+  if (whole(a.dy, a.z, a.act, a.x, a.dx, a.k, a.n) && (a.act == GS_ACT_NONE || a.z.type != GS_MAT_F32))
+    return f32 ? by_z<NC, KC, GS_MAT_F32, kWhole>(a, blocks, s) : by_z<NC, KC, GS_MAT_BF16, kWhole>(a, blocks, s);
+  if constexpr (NC == 4) {   // without an activation, as rows_bwd_runs has it
+    return f32 ? by_x<NC, KC, GS_MAT_F32, kNone, kHeldIn>(a, blocks, s)
+               : by_x<NC, KC, GS_MAT_BF16, kNone, kHeldIn>(a, blocks, s);
+  } else {
+    if (a.k < 16 || a.n < 16 || (a.act != GS_ACT_NONE && a.z.type == GS_MAT_F32))
+      return go<NC, KC, kAny, kAny, kAny, kNarrow>(a, blocks, s);
+    return f32 ? by_z<NC, KC, GS_MAT_F32, kHeldIn>(a, blocks, s) : by_z<NC, KC, GS_MAT_BF16, kHeldIn>(a, blocks, s);
+  }
 }
 
 // Blocks: one a turn with few rows; else as many as stay resident at once, each of at least
@@ -443,11 +452,20 @@ int shares(int k, int n) { return k <= 64 && n <= 64 ? 2 : 1; }
 
 }  // namespace
 
-// Up to four tiles of 64 x 64 of dW, what the registers hold (500k rows 256 to 64: 114 us, by
-// dz, dx and dW in turn 175; 64 to 256: 190 and 258).  Inputs below 16 columns take the kernel
-// for any type, whose registers do not hold four groups of dz (5 to 200: 618 us and 300).
+// Up to four tiles of 64 x 64 of dW (500k rows 256 to 64: 135 us without an activation, by dz, dx
+// and dW in turn 170; 64 to 256: 96 and 167).  Inputs below 16 columns take the kernel for any
+// type, whose registers do not hold four groups of dz (5 to 200: 618 us and 300).
 bool rows_bwd_takes(int k, int n) {
   return (k <= 128 && n <= 128) || (k <= 256 && n <= 64) || (k >= 16 && k <= 64 && n <= 256);
+}
+
+// Four groups of dz with an activation beside dW's tiles are more than the registers hold.  In
+// whole pieces with z in 8 or 16 bits the spills cost less than dz's way through memory (500k rows 64
+// to 256, silu: 167-198 us, by dz, dx and dW in turn 263-291), moved pieces and a float32 z more
+// (45 to 201: 302-354 us and 261-292; 64 to 256 with a float32 z 660 and 348).
+bool rows_bwd_runs(const MatArg& dy, const MatArg& z, int act, const MatArg& x, const MatArg& dx, int k, int n) {
+  return rows_bwd_takes(k, n) &&
+         (n <= 128 || act == GS_ACT_NONE || (z.type != GS_MAT_F32 && whole(dy, z, act, x, dx, k, n)));
 }
 
 // No less than fewer rows take: the blocks are up to 128 for 128 turns and fall to 65 for one more.

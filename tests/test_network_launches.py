@@ -110,3 +110,22 @@ for k, n in ((1, 1), (16, 16), (64, 64), (128, 128), (256, 256), (5, 200)):
     ok(fwd(ROWS, k, n))
     ok(bwd(ROWS, k, n))
 ''')
+
+
+def test_many_outputs_with_an_activation(recorder):
+    """129 outputs on against 16 to 64 inputs go in one pass over the rows, but with an activation
+    only in whole 16-column pieces and with z in 8 or 16 bits: other kernels would not hold their
+    values in registers.  The workspace is enough for either way."""
+    recorder('''
+for k, n in ((16, 144), (64, 256), (45, 201), (33, 129), (48, 130)):
+    for rows in (1, 300, 20000, 100000):
+        dz = (rows * ((n + 7) // 8 * 8) * 2 + 255) // 256 * 256
+        assert gs.gs_workspace_bytes(9, rows, 0, k, n, None) >= dz + k * ((n + 7) // 8 * 8) * 2, (k, n, rows)
+        for z, act in ((F32, 2), (F32, 1), (F32, 0), (BF16, 2), (MX8, 3), (MX8, 0), (None, 0)):
+            one_pass = act == 0 or z != F32 and k % 16 == 0 and n % 16 == 0
+            names = [name for name, _, _ in ok(bwd(rows, k, n, z, act))]
+            assert any("rows_bwd_kernel" in name for name in names) == one_pass, (k, n, rows, z, act, names)
+            assert any("transpose_kernel" in name for name in names) != one_pass, (k, n, rows, z, act, names)
+for k, n in ((64, 128), (128, 128), (256, 64), (5, 5), (99, 113)):
+    assert any("rows_bwd_kernel" in name for name, _, _ in ok(bwd(1000, k, n, F32, 2)))
+''')
