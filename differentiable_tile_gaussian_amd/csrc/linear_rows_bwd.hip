@@ -421,9 +421,9 @@ bool whole(const MatArg& dy, const MatArg& z, int act, const MatArg& x, const Ma
          (act == GS_ACT_NONE || buffer_ok(z));
 }
 
-// The types are compiled in (but for a float32 z and for widths below 16, which take one
-// kernel that reads them from the arguments); whole pieces have kernels of their own (500k
-// rows 99 to 113 by the kernel for any type: 407 us, with the types compiled in 144).
+// The types are compiled in, but for widths below 16, which take one kernel that reads them
+// from the arguments; whole pieces have kernels of their own (500k rows 99 to 113 by the kernel
+// for any type: 407 us, with the types compiled in 144; 128 to 128 with a float32 z 257 and 166).
 template <int NC, int KC>
 hipError_t by_type(const RowsBwdArgs& a, int blocks, hipStream_t s) {
   const bool f32 = a.dy.type == GS_MAT_F32;
@@ -433,8 +433,12 @@ hipError_t by_type(const RowsBwdArgs& a, int blocks, hipStream_t s) {
     return f32 ? by_x<NC, KC, GS_MAT_F32, kNone, kHeldIn>(a, blocks, s)
                : by_x<NC, KC, GS_MAT_BF16, kNone, kHeldIn>(a, blocks, s);
   } else {
-    if (a.k < 16 || a.n < 16 || (a.act != GS_ACT_NONE && a.z.type == GS_MAT_F32))
-      return go<NC, KC, kAny, kAny, kAny, kNarrow>(a, blocks, s);
+    if constexpr (NC == 1 || KC == 1) {
+      if (a.k < 16 || a.n < 16) return go<NC, KC, kAny, kAny, kAny, kNarrow>(a, blocks, s);
+    }
+    if (a.act != GS_ACT_NONE && a.z.type == GS_MAT_F32)
+      return f32 ? by_x<NC, KC, GS_MAT_F32, GS_MAT_F32, kHeldIn>(a, blocks, s)
+                 : by_x<NC, KC, GS_MAT_BF16, GS_MAT_F32, kHeldIn>(a, blocks, s);
     return f32 ? by_z<NC, KC, GS_MAT_F32, kHeldIn>(a, blocks, s) : by_z<NC, KC, GS_MAT_BF16, kHeldIn>(a, blocks, s);
   }
 }

@@ -129,3 +129,16 @@ for k, n in ((16, 144), (64, 256), (45, 201), (33, 129), (48, 130)):
 for k, n in ((64, 128), (128, 128), (256, 64), (5, 5), (99, 113)):
     assert any("rows_bwd_kernel" in name for name, _, _ in ok(bwd(1000, k, n, F32, 2)))
 ''')
+
+
+def test_the_kernel_for_any_type_is_for_narrow_widths(recorder):
+    """From 16 columns on both sides the types are compiled in, a float32 z among them."""
+    recorder('''
+def any_type(rows, k, n, z, act):
+    name, = {name for name, _, _ in ok(bwd(rows, k, n, z, act)) if "rows_bwd_kernel" in name}
+    return "ELin1ELin1ELin1E" in name       # the three types are the argument -1
+for k, n in ((16, 16), (64, 48), (128, 128), (99, 113), (256, 64), (64, 128)):
+    for z, act in ((F32, 2), (BF16, 1), (MX8, 3), (None, 0)):
+        assert not any_type(1000, k, n, z, act), (k, n, z, act)
+assert any_type(1000, 15, 64, BF16, 2) and any_type(1000, 64, 15, F32, 2)
+''')
