@@ -54,7 +54,7 @@ class FeatureDecoder:
     def _reserve(self, rows):
         if rows == self.rows:
             return
-        self.rows = rows
+        self.rows = -1   # until all of them are there
         w, n, dev, bf = self.width, self.hidden, self.device, torch.bfloat16
 
         def buf(cols, dtype=bf):
@@ -74,6 +74,7 @@ class FeatureDecoder:
                                   gs.gs_workspace_bytes(gs.GS_WS_LINEAR_BWD, rows, W=w, H=self.outputs),
                                   gs.gs_workspace_bytes(gs.GS_WS_RMSNORM_BWD, rows, W=w)),
                               dtype=torch.uint8, device=dev)
+        self.rows = rows
 
     def forward(self, x, base=None):
         """x [rows][width] (float32 or bfloat16) -> [rows][outputs] float32, plus base if given
