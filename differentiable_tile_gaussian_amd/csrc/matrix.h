@@ -136,23 +136,6 @@ __device__ inline uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
-// The chunk as bfloat16 operands of a matrix product: float32 rounds, the others are exact.
-__device__ inline u32x4 raw8_to_bf16(const Raw8& r, int type) {
-  if (type == GS_MAT_BF16) return r.lo;
-  if (type == GS_MAT_F32) {
-    u32x4 o;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      o[i] = pack_bf16(__uint_as_float(r.lo[2 * i]), __uint_as_float(r.lo[2 * i + 1]));
-      o[2 + i] = pack_bf16(__uint_as_float(r.hi[2 * i]), __uint_as_float(r.hi[2 * i + 1]));
-    }
-    return o;
-  }
-  const float s = mx8_scale(r.scale);
-  const u32x2 a = mx8_to_bf16x4(r.lo[0], s), b = mx8_to_bf16x4(r.lo[1], s);
-  return u32x4{a[0], a[1], b[0], b[1]};
-}
-
 // ---- rows of at least 8 columns, 8 to a lane, without branches
 //
 // A row is held by neighbouring lanes, lane l's chunk starting at column 8 l.  A chunk that
@@ -302,17 +285,11 @@ __device__ inline Buffer buffer_at(const void* p) {
 __device__ inline u32x4 buffer_load16(Buffer b, uint32_t off) {
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, int(off), 0, 0));
 }
-__device__ inline u32x2 buffer_load8(Buffer b, uint32_t off) {
-  return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(b, int(off), 0, 0));
-}
 __device__ inline uint32_t buffer_load1(Buffer b, uint32_t off) {
   return uint32_t(uint8_t(__builtin_amdgcn_raw_buffer_load_b8(b, int(off), 0, 0)));
 }
 __device__ inline void buffer_store16(Buffer b, uint32_t off, u32x4 v) {
   __builtin_amdgcn_raw_buffer_store_b128(v, b, int(off), 0, 0);
-}
-__device__ inline void buffer_store8(Buffer b, uint32_t off, u32x2 v) {
-  __builtin_amdgcn_raw_buffer_store_b64(v, b, int(off), 0, 0);
 }
 __device__ inline void buffer_store1(Buffer b, uint32_t off, uint32_t v) {
   __builtin_amdgcn_raw_buffer_store_b8(uint8_t(v), b, int(off), 0, 0);

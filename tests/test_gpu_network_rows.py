@@ -96,3 +96,27 @@ def test_bad_rows_reach_no_other(gs, k, n, kind):
     assert torch.equal(y[0][keep], y[1][keep])
     assert torch.equal(z[0].q.view(torch.uint8)[keep], z[1].q.view(torch.uint8)[keep])
     assert torch.equal(z[0].scales.view(torch.uint8)[keep], z[1].scales.view(torch.uint8)[keep])
+
+
+@pytest.mark.parametrize("cols", [32, 59, 64, 200])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_a_bad_element_reaches_no_other(gs, cols, value, kind):
+    """In 8 bits it becomes NaN; all other elements and all scales keep their bits, in its own
+    block too (it is not the block's largest finite element, which sets the scale)."""
+    g = rng("badelement", cols)
+    x = normal(g, 24, cols)
+    bad = x.clone()
+    at = [(int(r), int(c)) for r, c in zip(torch.randperm(24, generator=g)[:8], torch.randint(cols, (8,), generator=g))]
+    for r, c in at:
+        b = c // 32 * 32
+        top = int(x[r, b:b + 32].abs().argmax()) + b
+        assert cols - b > 1
+        bad[r, (c if c != top else b if top != b else b + 1)] = value
+    q = [gs.mx8_empty(24, cols) for _ in range(2)]
+    for v, m in zip((x, bad), q):
+        gs.gs_mx8_pack(given(gs, v, kind)[0], m)
+    hit = ~torch.isfinite(bad).cuda()
+    a, b = (m.q.view(torch.uint8) for m in q)
+    assert int(hit.sum()) == 8 and ((b[hit] & 0x7f) == 0x7f).all() and torch.equal(a[~hit], b[~hit])
+    assert torch.equal(q[0].scales.view(torch.uint8), q[1].scales.view(torch.uint8))
