@@ -205,3 +205,25 @@ def test_rows_of_several_launches(gs):
             assert torch.equal(whole[a:a + n], own), a
     gs.gs_rmsnorm_fwd(x, w, EPS, y, residual=back, h=back)
     assert torch.equal(back, h)
+
+
+@pytest.mark.parametrize("rows,k,n", [(400_003, 128, 128), (400_003, 64, 48), (200_003, 99, 113), (100_003, 256, 256), (4000, 128, 128),
+                                      (3000, 1024, 256), (8160, 1024, 1024), (16, 1024, 1024)])
+def test_sums_are_those_of_32_bits(gs, rows, k, n):
+    """z from exact operands is no farther from its value than a float32 product of them with the
+    bias added, small z included, whose roundings to 8 bits show it first (1.25: the scatter of
+    the two, from as few as 16384 values)."""
+    print("sums", rows, k, n, flush=True)
+    g = device_rng("sums", rows, k, n)
+    x, x64 = given(gs, normal(g, rows, k) * torch.exp(0.5 * normal(g, 1, k)) + normal(g, 1, k, scale=0.2), "mx8")
+    w, w64 = given(gs, normal(g, n, k, scale=k ** -0.5), "bf16")
+    b = normal(g, n, scale=0.1)
+    y, z = output(gs, rows, n, "bf16"), output(gs, rows, n, "f32")
+    gs.gs_linear_fwd(x, w, y, bias=b, z=z)
+    e = matmul_t(x64, w64) + b.double()
+    p = matmul_t(x64.float(), w.float()) + b
+    rms = e.square().mean().sqrt()
+    for at in (e.abs() < 0.3 * rms, e.abs() >= 0.3 * rms):
+        own, plain = ((v.double() - e)[at].square().mean().sqrt() / rms for v in (z, p))
+        print("   error over the values' size: %.3g, a float32 product's %.3g" % (own, plain))
+        assert own <= 1.25 * plain, (float(own), float(plain))
