@@ -9,7 +9,7 @@
 // columns 16 g + 4 t + i, so that a lane's four tiles are 16 consecutive columns of one row:
 // wide stores, and half an MX8 block.
 //
-// 1M rows 128 to 128 from MX8, silu, z kept in MX8: 116-130 us over runs (520 MB, 4.0-4.5
+// 1M rows 128 to 128 from MX8, silu, z kept in MX8: 116-132 us over runs (520 MB, 3.9-4.5
 // TB/s; the same reads and writes alone 105 us: two write streams and a read stream, where a
 // copy has one of each).
 #include "linear.h"
@@ -298,7 +298,9 @@ __global__ void __launch_bounds__(S::kThreads, S::kWaves) rows_fwd_kernel(RowsAr
 }
 
 // Any width, alignment and types: the same products, the pieces moved into place and the
-// stores piece by piece.
+// stores piece by piece.  1M rows 99 to 113 from bfloat16: 142 us (3.0 TB/s; from MX8 with silu
+// and an MX8 z 203, 2.2 TB/s), 35 to 59 with a float32 y 120, 7 to 64 85, 300k rows 201 to 255
+// 122: bounded by the vector work of moving pieces and by short stores that do not fill lines.
 constexpr int kAnyThreads = 256;
 
 template <int KC, bool MX, bool NARROW>
@@ -428,7 +430,12 @@ hipError_t go_any(const RowsArgs& a, hipStream_t s) {
 }
 
 // The fast kernel's conditions: whole 16-column pieces, buffers, and one of the combinations
-// of outputs that a network makes (a kept MX8 z, or a residual of y's type, or neither).
+// of outputs that a network makes (a kept MX8 z, or a residual of y's type, or neither; by the
+// kernel for any width 1M rows 128 to 128 take 167 us for 134, 199 for 143 and 119 for 106; 300k
+// rows 256 to 256 100 for 80).  The others go to that kernel: each would be 18 more kernels, and
+// takes 1.3 to 2.1 times its bytes at a copy's rate (a bfloat16 z 169 us and 119, an MX8 z and a
+// residual 242 and 144, an MX8 z and a float32 y 303 and 144, a float32 residual and a bfloat16 y 246
+// and 190).
 bool fast(const RowsArgs& a) {
   const Epilogue& e = a.e;
   if (a.k % 16 || a.n % 16 || !buffer_ok(a.x) || !buffer_ok(e.y) || !buffer_ok(e.z) || !buffer_ok(e.r)) return false;

@@ -11,7 +11,7 @@
 // products of the present one.  Each block writes its sums of dW and db once; they are joined
 // in order by launch_sum_parts.
 //
-// 1M rows 128 to 128, z and x in 8 bits, silu: 185 us (776 MB, 4.2 TB/s) and 8 us for the sums;
+// 1M rows 128 to 128, z and x in 8 bits, silu: 185-190 us (776 MB, 4.1 TB/s) and 8 us for the sums;
 // without an activation, x in bfloat16, 141 us; 100k rows 64 to 48 with a float32 dy: 15 and
 // 4 us.  What is left is the vector work of silu's slope and of the 8-bit decodes, in turns with
 // the two products: a block's registers and LDS leave room for one block a compute unit.

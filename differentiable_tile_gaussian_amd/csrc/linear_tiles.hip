@@ -4,9 +4,11 @@
 // memory and the next step's are written to LDS while the present one is computed, so that
 // one barrier a step suffices and nothing waits for memory.
 //
-// 8160 rows, 4096 to 1024 (68 GFLOP): from bfloat16 82 us (830 TFLOP/s), from MX8 with a
-// residual 82 too; the contraction over the rows for dW (4096 x 1024): 107 us (640 TFLOP/s).  What is left
-// is LDS: a step's operands are written once and read twice by the waves beside its matrix
+// 8160 rows, 4096 to 1024 (68 GFLOP), by the clock over many calls: from bfloat16 81 us (845
+// TFLOP/s), from MX8 with a residual 81-85; the first hundreds of calls after a pause are slower
+// while the card's clock settles (from MX8 91-93 us, which a trace of 39 calls shows).  The contraction
+// over the rows for dW (4096 x 1024), in such a trace: 107 us (640 TFLOP/s).  What is left is
+// LDS: a step's operands are written once and read twice by the waves beside its matrix
 // instructions.
 #include "linear.h"
 #include "profile.h"
@@ -413,7 +415,7 @@ hipError_t launch_tile_nt(const MatArg& P, const MatArg& Q, int np, int64_t nq, 
                           hipStream_t s) {
   // One 128 x 256 block a compute unit or two of 128 x 128: a long contraction runs better on
   // the larger (8160 x 4096 to 1024: 82 us, smaller tiles 89; from MX8 the two are level, 91 and
-  // 93), but two blocks hide each other's epilogue (8160 x 1024 to 4096: 110 us and 106; with
+  // 93 in calls after a pause, so it has the smaller alone), but two blocks hide each other's epilogue (8160 x 1024 to 4096: 110 us and 106; with
   // gelu and a kept z 138 and 118).
   const bool big = nk >= 2048 && int64_t(div_up(np, 128)) * div_up(nq, 256) >= 192;
   const Reach how = nk < 16 ? kNarrow : nk % 16 == 0 && buffer_ok(P) && buffer_ok(Q) ? kWhole : kHeldIn;

@@ -4,8 +4,9 @@
 // MX8 (the microscaling format with e4m3 elements): the 32-column block b of a row holds
 // v = q 2^(scale byte - 127), with the smallest scale exponent >= -126 for which the
 // block's largest finite magnitude is at most 448 2^e (448 is e4m3's largest value).  A
-// power-of-two scale makes the decoded value exact in bfloat16 (4 significant bits), so
-// the matrix products read the decoded values without another rounding.
+// power-of-two scale makes the decoded value exact in bfloat16 (4 significant bits; from 2^-126
+// on, where its full precision ends), so the matrix products read the decoded values without
+// another rounding.
 #pragma once
 
 #include "gs_internal.h"

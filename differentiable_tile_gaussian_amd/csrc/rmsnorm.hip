@@ -7,10 +7,12 @@
 // is read once and each output written once, up to kMaxHeld columns.  Wider rows are walked
 // twice by one wave, the second time from the caches.
 //
-// Forward, 3M rows of 128 with a residual and an 8-bit output and checkpoint: 554 us (3.11 GB,
-// 5.6 TB/s, a copy's rate); one row's latency sets small calls (1024 rows of 64: 4 us).
+// Forward, 3M rows of 128 with a residual and an 8-bit output and checkpoint: 550 us (3.11 GB,
+// 5.65 TB/s, a copy's rate); one row's latency sets small calls (1024 rows of 64: 4 us).
 // Backward, 1M rows of 128: 160 us (900 MB, 5.6 TB/s) and 5 us for joining dw's sums; 8160
-// rows of 1000: 16 and 4 us.
+// rows of 1000: 16 and 4 us.  Rows that are not held are for the range, not for speed: a wave has one
+// load of each input in flight (8160 rows of 8192: forward 223 us, 2.6 times its bytes at a
+// copy's rate, backward 324, 3.3 times; one row of 2^20 columns 4.9 and 5.3 ms).
 #include "matrix.h"
 #include "profile.h"
 

@@ -462,7 +462,7 @@ enum { GS_MAT_F32 = 0, GS_MAT_BF16 = 1, GS_MAT_MX8 = 2 };
 enum { GS_ACT_NONE = 0, GS_ACT_RELU = 1, GS_ACT_SILU = 2, GS_ACT_GELU = 3 };
 
 /* x (F32 or BF16) to q (MX8) of the same size, and back (x rounded to its type; an MX8 value
- * is exact in both unless it overflows). */
+ * is exact in both unless it overflows, in BF16 from 2^-126 on). */
 int32_t gs_mx8_pack(const gs_matrix* x, const gs_matrix* q, void* stream);
 int32_t gs_mx8_unpack(const gs_matrix* q, const gs_matrix* x, void* stream);
 
