@@ -7,8 +7,11 @@
 #include <stdio.h>
 
 #include "adam_math.h"
+#include "clip.h"
 #include "gs_internal.h"
+#include "lookup.h"
 #include "matrix.h"
+#include "mx4.h"
 #include "profile.h"
 
 namespace {
@@ -151,22 +154,28 @@ int32_t finish_preprocess(gs_proj* out, int n, float znear, const PreWs& w, uint
 constexpr int64_t kMaxCols = int64_t(1) << 20;
 inline bool width_ok(int64_t c) { return c >= 1 && c <= kMaxCols; }
 
-constexpr int kF32 = 1 << GS_MAT_F32, kBF16 = 1 << GS_MAT_BF16, kMX8 = 1 << GS_MAT_MX8;
+constexpr int kF32 = 1 << GS_MAT_F32, kBF16 = 1 << GS_MAT_BF16, kMX8 = 1 << GS_MAT_MX8, kMX4 = 1 << GS_MAT_MX4;
+constexpr int64_t kMaxMx4Ld = int64_t(1) << 21;
 
-// A matrix argument's own fields; types: the accepted ones (bits kF32 | kBF16 | kMX8).
+// A matrix argument's own fields; types: the accepted ones (bits kF32 | kBF16 | kMX8 | kMX4).
 int32_t check_matrix(const gs_matrix* m, const char* name, int types) {
   if (!m) return fail(GS_ERR_INVALID_ARG, "%s is null", name);
   if (m->rows < 0 || m->rows >= (int64_t(1) << 31)) return fail(GS_ERR_INVALID_ARG, "%s: rows out of range", name);
   if (m->cols < 1) return fail(GS_ERR_INVALID_ARG, "%s: cols must be positive", name);
   if (m->cols > kMaxCols) return fail(GS_ERR_UNSUPPORTED, "%s: more than 2^20 columns", name);
-  if (m->type < GS_MAT_F32 || m->type > GS_MAT_MX8) return fail(GS_ERR_INVALID_ARG, "%s: unknown type", name);
+  if ((m->type < GS_MAT_F32 || m->type > GS_MAT_MX8) && m->type != GS_MAT_MX4)
+    return fail(GS_ERR_INVALID_ARG, "%s: unknown type", name);
   if (!((types >> m->type) & 1)) return fail(GS_ERR_UNSUPPORTED, "%s: this type is not taken here", name);
   if (m->ld < m->cols || m->ld > (int64_t(1) << 31)) return fail(GS_ERR_INVALID_ARG, "%s: ld out of range", name);
+  if (m->type == GS_MAT_MX4 && (m->ld % 32 || m->ld > kMaxMx4Ld))
+    return fail(GS_ERR_INVALID_ARG, "%s: ld must be a multiple of 32 up to 2^21", name);
   if (m->rows == 0) return GS_OK;
   if (!m->data) return fail(GS_ERR_INVALID_ARG, "%s: data is null", name);
-  const uintptr_t unit = m->type == GS_MAT_F32 ? 4 : m->type == GS_MAT_BF16 ? 2 : 1;
+  const uintptr_t unit = m->type == GS_MAT_F32 ? 4 : m->type == GS_MAT_BF16 ? 2 : m->type == GS_MAT_MX4 ? 16 : 1;
   if (reinterpret_cast<uintptr_t>(m->data) % unit) return fail(GS_ERR_INVALID_ARG, "%s: data is misaligned", name);
-  if (m->type == GS_MAT_MX8) {
+  if (m->type == GS_MAT_MX4 && m->scales_ld > kMaxMx4Ld)
+    return fail(GS_ERR_INVALID_ARG, "%s: scales_ld out of range", name);
+  if (m->type == GS_MAT_MX8 || m->type == GS_MAT_MX4) {
     if (!m->scales) return fail(GS_ERR_INVALID_ARG, "%s: scales is null", name);
     if (m->scales_ld < (m->cols + 31) / 32 || m->scales_ld > (int64_t(1) << 31))
       return fail(GS_ERR_INVALID_ARG, "%s: scales_ld out of range", name);
@@ -186,6 +195,21 @@ int32_t check_shape(const gs_matrix* m, const char* name, int types, int64_t row
 // Whether an output starts where another matrix does (the sharing a check on the host can
 // see without knowing the allocations).
 bool same_data(const gs_matrix* a, const gs_matrix* b) { return a && b && a->data && a->data == b->data; }
+
+// A table (or its gradient) with the rows taken from it, and their indices.
+int32_t check_lookup(const gs_matrix* table, const char* table_name, const gs_matrix* rows, const char* rows_name,
+                     const void* index, int32_t index_bytes, float scale) {
+  int32_t st;
+  if ((st = check_matrix(table, table_name, kF32 | kBF16)) != GS_OK) return st;
+  if (table->rows < 1) return fail(GS_ERR_INVALID_ARG, "%s: rows must be positive", table_name);
+  if ((st = check_matrix(rows, rows_name, kF32 | kBF16)) != GS_OK) return st;
+  if ((st = check_shape(rows, rows_name, kF32 | kBF16, rows->rows, table->cols)) != GS_OK) return st;
+  if (index_bytes != 4 && index_bytes != 8) return fail(GS_ERR_INVALID_ARG, "index_bytes must be 4 or 8");
+  if (rows->rows > 0 && !index) return fail(GS_ERR_INVALID_ARG, "index is null");
+  if (reinterpret_cast<uintptr_t>(index) % uintptr_t(index_bytes)) return fail(GS_ERR_INVALID_ARG, "index is misaligned");
+  if (!std::isfinite(scale)) return fail(GS_ERR_INVALID_ARG, "scale must be finite");
+  return GS_OK;
+}
 
 // An output that may be the input itself has to have its type and ld.
 int32_t check_in_place(const gs_matrix* out, const gs_matrix* in, const char* name) {
@@ -254,6 +278,8 @@ size_t gs_workspace_bytes(int32_t which_call, int64_t n, uint32_t pairs, int32_t
     case GS_WS_CAMERA_GRAD: return gsk::camera_grad_ws_bytes(n < 0 ? 0 : n);
     case GS_WS_RELOCATE: return gsk::relocate_ws_bytes(n < 0 ? 0 : n);
     case GS_WS_RMSNORM_BWD: return n >= 0 && width_ok(W) ? gsk::rmsnorm_bwd_ws_bytes(n, W) : 0;
+    case GS_WS_LOOKUP_BWD: return n >= 0 && n < (int64_t(1) << 31) && width_ok(W) ? gsk::lookup_bwd_ws_bytes(n, W) : 0;
+    case GS_WS_CLIP_GRADS: return gsk::clip_ws_bytes();
     case GS_WS_LINEAR_BWD: return n >= 0 && width_ok(W) && width_ok(H) ? gsk::linear_bwd_ws_bytes(n, W, H) : 0;
     default: return 0;
   }
@@ -775,6 +801,87 @@ int32_t gs_mx8_unpack(const gs_matrix* q, const gs_matrix* x, void* stream) {
   return GS_OK;
 }
 
+int32_t gs_mx4_pack(const gs_matrix* x, const gs_matrix* q, void* stream) {
+  g_err[0] = 0;
+  int32_t st;
+  if ((st = check_matrix(x, "x", kF32 | kBF16)) != GS_OK) return st;
+  if ((st = check_shape(q, "q", kMX4, x->rows, x->cols)) != GS_OK) return st;
+  if (same_data(x, q)) return fail(GS_ERR_INVALID_ARG, "the output is one of the inputs");
+  if (x->rows == 0) return GS_OK;
+  const hipError_t e = gsk::launch_mx4_pack(gsk::mat_arg(x), gsk::mat_arg(q), x->rows, int(x->cols), as_stream(stream));
+  if (e != hipSuccess) return hip_fail(e, "mx4_pack");
+  return GS_OK;
+}
+
+int32_t gs_mx4_unpack(const gs_matrix* q, const gs_matrix* x, void* stream) {
+  g_err[0] = 0;
+  int32_t st;
+  if ((st = check_matrix(q, "q", kMX4)) != GS_OK) return st;
+  if ((st = check_shape(x, "x", kF32 | kBF16, q->rows, q->cols)) != GS_OK) return st;
+  if (same_data(x, q)) return fail(GS_ERR_INVALID_ARG, "the output is one of the inputs");
+  if (q->rows == 0) return GS_OK;
+  const hipError_t e =
+      gsk::launch_mx4_unpack(gsk::mat_arg(q), gsk::mat_arg(x), q->rows, int(q->cols), as_stream(stream));
+  if (e != hipSuccess) return hip_fail(e, "mx4_unpack");
+  return GS_OK;
+}
+
+int32_t gs_lookup_fwd(const gs_matrix* table, const void* index, int32_t index_bytes, float scale, const gs_matrix* y,
+                      void* stream) {
+  g_err[0] = 0;
+  int32_t st;
+  if ((st = check_lookup(table, "table", y, "y", index, index_bytes, scale)) != GS_OK) return st;
+  if (same_data(y, table)) return fail(GS_ERR_INVALID_ARG, "the output is one of the inputs");
+  if (y->rows == 0) return GS_OK;
+  const hipError_t e = gsk::launch_lookup_fwd(gsk::mat_arg(table), index, index_bytes == 8, scale, gsk::mat_arg(y), y->rows,
+                                              table->rows, int(y->cols), as_stream(stream));
+  if (e != hipSuccess) return hip_fail(e, "lookup_fwd");
+  return GS_OK;
+}
+
+int32_t gs_lookup_bwd(const gs_matrix* dy, const void* index, int32_t index_bytes, float scale, const gs_matrix* dtable,
+                      void* ws, size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  int32_t st;
+  if ((st = check_lookup(dtable, "dtable", dy, "dy", index, index_bytes, scale)) != GS_OK) return st;
+  if (same_data(dy, dtable)) return fail(GS_ERR_INVALID_ARG, "the output is one of the inputs");
+  const size_t need = gsk::lookup_bwd_ws_bytes(dy->rows, int(dy->cols));
+  if (need > 0 && (!ws || ws_bytes < need)) return fail(GS_ERR_CAPACITY, "lookup_bwd workspace needs %zu bytes", need);
+  const hipError_t e = gsk::launch_lookup_bwd(gsk::mat_arg(dy), index, index_bytes == 8, scale, gsk::mat_arg(dtable),
+                                              dy->rows, dtable->rows, int(dy->cols), ws, as_stream(stream));
+  if (e != hipSuccess) return hip_fail(e, "lookup_bwd");
+  return GS_OK;
+}
+
+int32_t gs_clip_grads(const gs_matrix* grads, const gs_matrix* out, int32_t count, double max_norm, float* norm, void* ws,
+                      size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  if (count < 0 || count > GS_CLIP_MAX) return fail(GS_ERR_INVALID_ARG, "count must be 0..%d", GS_CLIP_MAX);
+  if (count > 0 && !grads) return fail(GS_ERR_INVALID_ARG, "grads is null");
+  if (!norm) return fail(GS_ERR_INVALID_ARG, "norm is null");
+  if (!(max_norm > 0.0)) return fail(GS_ERR_INVALID_ARG, "max_norm must be positive");
+  int32_t st;
+  char name[32];
+  for (int i = 0; i < count; ++i) {
+    snprintf(name, sizeof name, "grads[%d]", i);
+    if ((st = check_matrix(&grads[i], name, kF32 | kBF16)) != GS_OK) return st;
+    if (!out) continue;
+    snprintf(name, sizeof name, "out[%d]", i);
+    if ((st = check_shape(&out[i], name, kF32 | kBF16, grads[i].rows, grads[i].cols)) != GS_OK) return st;
+    if ((st = check_in_place(&out[i], &grads[i], name)) != GS_OK) return st;
+    if (grads[i].rows == 0) continue;
+    for (int j = 0; j < i; ++j)   // a matrix that is there twice would be scaled twice
+      if (grads[j].rows > 0 &&
+          (same_data(&out[i], &out[j]) || same_data(&out[i], &grads[j]) || same_data(&out[j], &grads[i])))
+        return fail(GS_ERR_INVALID_ARG, "out[%d] shares its data with entry %d", i, j);
+  }
+  if (!ws || ws_bytes < gsk::clip_ws_bytes())
+    return fail(GS_ERR_CAPACITY, "clip_grads workspace needs %zu bytes", gsk::clip_ws_bytes());
+  const hipError_t e = gsk::launch_clip_grads(grads, out, count, max_norm, norm, ws, as_stream(stream));
+  if (e != hipSuccess) return hip_fail(e, "clip_grads");
+  return GS_OK;
+}
+
 int32_t gs_rmsnorm_fwd(const gs_matrix* x, const gs_matrix* residual, const float* weight, float eps,
                        const gs_matrix* h, const gs_matrix* ckpt, const gs_matrix* y, float* rstd, void* stream) {
   g_err[0] = 0;
@@ -825,20 +932,29 @@ int32_t gs_linear_fwd(const gs_matrix* x, const gs_matrix* w, const float* bias,
                       const gs_matrix* residual, const gs_matrix* z, const gs_matrix* y, void* stream) {
   g_err[0] = 0;
   int32_t st;
-  if ((st = check_matrix(x, "x", kBF16 | kMX8)) != GS_OK) return st;
-  if ((st = check_matrix(w, "w", kBF16)) != GS_OK) return st;
+  // a weight in MX4 also takes x in MX4 and gives y in MX8, and keeps no z
+  const bool mx4 = w && w->type == GS_MAT_MX4;
+  if ((st = check_matrix(x, "x", kBF16 | kMX8 | (mx4 ? kMX4 : 0))) != GS_OK) return st;
+  if ((st = check_matrix(w, "w", kBF16 | kMX4)) != GS_OK) return st;
   const int64_t rows = x->rows, in = x->cols, out = w->rows;
-  if ((st = check_shape(w, "w", kBF16, out, in)) != GS_OK) return st;
+  if ((st = check_shape(w, "w", kBF16 | kMX4, out, in)) != GS_OK) return st;
   if (!width_ok(out)) return fail(GS_ERR_INVALID_ARG, "w: rows must be 1..2^20");
   if (act < GS_ACT_NONE || act > GS_ACT_GELU) return fail(GS_ERR_INVALID_ARG, "unknown activation");
+  if (mx4 && z) return fail(GS_ERR_UNSUPPORTED, "z: not kept with w in MX4");
   if (residual && (st = check_shape(residual, "residual", kF32 | kBF16, rows, out)) != GS_OK) return st;
   if (z && (st = check_shape(z, "z", kF32 | kBF16 | kMX8, rows, out)) != GS_OK) return st;
-  if ((st = check_shape(y, "y", kF32 | kBF16, rows, out)) != GS_OK) return st;
+  if ((st = check_shape(y, "y", kF32 | kBF16 | (mx4 ? kMX8 : 0), rows, out)) != GS_OK) return st;
   if ((st = check_in_place(y, residual, "y")) != GS_OK) return st;
   if (same_data(y, x) || same_data(y, w) || same_data(y, z) || same_data(z, x) || same_data(z, w) ||
       same_data(z, residual))
     return fail(GS_ERR_INVALID_ARG, "an output is one of the inputs or another output");
   if (rows == 0) return GS_OK;
+  if (mx4) {
+    const hipError_t e = gsk::launch_linear_mx4(gsk::mat_arg(x), gsk::mat_arg(w), bias, act, gsk::mat_arg(residual),
+                                                gsk::mat_arg(y), rows, int(in), int(out), as_stream(stream));
+    if (e != hipSuccess) return hip_fail(e, "linear_mx4");
+    return GS_OK;
+  }
   const hipError_t e = gsk::launch_linear_fwd(gsk::mat_arg(x), gsk::mat_arg(w), bias, act, gsk::mat_arg(residual),
                                               gsk::mat_arg(z), gsk::mat_arg(y), rows, int(in), int(out),
                                               as_stream(stream));

@@ -1,0 +1,15 @@
+// The launches of lookup.hip (arguments checked by the caller) and what they take of sort.hip.
+#pragma once
+
+#include "matrix.h"
+
+namespace gsk {
+
+// index: int32, or int64 where wide.
+hipError_t launch_lookup_fwd(const MatArg& table, const void* index, bool wide, float scale, const MatArg& y, int64_t rows,
+                             int64_t entries, int cols, hipStream_t s);
+size_t lookup_bwd_ws_bytes(int64_t rows, int cols);
+hipError_t launch_lookup_bwd(const MatArg& dy, const void* index, bool wide, float scale, const MatArg& dtable, int64_t rows,
+                             int64_t entries, int cols, void* ws, hipStream_t s);
+
+}  // namespace gsk

@@ -71,7 +71,9 @@ inline size_t hist_entries(int nb) { return size_t((nb + kHistGroup - 1) / kHist
 // Where a radix pass reads its items from.
 enum Source {
   kFromKeys = 0,      // keys[idx], vals[idx], idx < count (count on the device if count_dev)
-  kFromDepth = 1      // d of Gaussian idx, value idx; only Gaussians with tiles[idx] > 0
+  kFromDepth = 1,     // d of Gaussian idx, value idx; only Gaussians with tiles[idx] > 0
+  kFromIndex = 2,     // an entry number (keys: int32; key_base: their number, which stands for those outside), value idx
+  kFromIndex64 = 3    // the same from int64
 };
 
 struct PassIn {
@@ -124,6 +126,12 @@ __device__ inline bool load_item(const PassIn& in, uint32_t idx, uint32_t& key, 
     key = b > in.key_base ? b - in.key_base : 0u;
     val = idx;
     return t != 0u;
+  } else if (SRC == kFromIndex || SRC == kFromIndex64) {
+    const int64_t e = SRC == kFromIndex ? int64_t(reinterpret_cast<const int32_t*>(in.keys)[idx])
+                                        : reinterpret_cast<const int64_t*>(in.keys)[idx];
+    key = uint64_t(e) < in.key_base ? uint32_t(e) : in.key_base;
+    val = idx;
+    return true;
   } else {
     key = in.keys[idx];
     val = in.vals[idx];
@@ -790,6 +798,35 @@ hipError_t launch_sort_pairs_u32(uint32_t* keys, uint32_t* vals, uint32_t count,
     const hipError_t e = radix_pass<kFromKeys>(in, kNoPlan, nb, kDigitBits * pass, std::min(kDigitBits, 32 - kDigitBits * pass),
                                                r, even ? alt_k : keys, even ? alt_v : vals, nullptr, nullptr,
                                                nullptr, nullptr, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+size_t sort_index_ws_bytes(int64_t n) { return sort_pairs_ws_bytes(n); }
+
+hipError_t launch_sort_index(const void* index, bool wide, uint32_t count, uint32_t entries, uint32_t* keys, uint32_t* vals,
+                             void* ws, hipStream_t s) {
+  Carver c{static_cast<char*>(ws)};
+  uint32_t* alt_k = c.take(size_t(count) * 4);
+  uint32_t* alt_v = c.take(size_t(count) * 4);
+  const RadixWs r = carve_radix(c, blocks_for(count));
+  const int nb = blocks_for(count);
+  const int all = std::max(1, bits_for(entries)), passes = (all + kDigitBits - 1) / kDigitBits;
+  const int low = (all + passes - 1) / passes;   // as evenly as the tile sort's
+  for (int pass = 0; pass < passes; ++pass) {
+    const bool last = (passes - 1 - pass) % 2 == 0;   // passes that write keys and vals
+    uint32_t *ko = last ? keys : alt_k, *vo = last ? vals : alt_v;
+    const int shift = low * pass, bits = std::min(low, all - shift);
+    PassIn in{last ? alt_k : keys, last ? alt_v : vals, nullptr, nullptr, 0u, count, nullptr};
+    if (pass == 0) {
+      in.keys = static_cast<const uint32_t*>(index);
+      in.key_base = entries;
+    }
+    const hipError_t e =
+        pass > 0 ? radix_pass<kFromKeys>(in, kNoPlan, nb, shift, bits, r, ko, vo, nullptr, nullptr, nullptr, nullptr, s)
+        : wide   ? radix_pass<kFromIndex64>(in, kNoPlan, nb, shift, bits, r, ko, vo, nullptr, nullptr, nullptr, nullptr, s)
+                 : radix_pass<kFromIndex>(in, kNoPlan, nb, shift, bits, r, ko, vo, nullptr, nullptr, nullptr, nullptr, s);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;

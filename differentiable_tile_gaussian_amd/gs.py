@@ -18,9 +18,10 @@ LIB_PATH = os.path.join(_HERE, "libgs.so")
 
 GS_OK, GS_ERR_INVALID_ARG, GS_ERR_CAPACITY, GS_ERR_UNSUPPORTED, GS_ERR_HIP = 0, -1, -2, -3, -4
 GS_WS_PREPROCESS, GS_WS_BIN_SORT, GS_WS_LOSS, GS_WS_RENDER, GS_WS_DENSIFY, GS_WS_LOSS_CHARBONNIER = 0, 1, 2, 3, 4, 5
-GS_WS_CAMERA_GRAD, GS_WS_RELOCATE, GS_WS_RMSNORM_BWD, GS_WS_LINEAR_BWD = 6, 7, 8, 9
+GS_WS_CAMERA_GRAD, GS_WS_RELOCATE, GS_WS_RMSNORM_BWD, GS_WS_LINEAR_BWD, GS_WS_LOOKUP_BWD, GS_WS_CLIP_GRADS = 6, 7, 8, 9, 10, 11
 GS_GRAD_SUMS_FLOAT, GS_GRAD_SUMS_FIXED = 0, 1
-GS_MAT_F32, GS_MAT_BF16, GS_MAT_MX8 = 0, 1, 2
+GS_MAT_F32, GS_MAT_BF16, GS_MAT_MX8, GS_MAT_MX4 = 0, 1, 2, 4
+GS_CLIP_MAX = 1024
 GS_ACT_NONE, GS_ACT_RELU, GS_ACT_SILU, GS_ACT_GELU = 0, 1, 2, 3
 ACTIVATIONS = {"none": GS_ACT_NONE, "relu": GS_ACT_RELU, "silu": GS_ACT_SILU, "gelu": GS_ACT_GELU}
 
@@ -29,7 +30,8 @@ EXPORTED = ("gs_preprocess", "gs_bin_sort", "gs_render_fwd", "gs_loss_l1_dssim",
             "gs_camera_grad", "gs_densify_accumulate", "gs_densify", "gs_relocate", "gs_loss_charbonnier",
             "gs_workspace_bytes", "gs_loss_l1_dssim_noalloc", "gs_profile_enable", "gs_profile_query", "gs_param_floats", "gs_params_to_blocked",
             "gs_params_from_blocked", "gs_mx8_pack", "gs_mx8_unpack", "gs_rmsnorm_fwd", "gs_rmsnorm_bwd",
-            "gs_linear_fwd", "gs_linear_bwd", "gs_last_error")
+            "gs_linear_fwd", "gs_linear_bwd", "gs_mx4_pack", "gs_mx4_unpack", "gs_lookup_fwd", "gs_lookup_bwd",
+            "gs_clip_grads", "gs_last_error")
 
 
 class GsError(RuntimeError):
@@ -125,8 +127,13 @@ def _load():
     lib.gs_rmsnorm_bwd.argtypes = [P, P, P, P, P, P, P, P, C.c_size_t, P]
     lib.gs_linear_fwd.argtypes = [P, P, P, I32, P, P, P, P]
     lib.gs_linear_bwd.argtypes = [P, P, I32, P, P, P, P, P, P, C.c_size_t, P]
+    lib.gs_mx4_pack.argtypes = [P, P, P]
+    lib.gs_mx4_unpack.argtypes = [P, P, P]
+    lib.gs_lookup_fwd.argtypes = [P, P, I32, C.c_float, P, P]
+    lib.gs_lookup_bwd.argtypes = [P, P, I32, C.c_float, P, P, C.c_size_t, P]
+    lib.gs_clip_grads.argtypes = [P, P, I32, C.c_double, P, P, C.c_size_t, P]
     for name in ("gs_mx8_pack", "gs_mx8_unpack", "gs_rmsnorm_fwd", "gs_rmsnorm_bwd", "gs_linear_fwd",
-                 "gs_linear_bwd"):
+                 "gs_linear_bwd", "gs_mx4_pack", "gs_mx4_unpack", "gs_lookup_fwd", "gs_lookup_bwd", "gs_clip_grads"):
         getattr(lib, name).restype = I32
     lib.gs_last_error.restype = C.c_char_p
     for name in ("gs_preprocess", "gs_bin_sort", "gs_render_fwd", "gs_loss_l1_dssim", "gs_render_bwd",
@@ -421,13 +428,46 @@ def mx8_empty(rows, cols, device="cuda"):
     return Mx8(q if pitch == cols else q[:, :cols], scales)
 
 
+class Mx4:
+    """An MX4 matrix of `cols` columns: q [rows][16 ceil(cols / 32)] (torch.uint8, two columns to a
+    byte, the even one in the low half) and scales [rows][ceil(cols / 32)] (torch.float8_e8m0fnu); the
+    rows of q start at multiples of 16 bytes."""
+
+    __slots__ = ("q", "scales", "cols")
+
+    def __init__(self, q, scales, cols):
+        self.q, self.scales, self.cols = q, scales, cols
+
+    @property
+    def shape(self):
+        return torch.Size((self.q.shape[0], self.cols))
+
+
+def mx4_empty(rows, cols, device="cuda"):
+    """An uninitialised MX4 matrix."""
+    blocks = (cols + 31) // 32
+    return Mx4(torch.empty((rows, 16 * blocks), dtype=torch.uint8, device=device),
+               torch.empty((rows, blocks), dtype=torch.float8_e8m0fnu, device=device), cols)
+
+
 _KINDS = {torch.float32: GS_MAT_F32, torch.bfloat16: GS_MAT_BF16}
 
 
 def _matrix(t, name):
-    """gs_matrix of a two-dimensional tensor (float32, bfloat16) or Mx8 with adjacent columns."""
-    if t is None:
-        return None
+    """gs_matrix of a two-dimensional tensor (float32, bfloat16), Mx8 or Mx4 with adjacent columns."""
+    return None if t is None else C.byref(_struct(t, name))
+
+
+def _struct(t, name):
+    if isinstance(t, Mx4):
+        if t.q.dtype != torch.uint8 or t.scales.dtype != torch.float8_e8m0fnu:
+            raise ValueError(f"{name}: an Mx4 is a uint8 matrix with float8_e8m0fnu scales")
+        rows, blocks = t.q.shape[0], (t.cols + 31) // 32
+        if t.cols < 1 or t.q.shape != (rows, 16 * blocks) or t.scales.shape != (rows, blocks):
+            raise ValueError(f"{name}: an Mx4 of {t.cols} columns has rows of whole blocks: 16 bytes and a scale for 32 columns")
+        _, scales, scales_ld = _rows(t.scales, f"{name} (scales)")
+        _, data, pitch = _rows(t.q, name)
+        return GsMatrix(data, scales, rows, t.cols, 2 * pitch, scales_ld, GS_MAT_MX4)
     if isinstance(t, Mx8):
         q, kind = t.q, GS_MAT_MX8
         if q.dtype != torch.float8_e4m3fn or t.scales.dtype != torch.float8_e8m0fnu:
@@ -436,11 +476,11 @@ def _matrix(t, name):
     else:
         q, kind, blocks, scales, scales_ld = t, _KINDS.get(t.dtype), None, None, 0
         if kind is None:
-            raise ValueError(f"{name}: expected float32, bfloat16 or an Mx8, got {t.dtype}")
+            raise ValueError(f"{name}: expected float32, bfloat16, an Mx8 or an Mx4, got {t.dtype}")
     (rows, cols), data, ld = _rows(q, name)
     if blocks is not None and blocks != (rows, (cols + 31) // 32):
         raise ValueError(f"{name}: scales must be [rows][ceil(cols / 32)]")
-    return C.byref(GsMatrix(data, scales, rows, cols, ld, scales_ld, kind))
+    return GsMatrix(data, scales, rows, cols, ld, scales_ld, kind)
 
 
 def _rows(t, name):
@@ -479,6 +519,88 @@ def gs_mx8_unpack(q, x, stream=None):
     _check(_lib.gs_mx8_unpack(_matrix(q, "q"), _matrix(x, "x"), _stream(stream)))
 
 
+def gs_mx4_pack(x, q, stream=None):
+    """x (float32 or bfloat16) to the Mx4 q of the same size."""
+    _check(_lib.gs_mx4_pack(_matrix(x, "x"), _matrix(q, "q"), _stream(stream)))
+
+
+def gs_mx4_unpack(q, x, stream=None):
+    """The Mx4 q's values to x (float32 or bfloat16)."""
+    _check(_lib.gs_mx4_unpack(_matrix(q, "q"), _matrix(x, "x"), _stream(stream)))
+
+
+def _index(t, rows):
+    """(address, bytes an element) of a contiguous int32 or int64 vector."""
+    if t.dtype not in (torch.int32, torch.int64) or t.dim() != 1 or not t.is_contiguous() or t.numel() != rows or not t.is_cuda:
+        raise ValueError(f"index: expected {rows} contiguous int32 or int64 values in device memory")
+    return t.data_ptr(), t.element_size()
+
+
+def gs_lookup_fwd(table, index, y, scale=1.0, stream=None):
+    """y[i] = scale table[index[i]], zeros where index[i] is outside the table (int32 or int64)."""
+    _check(_lib.gs_lookup_fwd(_matrix(table, "table"), *_index(index, y.shape[0]), float(scale), _matrix(y, "y"),
+                              _stream(stream)))
+
+
+def gs_lookup_bwd(dy, index, dtable, ws, scale=1.0, stream=None):
+    """dtable[t] = scale times the sum of dy[i] over the rows i with index[i] = t."""
+    _check(_lib.gs_lookup_bwd(_matrix(dy, "dy"), *_index(index, dy.shape[0]), float(scale), _matrix(dtable, "dtable"),
+                              _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)))
+
+
+class Matrices:
+    """A list of float32 or bfloat16 tensors as the array of gs_matrix that gs_clip_grads takes, for
+    buffers that stay where they are from step to step (it keeps them alive).  Matrices need adjacent
+    columns, tensors of other dimensions have to be contiguous."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        parts = []
+        for i, t in enumerate(self.tensors):
+            parts += [_struct(v, f"[{i}]") for v in _as_matrices(t, f"[{i}]")]
+        self.count = len(parts)
+        self.array = (GsMatrix * max(self.count, 1))(*parts)
+
+
+def _as_matrices(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: expected a tensor")
+    if t.dim() == 2 and t.shape[1] <= 1 << 20:
+        return [t] if t.shape[1] else []
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a matrix with adjacent columns, or a contiguous tensor")
+    t, n = t.view(-1), t.numel()
+    whole = n >> 20 << 20
+    return ([t[:whole].view(-1, 1 << 20)] if whole else []) + ([t[whole:].view(1, -1)] if n > whole else [])
+
+
+def blocked_matrices(t, n, sh_degree):
+    """The parameters of n Gaussians in a blocked array as matrices (without the padding)."""
+    _blocked(t, n, sh_degree)
+    P, full = 11 + 3 * (sh_degree + 1) ** 2, n // 64
+    t = t.view(-1)
+    out = [t[:full * P * 64].view(-1, 64)] if full else []
+    if n % 64:
+        out.append(t[full * P * 64:(full + 1) * P * 64].view(P, 64)[:, :n % 64])
+    return out
+
+
+def gs_clip_grads(grads, max_norm, norm, ws, out=None, stream=None):
+    """norm (float32 [1]) = the norm of all grads together, and out = grads min(1, max_norm / norm).
+    grads, out: lists of tensors, or Matrices; out None: in place; max_norm inf: only the norm (with
+    out None)."""
+    grads = grads if isinstance(grads, Matrices) else Matrices(grads)
+    if out is None:
+        to = None if max_norm == float("inf") else grads.array
+    else:
+        out = out if isinstance(out, Matrices) else Matrices(out)
+        if out.count != grads.count:
+            raise ValueError(f"out: expected {grads.count} matrices, got {out.count}")
+        to = out.array
+    _check(_lib.gs_clip_grads(grads.array, to, grads.count, float(max_norm), _floats(norm, 1, "norm"), _ptr(ws),
+                              ws.numel() if ws is not None else 0, _stream(stream)))
+
+
 def gs_rmsnorm_fwd(x, weight, eps, y, rstd=None, residual=None, h=None, ckpt=None, stream=None):
     """h = x + residual, y = h (mean(h^2) + eps)^-1/2 weight by rows; ckpt: an Mx8 for h."""
     rows, cols = x.shape
@@ -497,7 +619,8 @@ def gs_rmsnorm_bwd(dy, h, weight, rstd, dh, dweight, ws, dres=None, stream=None)
 
 
 def gs_linear_fwd(x, w, y, bias=None, act="none", residual=None, z=None, stream=None):
-    """y = act(x w^T + bias) + residual; z (float32, bfloat16 or Mx8) receives x w^T + bias."""
+    """y = act(x w^T + bias) + residual; z (float32, bfloat16 or Mx8) receives x w^T + bias.  With w an
+    Mx4, x may be one too, y an Mx8, and z is None."""
     _check(_lib.gs_linear_fwd(_matrix(x, "x"), _matrix(w, "w"), _floats(bias, w.shape[0], "bias"), _activation(act),
                               _matrix(residual, "residual"), _matrix(z, "z"), _matrix(y, "y"), _stream(stream)))
 

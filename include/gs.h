@@ -438,6 +438,15 @@ int32_t gs_relocate(float* params, float* m, float* v, int64_t n, int32_t sh_deg
  *                nearest e4m3 value (ties to even), so nothing saturates; infinities and NaN
  *                become NaN, and a NaN or infinity leaves its neighbours' scale alone.  Read with
  *                byte 255 as NaN.
+ *   GS_MAT_MX4   e2m1 codes, two to a byte with the even column in the low half: values 0, 0.5, 1,
+ *                1.5, 2, 3, 4, 6 for the codes 0 .. 7, negative ones for 8 .. 15, times 2^(s - 127) with
+ *                s the scale byte as for MX8.  Written with the smallest exponent >= -126 for which
+ *                the block's largest magnitude is at most 6 2^(s - 127), and the nearest value (ties
+ *                to the even code).  There is no NaN among them: an infinity or a NaN gives its block
+ *                the scale byte 255, with which all 32 columns read as NaN.  Rows are stored in
+ *                whole blocks: data is 16-byte aligned, ld a multiple of 32 (at most 2^21, as
+ *                scales_ld), and element (i, j) is half j % 2 of byte (i * ld + j) / 2; what a
+ *                row's last block holds behind cols is written as zero and not read as a value.
  * There is no float16: the loss's gradients carry 1 / (3 W H), below its normal range.
  * 0 <= rows < 2^31, 1 <= cols <= 2^20, ld >= cols, scales_ld >= ceil(cols / 32).  Any ld and any
  * alignment of the element's own size are taken; rows that start at multiples of 16 bytes are
@@ -449,13 +458,13 @@ int32_t gs_relocate(float* params, float* m, float* v, int64_t n, int32_t sh_deg
  * Every call only enqueues. */
 typedef struct gs_matrix {
   void* data;
-  uint8_t* scales;      /* GS_MAT_MX8 only */
+  uint8_t* scales;      /* GS_MAT_MX8 and GS_MAT_MX4 only */
   int64_t rows, cols;
   int64_t ld;           /* elements between rows */
   int64_t scales_ld;    /* bytes between rows of scales */
   int32_t type;
 } gs_matrix;
-enum { GS_MAT_F32 = 0, GS_MAT_BF16 = 1, GS_MAT_MX8 = 2 };
+enum { GS_MAT_F32 = 0, GS_MAT_BF16 = 1, GS_MAT_MX8 = 2, GS_MAT_MX4 = 4 };
 
 /* Activations of a linear layer: none, max(z, 0), z sigmoid(z), and the tanh form of gelu,
  * z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2. */
@@ -465,6 +474,37 @@ enum { GS_ACT_NONE = 0, GS_ACT_RELU = 1, GS_ACT_SILU = 2, GS_ACT_GELU = 3 };
  * is exact in both unless it overflows, in BF16 from 2^-126 on). */
 int32_t gs_mx8_pack(const gs_matrix* x, const gs_matrix* q, void* stream);
 int32_t gs_mx8_unpack(const gs_matrix* q, const gs_matrix* x, void* stream);
+
+/* x (F32 or BF16) to q (MX4) of the same size, and back. */
+int32_t gs_mx4_pack(const gs_matrix* x, const gs_matrix* q, void* stream);
+int32_t gs_mx4_unpack(const gs_matrix* q, const gs_matrix* x, void* stream);
+
+/* Feature rows that Gaussians share: y[i] = scale table[index[i]], a row of zeros where index[i]
+ * is outside [0, table->rows) (a Gaussian without a feature: -1).  table [entries][cols], y
+ * [rows][cols]: F32 or BF16.  index: device array of y->rows int32 (index_bytes 4) or int64
+ * (8).  entries >= 1; scale finite. */
+int32_t gs_lookup_fwd(const gs_matrix* table, const void* index, int32_t index_bytes, float scale, const gs_matrix* y,
+                      void* stream);
+
+/* Its gradient: dtable[t] = scale times the sum of dy[i] over the rows i with index[i] = t, zero for
+ * an entry that no row has (dtable is overwritten).  dy [rows][cols], dtable [entries][cols]: F32
+ * or BF16.  The sums are float32 and their order depends on index alone, so that results are the
+ * same bits every time.  ws: gs_workspace_bytes(GS_WS_LOOKUP_BWD, rows, 0, cols, entries, NULL). */
+int32_t gs_lookup_bwd(const gs_matrix* dy, const void* index, int32_t index_bytes, float scale, const gs_matrix* dtable,
+                      void* ws, size_t ws_bytes, void* stream);
+
+/* Clipping by the global norm, before an update: *norm (device float) = the Euclidean norm of all
+ * elements of grads[0 .. count - 1] together, and out[i] = grads[i] min(1, max_norm / norm).  grads,
+ * out: HOST arrays of matrices, F32 or BF16, out[i] of grads[i]'s size and not necessarily its
+ * type; out[i] may be grads[i] itself (same type and ld), but no matrix may be in out twice.  out
+ * NULL: only the norm.  count <= GS_CLIP_MAX.  max_norm > 0 (infinity: a copy).  The squares are
+ * added in float64 (no overflow, nothing vanishes), in a fixed order.  A NaN makes the norm and
+ * all of out NaN; an infinity makes the norm infinite and out zero, NaN in its own place.  A
+ * blocked parameter array is two matrices: its whole groups, [n / 64 P][64], and the last group's
+ * [P][n % 64] with ld 64.  ws: gs_workspace_bytes(GS_WS_CLIP_GRADS, 0, 0, 0, 0, NULL). */
+enum { GS_CLIP_MAX = 1024 };
+int32_t gs_clip_grads(const gs_matrix* grads, const gs_matrix* out, int32_t count, double max_norm, float* norm, void* ws,
+                      size_t ws_bytes, void* stream);
 
 /* Root-mean-square norm with the residual's addition: for every row
  *   h = x + residual (x alone without one),  rstd = (mean(h^2) + eps)^(-1/2),
@@ -491,7 +531,9 @@ int32_t gs_rmsnorm_bwd(const gs_matrix* dy, const gs_matrix* h, const float* wei
  * x [rows][in]: BF16 or MX8; w [out][in]: BF16; bias (nullable): float[out]; residual (nullable)
  * [rows][out]: F32 or BF16; z (nullable) [rows][out]: any type, the pre-activation kept for
  * gs_linear_bwd; y [rows][out]: F32 or BF16, may be residual itself (same type and ld).  The
- * products are exact, their sums float32, and y uses z before it is rounded. */
+ * products are exact, their sums float32, and y uses z before it is rounded.
+ * A trained layer is served with w in MX4: x may then be MX4 too, y also MX8 (what a following
+ * layer reads), and z is NULL (gs_linear_bwd takes w in BF16 alone). */
 int32_t gs_linear_fwd(const gs_matrix* x, const gs_matrix* w, const float* bias, int32_t act,
                       const gs_matrix* residual, const gs_matrix* z, const gs_matrix* y, void* stream);
 
@@ -508,11 +550,12 @@ int32_t gs_linear_bwd(const gs_matrix* dy, const gs_matrix* z, int32_t act, cons
 /* Workspace sizes, in bytes, for the calls that take one. */
 enum { GS_WS_PREPROCESS = 0, GS_WS_BIN_SORT = 1, GS_WS_LOSS = 2, GS_WS_RENDER = 3, GS_WS_DENSIFY = 4,
        GS_WS_LOSS_CHARBONNIER = 5, GS_WS_CAMERA_GRAD = 6, GS_WS_RELOCATE = 7, GS_WS_RMSNORM_BWD = 8,
-       GS_WS_LINEAR_BWD = 9 };
+       GS_WS_LINEAR_BWD = 9, GS_WS_LOOKUP_BWD = 10, GS_WS_CLIP_GRADS = 11 };
 
 /* Workspace size in bytes for the call `which_call` (GS_WS_*) with n Gaussians (rows, for the
  * network operators), `pairs` pairs and a W x H image (for the network operators W is the input
- * width and H the output width of a linear layer, W the width of a norm); cfg as the call will
+ * width and H the output width of a linear layer, W the width of a norm or of a table's rows and H
+ * the table's entries); cfg as the call will
  * receive it (NULL: defaults).  A network operator's workspace for n rows also serves fewer rows
  * of the same widths.  The render workspace (GS_WS_RENDER) depends on cfg's split sizes and
  * gradient-sum mode; the others do not. */
