@@ -123,9 +123,51 @@ __device__ inline void finish16(const Epilogue& e, int64_t row, int col, float v
   store16<WHOLE>(e.y, Y == kAny ? e.y.type : Y, row, col, v, n);
 }
 
+// ------------------------------------------------------------- tile kernels
+
+// Ends a step: LDS writes done, all waves there; loads from memory stay in flight.
+__device__ inline void step_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// The order in which a step's instructions are issued: a few operand reads, then four matrix
+// instructions at a time with what the next ones need in between: an operand read or two, an
+// LDS write of the step to come, a load from memory.  (Left to itself the compiler puts the
+// writes first, and every wave waits for them in front of its first operand.)
+template <int READS, int WRITES, int LOADS, int GROUPS, int I = 0>
+__device__ inline void interleave() {
+  constexpr int kFirst = READS / 4, kRest = READS - kFirst, kOver = GROUPS - 2;
+  if constexpr (I == 0) __builtin_amdgcn_sched_group_barrier(0x100, kFirst, 0);
+  if constexpr (I < GROUPS) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+    if constexpr (I < kOver) {
+      constexpr int reads = (I + 1) * kRest / kOver - I * kRest / kOver;
+      if constexpr (reads > 0) __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);
+    }
+    constexpr int writes = (I + 1) * WRITES / GROUPS - I * WRITES / GROUPS;
+    if constexpr (writes > 0) __builtin_amdgcn_sched_group_barrier(0x200, writes, 0);
+    constexpr int loads = (I + 1) * LOADS / GROUPS - I * LOADS / GROUPS;
+    if constexpr (loads > 0) __builtin_amdgcn_sched_group_barrier(0x020, loads, 0);
+    interleave<READS, WRITES, LOADS, GROUPS, I + 1>();
+  }
+}
+
+// Which tile a block takes: consecutive blocks go to different XCDs, each with its own L2, so
+// an XCD is given neighbouring tiles (the P tiles of one Q tile after another).
+__device__ inline int tile_of(int block, int tiles) {
+  const int per = (tiles + 7) / 8;
+  return block % 8 * per + block / 8;
+}
+
 // ---- linear_rows.hip: narrow layers over many rows, the weight kept in LDS
 bool rows_fwd_takes(int k, int n);
 hipError_t launch_rows_fwd(const MatArg& x, const MatArg& w, const Epilogue& e, int64_t rows, int k, int n,
+                           hipStream_t s);
+
+// ---- linear_rows_mx4.hip: the same with the weight in MX4, where rows_fwd_takes the widths
+hipError_t launch_rows_mx4(const MatArg& x, const MatArg& w, const Epilogue& e, int64_t rows, int k, int n,
                            hipStream_t s);
 
 // ---- linear_rows_bwd.hip: the gradients of the narrowest of them in one pass
@@ -137,7 +179,7 @@ hipError_t launch_rows_bwd(const MatArg& dy, const MatArg& z, int act, const Mat
                            hipStream_t s);
 
 // ---- linear_tiles.hip: products bounded by the matrix cores, in 128-column tiles
-// out(q, p) = sum_k Q(q, k) P(p, k), finished as a forward's result
+// out(q, p) = sum_k Q(q, k) P(p, k), finished as a forward's result (P: bfloat16 or MX4)
 hipError_t launch_tile_nt(const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, const Epilogue& e,
                           hipStream_t s);
 // out(q, p) = sum_m Q(m, q) P(m, p) in `slices` parts of the rows m (part: [slices][nq][np]

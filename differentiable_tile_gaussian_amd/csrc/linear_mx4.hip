@@ -172,12 +172,157 @@ hipError_t go(const MatArg& x, const MatArg& w, const Epilogue& e, int64_t rows,
   return hipGetLastError();
 }
 
+// ------------------------------------------------------------- both operands in MX4, by tiles
+
+// Tiles of 128 columns by 32 QT rows, 64 x 16 QT for each of four waves, in steps of 128 k staged
+// through registers into two LDS buffers as in linear_tiles.hip.  LDS holds the operands as the
+// matrix cores take them: a fragment (16 rows, 128 k) is 1 KiB, 16 bytes a lane in the lanes'
+// order, which is also the order in which a wave loads it, so that writes and reads are
+// contiguous; and its scales, four bytes a row, of which a lane reads its own.  ALIGNED: rows
+// of scales are whole aligned words.
+constexpr int kTileThreads = 256;
+
+template <int QT, bool ALIGNED>
+__global__ void __launch_bounds__(kTileThreads) tile_mx4_kernel(MatArg W, MatArg X, int np, int64_t nq, int nk, Epilogue e,
+                                                                 int ptiles, int tiles) {
+  constexpr int BP = 128, BQ = 32 * QT, kP = BP / 16, kQ = BQ / 16, kFrags = kP + kQ, kStep = kFrags * (1024 + 64), D = 2;
+  __shared__ __align__(16) uint8_t lds[2 * kStep];
+  const int tile = tile_of(blockIdx.x, tiles);
+  if (tile >= tiles) return;
+  const int p0 = tile % ptiles * BP;
+  const int64_t q0 = int64_t(tile / ptiles) * BQ;
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, wp = wave % 2, wq = wave / 2, g = lane / 16, r = lane % 16;
+  const int blocks = (nk + 31) / 32, steps = (blocks + 3) / 4;
+  const uint32_t wpitch = uint32_t(mx4_pitch(W)), xpitch = uint32_t(mx4_pitch(X));
+  const Buffer wb = buffer_at(W.p + int64_t(p0) * wpitch), ws = buffer_at(W.s + p0 * W.lds);
+  const Buffer xb = buffer_at(X.p + q0 * xpitch), xs = buffer_at(X.s + q0 * X.lds);
+  // a lane's four result tiles are 16 consecutive columns
+  auto wrow = [](int f, int r) { return f / 4 * 64 + r / 4 * 16 + f % 4 * 4 + r % 4; };
+  uint32_t woff[kP / 4], xoff[kQ / 4];
+#pragma unroll
+  for (int u = 0; u < kP / 4; ++u) {
+    const int row = wrow(wave + 4 * u, r);
+    woff[u] = p0 + row < np ? row * wpitch + g * 16 : kAbsent;
+  }
+#pragma unroll
+  for (int u = 0; u < kQ / 4; ++u) {
+    const int row = (wave + 4 * u) * 16 + r;
+    xoff[u] = q0 + row < nq ? row * xpitch + g * 16 : kAbsent;
+  }
+  // the thread's row of scales
+  const int sf = threadIdx.x / 16, srow = sf < kP ? wrow(sf, r) : (sf - kP) * 16 + r;
+  const bool is_w = sf < kP, has_scales = is_w ? p0 + srow < np : sf < kFrags && q0 + srow < nq;
+  const uint32_t soff = srow * uint32_t(is_w ? W.lds : X.lds);
+  u32x4 wr[D][kP / 4], xr[D][kQ / 4];
+  uint32_t sr[D];
+  auto fetch = [&](int d, int s) {
+    const bool in = s * 4 + g < blocks;
+#pragma unroll
+    for (int u = 0; u < kP / 4; ++u) wr[d][u] = buffer_load16(wb, in ? woff[u] + s * 64 : kAbsent);
+#pragma unroll
+    for (int u = 0; u < kQ / 4; ++u) xr[d][u] = buffer_load16(xb, in ? xoff[u] + s * 64 : kAbsent);
+    // both matrices' descriptors are uniform, the choice is the wave's (a wave holds four fragments)
+    const Buffer from = __builtin_amdgcn_readfirstlane(is_w) ? ws : xs;
+    if constexpr (ALIGNED) {
+      sr[d] = buffer_load4(from, has_scales && s * 4 < blocks ? soff + s * 4 : kAbsent);
+    } else {
+      uint32_t b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[i] = buffer_load1(from, has_scales && s * 4 + i < blocks ? soff + s * 4 + i : kAbsent);
+      sr[d] = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
+    }
+  };
+  auto stage = [&](int d, int s, uint8_t* at) {
+    if (nk % 32 && s == steps - 1) {   // x ends inside a block (what the weight holds behind it meets zeros)
+#pragma unroll
+      for (int u = 0; u < kQ / 4; ++u) xr[d][u] = mx4_keep(xr[d][u], nk - (s * 4 + g) * 32);
+    }
+#pragma unroll
+    for (int u = 0; u < kP / 4; ++u) *reinterpret_cast<u32x4*>(at + (wave + 4 * u) * 1024 + lane * 16) = wr[d][u];
+#pragma unroll
+    for (int u = 0; u < kQ / 4; ++u) *reinterpret_cast<u32x4*>(at + (kP + wave + 4 * u) * 1024 + lane * 16) = xr[d][u];
+    if (sf < kFrags) *reinterpret_cast<uint32_t*>(at + kFrags * 1024 + threadIdx.x * 4) = sr[d];
+  };
+  f32x4 acc[QT][4];
+#pragma unroll
+  for (int i = 0; i < QT; ++i)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
+  fetch(0, 0);
+  stage(0, 0, lds);
+#pragma unroll
+  for (int d = 0; d < D; ++d) fetch(d, d + 1);
+  for (int s0 = 0; s0 < steps; s0 += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const int s = s0 + d;
+      if (s >= steps) break;
+      step_barrier();
+      const uint8_t* now = lds + (s & 1) * kStep;
+      const uint8_t *data = now + lane * 16, *scales = now + kFrags * 1024 + r * 4 + g;
+      u32x4 wf[4], xf[QT];
+      uint32_t wsc[4], xsc[QT];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        wf[t] = *reinterpret_cast<const u32x4*>(data + (wp * 4 + t) * 1024);
+        wsc[t] = scales[(wp * 4 + t) * 64];
+      }
+#pragma unroll
+      for (int i = 0; i < QT; ++i) {
+        xf[i] = *reinterpret_cast<const u32x4*>(data + (kP + wq * QT + i) * 1024);
+        xsc[i] = scales[(kP + wq * QT + i) * 64];
+      }
+      stage(d, s + 1, lds + (~s & 1) * kStep);   // past the end: zeros, not read
+      fetch(d, s + 1 + D);
+#pragma unroll
+      for (int i = 0; i < QT; ++i)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[i][t] = product4(wf[t], wsc[t], xf[i], xsc[i], acc[i][t]);
+    }
+  }
+  const int col = p0 + wp * 64 + g * 16, n = np - col < 16 ? np - col : 16;
+  float bias[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) bias[j] = e.bias && j < n ? e.bias[col + j] : 0.0f;
+#pragma unroll
+  for (int i = 0; i < QT; ++i) {
+    const int64_t row = q0 + (wq * QT + i) * 16 + r;
+    float v[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = acc[i][j / 4][j % 4] + bias[j];
+    finish16<false, kNone, kAny>(e, row, col, v, row < nq ? n : 0);
+  }
+}
+
+template <int QT>
+hipError_t go_tiles(const MatArg& x, const MatArg& w, const Epilogue& e, int64_t rows, int k, int n, hipStream_t s) {
+  auto words = [&](const MatArg& m) { return reinterpret_cast<uintptr_t>(m.s) % 4 == 0 && m.lds % 4 == 0; };
+  const auto kernel = (k + 31) / 32 % 4 == 0 && words(x) && words(w) ? &tile_mx4_kernel<QT, true> : &tile_mx4_kernel<QT, false>;
+  const int ptiles = int(div_up(n, 128));
+  const int64_t most = (kMaxBlocks - 8) / ptiles * (32 * QT);   // rows of one launch
+  for (int64_t first = 0; first < rows; first += most) {
+    const int64_t count = rows - first < most ? rows - first : most;
+    Epilogue part = e;
+    part.r = rows_from(e.r, first);
+    part.y = rows_from(e.y, first);
+    const int tiles = int(ptiles * int64_t(div_up(count, 32 * QT)));
+    kernel<<<(tiles + 7) / 8 * 8, kTileThreads, 0, s>>>(w, mx4_rows_from(x, first), n, count, k, part, ptiles, tiles);
+  }
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_linear_mx4(const MatArg& x, const MatArg& w, const float* bias, int act, const MatArg& r,
                              const MatArg& y, int64_t rows, int k, int n, hipStream_t s) {
   const Epilogue e{bias, act, r, MatArg{nullptr, nullptr, 0, 0, GS_MAT_F32}, y};
+  if (rows_fwd_takes(k, n) && rows > 16) return launch_rows_mx4(x, w, e, rows, k, n, s);
   GSK_PROF("linear_mx4", s);
+  const int64_t tiles = int64_t(div_up(n, 128)) * div_up(rows, 128);
+  if (tiles > 64) {
+    if (x.type != GS_MAT_MX4) return launch_tile_nt(w, x, n, rows, k, e, s);
+    return tiles <= 256 ? go_tiles<2>(x, w, e, rows, k, n, s) : go_tiles<4>(x, w, e, rows, k, n, s);
+  }
   if (x.type == GS_MAT_MX4) return go<GS_MAT_MX4, false>(x, w, e, rows, k, n, s);
   if (x.type == GS_MAT_MX8) return k < 16 ? go<GS_MAT_MX8, true>(x, w, e, rows, k, n, s) : go<GS_MAT_MX8, false>(x, w, e, rows, k, n, s);
   return k < 16 ? go<GS_MAT_BF16, true>(x, w, e, rows, k, n, s) : go<GS_MAT_BF16, false>(x, w, e, rows, k, n, s);

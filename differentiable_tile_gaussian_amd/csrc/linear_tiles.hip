@@ -11,48 +11,13 @@
 // LDS: a step's operands are written once and read twice by the waves beside its matrix
 // instructions.
 #include "linear.h"
+#include "mx4.h"
 #include "profile.h"
 
 namespace gsk {
 namespace {
 
 constexpr int kThreads = 256;
-
-// Ends a step: LDS writes done, all waves there; loads from memory stay in flight.
-__device__ inline void step_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
-// The order in which a step's instructions are issued: a few operand reads, then four matrix
-// instructions at a time with what the next ones need in between: an operand read or two, an
-// LDS write of the step to come, a load from memory.  (Left to itself the compiler puts the
-// writes first, and every wave waits for them in front of its first operand.)
-template <int READS, int WRITES, int LOADS, int GROUPS, int I = 0>
-__device__ inline void interleave() {
-  constexpr int kFirst = READS / 4, kRest = READS - kFirst, kOver = GROUPS - 2;
-  if constexpr (I == 0) __builtin_amdgcn_sched_group_barrier(0x100, kFirst, 0);
-  if constexpr (I < GROUPS) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
-    if constexpr (I < kOver) {
-      constexpr int reads = (I + 1) * kRest / kOver - I * kRest / kOver;
-      if constexpr (reads > 0) __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);
-    }
-    constexpr int writes = (I + 1) * WRITES / GROUPS - I * WRITES / GROUPS;
-    if constexpr (writes > 0) __builtin_amdgcn_sched_group_barrier(0x200, writes, 0);
-    constexpr int loads = (I + 1) * LOADS / GROUPS - I * LOADS / GROUPS;
-    if constexpr (loads > 0) __builtin_amdgcn_sched_group_barrier(0x020, loads, 0);
-    interleave<READS, WRITES, LOADS, GROUPS, I + 1>();
-  }
-}
-
-// Which tile a block takes: consecutive blocks go to different XCDs, each with its own L2, so
-// an XCD is given neighbouring tiles (the P tiles of one Q tile after another).
-__device__ inline int tile_of(int block, int tiles) {
-  const int per = (tiles + 7) / 8;
-  return block % 8 * per + block / 8;
-}
 
 // 16 values of a row as loaded: bfloat16 (two 16-byte words) or MX8 (one, and the scale).
 template <int TYPE>
@@ -100,16 +65,32 @@ struct Unit {
   }
 };
 
+// From MX4: half a block.
+template <>
+struct Unit<GS_MAT_MX4> {
+  u32x2 a;
+  uint32_t scale;
+  __device__ void load(Buffer data, Buffer scales, uint32_t off, uint32_t soff) {
+    a = buffer_load8(data, off);
+    scale = buffer_load1(scales, soff);
+  }
+  __device__ void operands(u32x4& p, u32x4& q) const {
+    const float s = mx8_scale(scale);
+    p = __builtin_bit_cast(u32x4, mx4_to_bf16x8(a[0], s));
+    q = __builtin_bit_cast(u32x4, mx4_to_bf16x8(a[1], s));
+  }
+};
+
 // ------------------------------------------------- contraction contiguous in both operands
 
 // out(q, p) = sum_k Q(q, k) P(p, k) for the rows q of Q (bfloat16 or MX8) and p of P
-// (bfloat16).  kWhole: nk is a multiple of 16 and both are in buffers' reach.  An LDS row is 64 k, 128 bytes, whose 16-byte pieces are
+// (bfloat16, or MX4, whose blocks are whole: what they hold behind nk meets zeros of Q).  kWhole: nk is a multiple of 16 and both are in buffers' reach.  An LDS row is 64 k, 128 bytes, whose 16-byte pieces are
 // permuted by the row's number so that a fragment read's 16 rows fall into different banks;
 // P's rows are stored so that a lane's four result tiles are 16 consecutive columns.
-template <int QTYPE, int QT, int D, Reach HOW>
+template <int PTYPE, int QTYPE, int QT, int D, Reach HOW>
 __global__ void __launch_bounds__(kThreads) tile_nt_kernel(MatArg P, MatArg Q, int np, int64_t nq, int nk, Epilogue e,
                                                             int ptiles, int tiles) {
-  constexpr bool WHOLE = HOW == kWhole, kFew = HOW == kNarrow;
+  constexpr bool WHOLE = HOW == kWhole, kFew = HOW == kNarrow, kP4 = PTYPE == GS_MAT_MX4;
   constexpr int BP = 128, BQ = 32 * QT, kStep = (BP + BQ) * 128;
   extern __shared__ __align__(16) uint8_t lds[];
   const int tile = tile_of(blockIdx.x, tiles);
@@ -120,28 +101,39 @@ __global__ void __launch_bounds__(kThreads) tile_nt_kernel(MatArg P, MatArg Q, i
   // a thread stages piece `piece` (16 k) of the rows row + 64 u
   const int row = threadIdx.x / 4, piece = threadIdx.x % 4;
   constexpr uint32_t kQ = element_bytes(QTYPE);
-  const Buffer pb = buffer_at(P.p + int64_t(p0) * P.ld * 2), qb = buffer_at(Q.p + q0 * Q.ld * kQ);
+  const uint32_t pp = kP4 ? uint32_t(P.ld) / 2 : uint32_t(P.ld) * 2;
+  const Buffer pb = buffer_at(P.p + int64_t(p0) * pp), psb = buffer_at(kP4 ? P.s + p0 * P.lds : nullptr), qb = buffer_at(Q.p + q0 * Q.ld * kQ);
   const Buffer sb = buffer_at(QTYPE == GS_MAT_MX8 ? Q.s + q0 * Q.lds : nullptr);
-  uint32_t poff[BP / 64], qoff[BQ / 64], soff[BQ / 64];
+  uint32_t poff[BP / 64], psoff[BP / 64], qoff[BQ / 64], soff[BQ / 64];
 #pragma unroll
-  for (int u = 0; u < BP / 64; ++u)
-    poff[u] = p0 + u * 64 + row < np ? (u * 64 + row) * uint32_t(P.ld) * 2 + piece * 32 : kAbsent;
+  for (int u = 0; u < BP / 64; ++u) {
+    const bool in = p0 + u * 64 + row < np;
+    poff[u] = in ? (u * 64 + row) * pp + piece * (kP4 ? 8 : 32) : kAbsent;
+    psoff[u] = in ? (u * 64 + row) * uint32_t(P.lds) + piece / 2 : kAbsent;
+  }
 #pragma unroll
   for (int u = 0; u < BQ / 64; ++u) {
     const bool in = q0 + u * 64 + row < nq;
     qoff[u] = in ? (u * 64 + row) * uint32_t(Q.ld) * kQ + piece * 16 * kQ : kAbsent;
     soff[u] = in ? (u * 64 + row) * uint32_t(Q.lds) + piece / 2 : kAbsent;
   }
-  Unit<GS_MAT_BF16> pr[D][BP / 64];
+  Unit<PTYPE> pr[D][BP / 64];
   Unit<QTYPE> qr[D][BQ / 64];
   auto fetch = [&](int d, int k0) {
     const bool in = k0 + piece * 16 < nk;
+    if constexpr (kP4) {
+#pragma unroll
+      for (int u = 0; u < BP / 64; ++u)
+        pr[d][u].load(pb, psb, in ? poff[u] + k0 / 2 : kAbsent, in ? psoff[u] + k0 / 32 : kAbsent);
+    }
     if constexpr (!WHOLE) {
       const int k = k0 + piece * 16;
+      if constexpr (!kP4) {
 #pragma unroll
-      for (int u = 0; u < BP / 64; ++u) {
-        const int at = p0 + u * 64 + row;
-        pr[d][u].template load_any<kFew>(P, at < np ? at : np - 1, k, nk, at < np);
+        for (int u = 0; u < BP / 64; ++u) {
+          const int at = p0 + u * 64 + row;
+          pr[d][u].template load_any<kFew>(P, at < np ? at : np - 1, k, nk, at < np);
+        }
       }
 #pragma unroll
       for (int u = 0; u < BQ / 64; ++u) {
@@ -150,8 +142,10 @@ __global__ void __launch_bounds__(kThreads) tile_nt_kernel(MatArg P, MatArg Q, i
       }
       return;
     }
+    if constexpr (!kP4) {
 #pragma unroll
-    for (int u = 0; u < BP / 64; ++u) pr[d][u].load(pb, pb, in ? poff[u] + k0 * 2 : kAbsent, 0);
+      for (int u = 0; u < BP / 64; ++u) pr[d][u].load(pb, pb, in ? poff[u] + k0 * 2 : kAbsent, 0);
+    }
 #pragma unroll
     for (int u = 0; u < BQ / 64; ++u)
       qr[d][u].load(qb, sb, in ? qoff[u] + k0 * kQ : kAbsent, in ? soff[u] + k0 / 32 : kAbsent);
@@ -166,7 +160,7 @@ __global__ void __launch_bounds__(kThreads) tile_nt_kernel(MatArg P, MatArg Q, i
 #pragma unroll
     for (int u = 0; u < BP / 64; ++u) {
       const int r = u * 64 + row;
-      if constexpr (!WHOLE) pr[d][u].settle();
+      if constexpr (!WHOLE && !kP4) pr[d][u].settle();
       pr[d][u].operands(a, b);
       put(at, (r & ~63) | ((r & 12) << 2) | ((r & 48) >> 2) | (r & 3), a, b);
     }
@@ -384,10 +378,10 @@ __global__ void __launch_bounds__(kThreads) tile_tn_kernel(MatArg P, MatArg Q, i
   }
 }
 
-template <int QTYPE, int QT, int D, Reach HOW>
+template <int PTYPE, int QTYPE, int QT, int D, Reach HOW>
 hipError_t go_nt(const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, const Epilogue& e, hipStream_t s) {
   constexpr int kLds = 2 * (128 + 32 * QT) * 128;
-  const auto kernel = &tile_nt_kernel<QTYPE, QT, D, HOW>;
+  const auto kernel = &tile_nt_kernel<PTYPE, QTYPE, QT, D, HOW>;
   static LdsLimit limit;
   if (const hipError_t no = limit.allow(kernel, kLds); no != hipSuccess) return no;
   const int ptiles = int(div_up(np, 128)), tiles = int(ptiles * int64_t(div_up(nq, 32 * QT)));
@@ -409,35 +403,41 @@ hipError_t go_tn(const MatArg& P, const MatArg& Q, int np, int nq, int64_t rows,
   return hipGetLastError();
 }
 
-}  // namespace
-
-hipError_t launch_tile_nt(const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, const Epilogue& e,
+template <int PTYPE>
+hipError_t by_size(const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, const Epilogue& e,
                           hipStream_t s) {
   // One 128 x 256 block a compute unit or two of 128 x 128: a long contraction runs better on
   // the larger (8160 x 4096 to 1024: 82 us, smaller tiles 89; from MX8 the two are level, 91 and
   // 93 in calls after a pause, so it has the smaller alone), but two blocks hide each other's epilogue (8160 x 1024 to 4096: 110 us and 106; with
   // gelu and a kept z 138 and 118).
   const bool big = nk >= 2048 && int64_t(div_up(np, 128)) * div_up(nq, 256) >= 192;
-  const Reach how = nk < 16 ? kNarrow : nk % 16 == 0 && buffer_ok(P) && buffer_ok(Q) ? kWhole : kHeldIn;
+  const Reach how = nk < 16 ? kNarrow : nk % 16 == 0 && (PTYPE == GS_MAT_MX4 || buffer_ok(P)) && buffer_ok(Q) ? kWhole : kHeldIn;
   // Up to 128 tiles of 128 x 128 leave half the card idle: twice as many of half the rows (1500 x
   // 4096 to 768: 51 us and 38, 2000 x 1024 to 1024: 18.7 and 15.6; with more, as 1364 x 1136 to
   // 1664, 21.4 and 23.3).
   const bool few = int64_t(div_up(np, 128)) * div_up(nq, 128) <= 128;
   if (few && how != kNarrow) {
     if (Q.type == GS_MAT_MX8)
-      return how == kWhole ? go_nt<GS_MAT_MX8, 2, 3, kWhole>(P, Q, np, nq, nk, e, s)
-                           : go_nt<GS_MAT_MX8, 2, 2, kHeldIn>(P, Q, np, nq, nk, e, s);
-    return how == kWhole ? go_nt<GS_MAT_BF16, 2, 3, kWhole>(P, Q, np, nq, nk, e, s)
-                         : go_nt<GS_MAT_BF16, 2, 2, kHeldIn>(P, Q, np, nq, nk, e, s);
+      return how == kWhole ? go_nt<PTYPE, GS_MAT_MX8, 2, 3, kWhole>(P, Q, np, nq, nk, e, s)
+                           : go_nt<PTYPE, GS_MAT_MX8, 2, 2, kHeldIn>(P, Q, np, nq, nk, e, s);
+    return how == kWhole ? go_nt<PTYPE, GS_MAT_BF16, 2, 3, kWhole>(P, Q, np, nq, nk, e, s)
+                         : go_nt<PTYPE, GS_MAT_BF16, 2, 2, kHeldIn>(P, Q, np, nq, nk, e, s);
   }
   if (Q.type == GS_MAT_MX8)
-    return how == kWhole    ? go_nt<GS_MAT_MX8, 4, 2, kWhole>(P, Q, np, nq, nk, e, s)
-           : how == kHeldIn ? go_nt<GS_MAT_MX8, 4, 2, kHeldIn>(P, Q, np, nq, nk, e, s)
-                            : go_nt<GS_MAT_MX8, 4, 1, kNarrow>(P, Q, np, nq, nk, e, s);
-  if (how == kHeldIn) return go_nt<GS_MAT_BF16, 4, 2, kHeldIn>(P, Q, np, nq, nk, e, s);
-  if (how == kNarrow) return go_nt<GS_MAT_BF16, 4, 1, kNarrow>(P, Q, np, nq, nk, e, s);
-  return big ? go_nt<GS_MAT_BF16, 8, 3, kWhole>(P, Q, np, nq, nk, e, s)
-             : go_nt<GS_MAT_BF16, 4, 2, kWhole>(P, Q, np, nq, nk, e, s);
+    return how == kWhole    ? go_nt<PTYPE, GS_MAT_MX8, 4, 2, kWhole>(P, Q, np, nq, nk, e, s)
+           : how == kHeldIn ? go_nt<PTYPE, GS_MAT_MX8, 4, 2, kHeldIn>(P, Q, np, nq, nk, e, s)
+                            : go_nt<PTYPE, GS_MAT_MX8, 4, 1, kNarrow>(P, Q, np, nq, nk, e, s);
+  if (how == kHeldIn) return go_nt<PTYPE, GS_MAT_BF16, 4, 2, kHeldIn>(P, Q, np, nq, nk, e, s);
+  if (how == kNarrow) return go_nt<PTYPE, GS_MAT_BF16, 4, 1, kNarrow>(P, Q, np, nq, nk, e, s);
+  return big ? go_nt<PTYPE, GS_MAT_BF16, 8, 3, kWhole>(P, Q, np, nq, nk, e, s)
+             : go_nt<PTYPE, GS_MAT_BF16, 4, 2, kWhole>(P, Q, np, nq, nk, e, s);
+}
+
+}  // namespace
+
+hipError_t launch_tile_nt(const MatArg& P, const MatArg& Q, int np, int64_t nq, int nk, const Epilogue& e,
+                          hipStream_t s) {
+  return P.type == GS_MAT_MX4 ? by_size<GS_MAT_MX4>(P, Q, np, nq, nk, e, s) : by_size<GS_MAT_BF16>(P, Q, np, nq, nk, e, s);
 }
 
 // Slices of the rows: about one block a compute unit, at least 256 rows each (two blocks a unit

@@ -61,13 +61,14 @@ __device__ inline bf16x8 mx4_to_bf16x8(uint32_t w, float scale) {
   return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// Of a block's 32 elements the first n are kept (n >= 32: all, n <= 0: none).
+// Of eight elements, or of a block's 32, the first n are kept (n from 8, 32 on: all; n <= 0: none).
+__device__ inline uint32_t mx4_keep8(uint32_t w, int n) {
+  return w & (n >= 8 ? ~0u : n <= 0 ? 0u : (1u << (4 * n)) - 1u);
+}
+
 __device__ inline u32x4 mx4_keep(u32x4 q, int n) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int left = n - 8 * j;
-    q[j] &= left >= 8 ? ~0u : left <= 0 ? 0u : (1u << (4 * left)) - 1u;
-  }
+  for (int j = 0; j < 4; ++j) q[j] = mx4_keep8(q[j], n - 8 * j);
   return q;
 }
 
