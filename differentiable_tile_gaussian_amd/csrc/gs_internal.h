@@ -96,12 +96,6 @@ size_t bin_sort_ws_bytes(uint32_t pairs);
 size_t sort_pairs_ws_bytes(int64_t capacity);
 hipError_t launch_sort_pairs_u32(uint32_t* keys, uint32_t* vals, uint32_t count, int64_t capacity, void* ws,
                                  hipStream_t s);
-// The places 0 .. count - 1 in the order of their entries (index: int32, int64 where wide; outside
-// [0, entries): behind all others, as entry `entries`), equal ones in their own order.  keys,
-// vals: count entries each.
-size_t sort_index_ws_bytes(int64_t count);
-hipError_t launch_sort_index(const void* index, bool wide, uint32_t count, uint32_t entries, uint32_t* keys, uint32_t* vals,
-                             void* ws, hipStream_t s);
 hipError_t launch_bin_sort(const gs_proj& proj, int n, const gs_camera& cam, uint32_t pairs, uint32_t* keys,
                            uint32_t* vals, uint32_t* ranges, void* ws, hipStream_t s);
 

@@ -4,9 +4,10 @@
 // flight.  The backward adds the rows of one entry in the order of their places, without
 // atomics: the indices are sorted (sort.hip's stable radix passes over the bits that the
 // entries have), and the sorted list is cut into slots of equal length, however the entries are
-// used.  A slot adds up its runs of equal entries in float32; the runs inside it are whole and are
-// written, its first and last may go on next door and become two rows of partial sums, which form
-// a sorted list again, 2 / kSlot as long.  A list of one slot has no neighbours and ends it.
+// used.  The lanes of a slot add up its runs of equal entries in float32, and runs that reach into
+// the next slots of the block are joined through LDS.  What goes on in another block becomes a row of
+// partial sums, at most one at each end of a block, and a second kernel joins those: the block in
+// which a run begins adds the rows of the blocks that it reaches.
 #include "lookup.h"
 #include "profile.h"
 
@@ -53,94 +54,237 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(MatArg table, const vo
 
 // ------------------------------------------------------------- the gradient
 
-__global__ void __launch_bounds__(kThreads) zero_rows_kernel(MatArg m, int64_t rows, int cols, int lanes) {
-  const int lane = threadIdx.x & (lanes - 1), col = (int(blockIdx.y) * lanes + lane) * 8;
-  const int64_t row = int64_t(blockIdx.x) * (kThreads / lanes) + threadIdx.x / lanes;
-  const float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (row < rows && col < cols) store8(m, row, col, v, cols - col);
-}
-
-constexpr int kSlot = 64;      // places of a slot
 constexpr int kFlight = 8;     // rows loaded ahead
+constexpr int kLong = 32;      // blocks' sums that a run's own lanes add
+constexpr uint32_t kNoKey = 0xffffffffu;
+// Of a slot, and of a block: no run goes on behind it; the last run, which begins in it; the only run,
+// which began in front of it.
+enum { kEnds = 0, kBegins = 1, kThrough = 2 };
 
 struct SegArgs {
-  MatArg src;               // the list's rows
-  const uint32_t* key;      // their entries, ascending
-  const uint32_t* order;    // place -> row of src (nullptr: the place itself)
+  MatArg src;               // the rows, in their places
+  const uint32_t* key;      // entries, ascending
+  const uint32_t* order;    // their places
   MatArg dst;
   float scale;
   uint32_t entries;
   int cols;
-  int64_t count, slots;
-  float* part;              // [2 slots][cols]
-  uint32_t* part_key;
+  int64_t count, slots, blocks;
+  int per_slot, per_block;  // places
+  float* part;              // [2 blocks][cols]: of a block, the run that came from before, the run that goes on
+  uint32_t* flags;          // [blocks]
   int lanes;
 };
 
+// This thread's share of the columns: what is loaded (at), and whether its results are its own.
+struct Share {
+  Held c;
+  int col, at, n;
+  bool own;
+};
+
+template <bool NARROW>
+__device__ inline Share share_of(const SegArgs& a) {
+  Share s;
+  s.col = (int(blockIdx.y) * a.lanes + (threadIdx.x & (a.lanes - 1))) * 8;
+  s.c = held_at(s.col, a.cols);
+  s.at = NARROW ? s.col : s.c.at;
+  s.n = NARROW ? a.cols - s.col : 8;
+  s.own = NARROW ? s.n > 0 : s.c.skip < 8;
+  return s;
+}
+
+template <bool NARROW>
+__device__ inline Raw8 load_share(const MatArg& m, int64_t row, const Share& s) {
+  return NARROW ? load_raw8(m, row, s.col, s.n) : load_held(m, row, s.c);
+}
+
+__device__ inline void write_entry(const SegArgs& a, const Share& s, uint32_t key, const float sum[8]) {
+  if (!s.own || key >= a.entries) return;
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = sum[i] * a.scale;
+  store8(a.dst, key, s.at, v, s.n);
+}
+
 template <bool NARROW>
 __global__ void __launch_bounds__(kThreads) segment_sums_kernel(SegArgs a) {
-  const int lane = threadIdx.x & (a.lanes - 1);
-  const int64_t slot = int64_t(blockIdx.x) * (kThreads / a.lanes) + threadIdx.x / a.lanes;
-  const int col = (int(blockIdx.y) * a.lanes + lane) * 8;
-  if (slot >= a.slots) return;
-  const Held c = held_at(col, a.cols);
-  const bool own = NARROW ? col < a.cols : c.skip < 8;
-  const int at = NARROW ? col : c.at, n = NARROW ? a.cols - col : 8;
-  const int64_t first = slot * kSlot, last = first + kSlot < a.count ? first + kSlot : a.count;
+  __shared__ float heads[kThreads * 8];   // a slot's run that came from before
+  __shared__ int states[kThreads];
+  const int groups = kThreads / a.lanes, group = threadIdx.x / a.lanes;
+  const bool leads = (threadIdx.x & (a.lanes - 1)) == 0 && blockIdx.y == 0;
+  const int64_t slot = int64_t(blockIdx.x) * groups + group;
+  const Share s = share_of<NARROW>(a);
+  const int64_t first = slot * a.per_slot, last = first + a.per_slot < a.count ? first + a.per_slot : a.count;
   const MatArg part{reinterpret_cast<char*>(a.part), nullptr, a.cols, 0, GS_MAT_F32};
   float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  uint32_t key = a.key[first];
-  bool head = a.slots > 1;    // the present run began at the slot's edge
-  auto flush = [&](bool edge) {
-    if (edge) {
-      if (own) store8(part, 2 * slot + (head ? 0 : 1), at, sum, n);
-    } else if (own && key < a.entries) {
-      float v[8];
+  float* head = heads + threadIdx.x * 8;
+  uint32_t key = kNoKey;
+  int state = kEnds;
+  bool block_head = false;    // group 0: its first run came from the block before
+  if (slot < a.slots) {
+    const uint32_t before = first > 0 ? a.key[first - 1] : kNoKey, behind = last < a.count ? a.key[last] : kNoKey;
+    uint32_t keys[kFlight], places[kFlight];
+    auto fetch = [&](int64_t p0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = sum[i] * a.scale;
-      store8(a.dst, key, at, v, n);
-    }
-  };
-  const uint32_t first_key = key;
-  for (int64_t p0 = first; p0 < last; p0 += kFlight) {
-    uint32_t keys[kFlight];
-    Raw8 raw[kFlight];
-#pragma unroll
-    for (int u = 0; u < kFlight; ++u) {
-      const int64_t p = p0 + u < last ? p0 + u : last - 1;
-      keys[u] = a.key[p];
-      const int64_t row = a.order ? int64_t(a.order[p]) : p;
-      raw[u] = NARROW ? load_raw8(a.src, row, col, n) : load_held(a.src, row, c);
-    }
-#pragma unroll
-    for (int u = 0; u < kFlight; ++u) {
-      if (p0 + u >= last) break;
-      if (keys[u] != key) {
-        flush(head);
-        head = false;
-        key = keys[u];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
+      for (int u = 0; u < kFlight; ++u) {
+        const int64_t p = p0 + u < last ? p0 + u : last - 1;
+        keys[u] = a.key[p];
+        places[u] = a.order[p];
       }
-      float v[8];
-      raw8_to_float(raw[u], a.src.type, v);
+    };
+    fetch(first);
+    key = keys[0];
+    bool from_before = key == before;    // the present run began in front of the slot
+    block_head = group == 0 && from_before;
+    for (int64_t p0 = first; p0 < last; p0 += kFlight) {
+      Raw8 raw[kFlight];
+      uint32_t now[kFlight];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] += v[i];
+      for (int u = 0; u < kFlight; ++u) {
+        raw[u] = load_share<NARROW>(a.src, places[u], s);
+        now[u] = keys[u];
+      }
+      fetch(p0 + kFlight < last ? p0 + kFlight : p0);
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u) {
+        if (p0 + u >= last) break;
+        if (now[u] != key) {
+          if (!from_before) write_entry(a, s, key, sum);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (from_before) head[i] = sum[i];
+            sum[i] = 0.0f;
+          }
+          from_before = false;
+          key = now[u];
+        }
+        float v[8];
+        raw8_to_float(raw[u], a.src.type, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] += v[i];
+      }
+    }
+    state = key != behind ? kEnds : from_before ? kThrough : kBegins;
+    if (from_before) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) head[i] = sum[i];
+    } else if (state == kEnds) {
+      write_entry(a, s, key, sum);
     }
   }
-  if (a.slots == 1) {
-    flush(false);
-    return;
-  }
-  flush(true);
-  if (head) {    // one run alone: nothing is left for the other row
+  states[threadIdx.x] = state;
+  __syncthreads();
+  auto state_of = [&](int g) { return states[g * a.lanes]; };
+  auto add_head = [&](int g) {
+    const float* h = heads + (g * a.lanes + (threadIdx.x & (a.lanes - 1))) * 8;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
-    if (own) store8(part, 2 * slot + 1, at, sum, n);
+    for (int i = 0; i < 8; ++i) sum[i] += h[i];
+  };
+  if (state == kBegins) {    // the run ends in a later slot of the block, or leaves it
+    int g = group + 1;
+    for (; g < groups; ++g) {
+      add_head(g);
+      if (state_of(g) != kThrough) break;
+    }
+    if (g < groups) {
+      write_entry(a, s, key, sum);
+    } else {
+      if (s.own) store8(part, 2 * int64_t(blockIdx.x) + 1, s.at, sum, s.n);
+      if (leads) a.flags[blockIdx.x] = kBegins;
+    }
   }
-  if (lane == 0 && blockIdx.y == 0) {
-    a.part_key[2 * slot] = first_key;
-    a.part_key[2 * slot + 1] = key;
+  if (block_head) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] = head[i];
+    int g = 0;
+    while (state_of(g) == kThrough && ++g < groups) add_head(g);
+    if (s.own) store8(part, 2 * int64_t(blockIdx.x), s.at, sum, s.n);
+    if (leads && g == groups) a.flags[blockIdx.x] = kThrough;
+  }
+  if (leads && state == kEnds && (group == groups - 1 || slot == a.slots - 1)) a.flags[blockIdx.x] = kEnds;
+}
+
+// The runs that reach over a block's end, from the blocks in which they begin.
+template <bool NARROW>
+__global__ void __launch_bounds__(kThreads) segment_joins_kernel(SegArgs a) {
+  __shared__ float sums[kThreads * 8];
+  __shared__ int is_long_run[kThreads], beyond;
+  const int groups = kThreads / a.lanes, group = threadIdx.x / a.lanes;
+  const int64_t block = int64_t(blockIdx.x) * groups + group;
+  const Share s = share_of<NARROW>(a);
+  const MatArg part{reinterpret_cast<char*>(a.part), nullptr, a.cols, 0, GS_MAT_F32};
+  auto add = [&](float sum[8], int64_t row) {
+    float v[8];
+    raw8_to_float(load_share<NARROW>(part, row, s), GS_MAT_F32, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] += v[i];
+  };
+  auto key_of = [&](int64_t block) { return a.key[(block + 1) * a.per_block - 1]; };   // (the last block's run does not go on)
+  bool is_long = false;
+  if (block < a.blocks && a.flags[block] == kBegins) {
+    const uint32_t key = key_of(block);
+    float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    add(sum, 2 * block + 1);
+    int reach = 0;    // the blocks that the run reaches
+    for (int i = 1; i <= kLong && reach == 0; i += 8) {
+      uint32_t flag[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) flag[u] = a.flags[block + i + u < a.blocks ? block + i + u : a.blocks - 1];
+#pragma unroll
+      for (int u = 7; u >= 0; --u) reach = flag[u] != kThrough ? i + u : reach;
+    }
+    is_long = reach == 0;
+    if (!is_long) {
+#pragma unroll 4
+      for (int i = 1; i <= reach; ++i) add(sum, 2 * (block + i));
+      write_entry(a, s, key, sum);
+    }
+  }
+  // the long ones, in the order of their blocks
+  is_long_run[threadIdx.x] = 0;
+  __syncthreads();
+  if (is_long && (threadIdx.x & (a.lanes - 1)) == 0) is_long_run[group] = 1;
+  __syncthreads();
+  for (int g = 0; g < groups; ++g) {
+    if (!is_long_run[g]) continue;
+    const int64_t from = int64_t(blockIdx.x) * groups + g;
+    // the block in which the run ends
+    constexpr int kLook = 4;
+    int64_t end = from + 1;
+    for (;; end += kThreads * kLook) {
+      if (threadIdx.x == 0) beyond = kThreads * kLook;
+      __syncthreads();
+      int at = kThreads * kLook;
+#pragma unroll
+      for (int u = kLook - 1; u >= 0; --u) {
+        const int64_t look = end + u * kThreads + threadIdx.x;
+        at = a.flags[look < a.blocks ? look : a.blocks - 1] != kThrough ? u * kThreads + threadIdx.x : at;
+      }
+      if (at < kThreads * kLook) atomicMin(&beyond, at);
+      __syncthreads();
+      const int b = beyond;
+      __syncthreads();
+      if (b < kThreads * kLook) {
+        end += b;
+        break;
+      }
+    }
+    float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (group == 0) add(sum, 2 * from + 1);
+#pragma unroll 8
+    for (int64_t at = from + 1 + group; at <= end; at += groups) add(sum, 2 * at);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sums[threadIdx.x * 8 + i] = sum[i];
+    for (int d = groups / 2; d > 0; d /= 2) {
+      __syncthreads();
+      if (group < d) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sums[threadIdx.x * 8 + i] = sum[i] += sums[(threadIdx.x + d * a.lanes) * 8 + i];
+      }
+    }
+    if (group == 0) write_entry(a, s, key_of(from), sum);
+    __syncthreads();
   }
 }
 
@@ -151,14 +295,19 @@ int lanes_for(int cols) {
 }
 
 inline size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
-inline int64_t slots_of(int64_t count) { return (count + kSlot - 1) / kSlot; }
 
-// The sorted indices, the sort's space, and the lists of partial sums (two take turns).
+// Places of a slot: few enough to give each compute unit four waves.
+int per_slot(int64_t rows, int lanes) {
+  for (int n = 32; n > 8; n /= 2)
+    if (rows * lanes / 64 / n >= 1024) return n;
+  return 8;
+}
+
+// The sorted indices, the sort's space, and the partial sums.
 struct BwdWs {
-  uint32_t *key, *order;
+  uint32_t *key, *order, *flags;
   void* sort;
-  float* part[2];
-  uint32_t* part_key[2];
+  float* part;
   size_t bytes;
 };
 
@@ -174,12 +323,11 @@ BwdWs carve(void* ws, int64_t rows, int cols) {
   w.key = reinterpret_cast<uint32_t*>(take(size_t(rows) * 4));
   w.order = reinterpret_cast<uint32_t*>(take(size_t(rows) * 4));
   w.sort = take(sort_index_ws_bytes(rows));
-  int64_t count = rows;
-  for (int i = 0; i < 2; ++i) {
-    count = 2 * slots_of(count);
-    w.part[i] = reinterpret_cast<float*>(take(size_t(count) * cols * 4));
-    w.part_key[i] = reinterpret_cast<uint32_t*>(take(size_t(count) * 4));
-  }
+  // at least as many blocks as fewer rows take (512 where slots are longest for their number)
+  const int lanes = lanes_for(cols), n = per_slot(rows, lanes);
+  const int64_t here = div_up(rows, int64_t(n) * (kThreads / lanes)), fewer = n > 8 ? 512 : 0, blocks = here > fewer ? here : fewer;
+  w.flags = reinterpret_cast<uint32_t*>(take(size_t(blocks) * 4));
+  w.part = reinterpret_cast<float*>(take(size_t(blocks) * 2 * cols * 4));
   w.bytes = at;
   return w;
 }
@@ -206,29 +354,21 @@ hipError_t launch_lookup_bwd(const MatArg& dy, const void* index, bool wide, flo
                              int64_t entries, int cols, void* ws, hipStream_t s) {
   const int lanes = lanes_for(cols);
   const unsigned across = div_up(cols, lanes * 8);
-  {
-    GSK_PROF("lookup_zero", s);
-    for_row_parts(entries, kThreads / lanes, [&](int64_t first, int64_t count, unsigned blocks) {
-      zero_rows_kernel<<<dim3(blocks, across), kThreads, 0, s>>>(rows_from(dtable, first), count, cols, lanes);
-    });
-  }
-  if (rows == 0) return hipGetLastError();
   const BwdWs w = carve(ws, rows, cols);
-  hipError_t e = launch_sort_index(index, wide, uint32_t(rows), uint32_t(entries), w.key, w.order, w.sort, s);
-  if (e != hipSuccess) return e;
-  SegArgs a{dy, w.key, w.order, dtable, scale, uint32_t(entries), cols, rows, slots_of(rows), w.part[0], w.part_key[0], lanes};
-  for (int i = 0;; ++i) {
+  hipError_t e = launch_sort_index(index, wide, uint32_t(rows), uint32_t(entries), w.key, w.order, dtable, cols, w.sort, s);
+  if (e != hipSuccess || rows == 0) return e;
+  const int n = per_slot(rows, lanes), per_block = n * (kThreads / lanes);
+  const SegArgs a{dy,   w.key, w.order, dtable,    scale,  uint32_t(entries), cols, rows, (rows + n - 1) / n, div_up(rows, per_block), n,
+                  per_block, w.part, w.flags, lanes};
+  {
     GSK_PROF("lookup_sums", s);
     const auto kernel = cols < 8 ? &segment_sums_kernel<true> : &segment_sums_kernel<false>;
-    kernel<<<dim3(div_up(a.slots, kThreads / lanes), across), kThreads, 0, s>>>(a);
-    if (a.slots == 1) break;
-    a.src = MatArg{reinterpret_cast<char*>(a.part), nullptr, cols, 0, GS_MAT_F32};
-    a.key = a.part_key;
-    a.order = nullptr;
-    a.count = 2 * a.slots;
-    a.slots = slots_of(a.count);
-    a.part = w.part[(i + 1) % 2];
-    a.part_key = w.part_key[(i + 1) % 2];
+    kernel<<<dim3(unsigned(a.blocks), across), kThreads, 0, s>>>(a);
+  }
+  if (a.blocks > 1) {
+    GSK_PROF("lookup_joins", s);
+    const auto kernel = cols < 8 ? &segment_joins_kernel<true> : &segment_joins_kernel<false>;
+    kernel<<<dim3(div_up(a.blocks, kThreads / lanes), across), kThreads, 0, s>>>(a);
   }
   return hipGetLastError();
 }

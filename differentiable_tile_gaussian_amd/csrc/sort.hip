@@ -38,6 +38,7 @@
 #include <cstring>
 
 #include "gs_internal.h"
+#include "lookup.h"
 #include "profile.h"
 
 namespace gsk {
@@ -47,6 +48,10 @@ constexpr int kSortThreads = 256;
 constexpr int kWaves = kSortThreads / 64;
 constexpr int kSortItems = 16;
 constexpr int kSortTile = kSortThreads * kSortItems;   // 4096 items per block
+// Index sorts of up to 4M places take 1024 a block: they are short of blocks, not of histogram
+// (1M places in two passes: 4096 a block 60 us).
+constexpr int kIndexItems = 4;
+constexpr int64_t kIndexMost = int64_t(1) << 22;
 constexpr int kDigitBits = 9;
 constexpr int kRadix = 1 << kDigitBits;                 // 512 digits
 constexpr int kDepthPasses = 3;                         // always made: d < 2^27
@@ -175,22 +180,21 @@ __device__ inline uint2 block_scan2(uint32_t x, uint32_t y, uint32_t* s, uint32_
   return make_uint2(px + ix - x, py + iy - y);
 }
 
-template <int SRC>
-__global__ void __launch_bounds__(kSortThreads) radix_upsweep_kernel(PassIn in, DepthPlan dp, int shift, uint32_t mask,
-                                                                      int nb, uint32_t* __restrict__ hist) {
+template <int SRC, int ITEMS>
+__device__ inline void radix_upsweep(PassIn in, DepthPlan dp, int shift, uint32_t mask, uint32_t* __restrict__ hist) {
   __shared__ uint32_t s_hist[kRadix];
   if (!pass_runs(dp)) return;
   plan_source(in, dp);
   for (int d = threadIdx.x; d < kRadix; d += kSortThreads) s_hist[d] = 0u;
   __syncthreads();
   const uint32_t count = pass_count(in);
-  const uint32_t base = blockIdx.x * kSortTile;
+  const uint32_t base = blockIdx.x * uint32_t(kSortThreads * ITEMS);
   uint32_t kmax = 0u;
   if (base < count) {
-    uint32_t key[kSortItems];
-    bool ok[kSortItems];
+    uint32_t key[ITEMS];
+    bool ok[ITEMS];
 #pragma unroll
-    for (int k = 0; k < kSortItems; ++k) {
+    for (int k = 0; k < ITEMS; ++k) {
       const uint32_t idx = base + k * kSortThreads + threadIdx.x;
       uint32_t val;
       ok[k] = load_item<SRC>(in, min(idx, count - 1), key[k], val) && idx < count;
@@ -198,7 +202,7 @@ __global__ void __launch_bounds__(kSortThreads) radix_upsweep_kernel(PassIn in, 
     if (dp.pass >= 0) {
       // depth digits are spread: one LDS atomic per item
 #pragma unroll
-      for (int k = 0; k < kSortItems; ++k) {
+      for (int k = 0; k < ITEMS; ++k) {
         if (ok[k]) {
           atomicAdd(&s_hist[(key[k] >> shift) & mask], 1u);
           kmax = max(kmax, key[k]);
@@ -211,7 +215,7 @@ __global__ void __launch_bounds__(kSortThreads) radix_upsweep_kernel(PassIn in, 
       const uint64_t lt_mask = (uint64_t(1) << __lane_id()) - 1;
       const int nbits = __popc(mask);
 #pragma unroll
-      for (int k = 0; k < kSortItems; ++k) {
+      for (int k = 0; k < ITEMS; ++k) {
         const uint32_t d = (key[k] >> shift) & mask;
         uint64_t peers = __ballot(ok[k]);
         for (int b = 0; b < nbits; ++b) {
@@ -234,6 +238,27 @@ __global__ void __launch_bounds__(kSortThreads) radix_upsweep_kernel(PassIn in, 
   __syncthreads();
   // only the pass's digits have rows (a tile pass of 6 bits uses 64 of them)
   for (int d = threadIdx.x; d <= int(mask); d += kSortThreads) hist[hist_at(d, blockIdx.x)] = s_hist[d];
+}
+
+template <int SRC>
+__global__ void __launch_bounds__(kSortThreads) radix_upsweep_kernel(PassIn in, DepthPlan dp, int shift, uint32_t mask,
+                                                                      int nb, uint32_t* __restrict__ hist) {
+  radix_upsweep<SRC, kSortItems>(in, dp, shift, mask, hist);
+}
+
+// An index sort's histograms (of nb blocks).  The first pass's blocks, and more where the table is
+// larger, also clear the rows of a table, whose writes take the memory that the histogram leaves idle.
+template <int SRC, int ITEMS>
+__global__ void __launch_bounds__(kSortThreads) index_upsweep_kernel(PassIn in, int shift, uint32_t mask, int nb,
+                                                                      uint32_t* __restrict__ hist, MatArg table,
+                                                                      int64_t rows, int cols, int lanes) {
+  if (SRC != kFromKeys) {
+    const float zeros[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    const int lane = threadIdx.x & (lanes - 1), per = kSortThreads / lanes;
+    for (int64_t row = int64_t(blockIdx.x) * per + threadIdx.x / lanes; row < rows; row += int64_t(gridDim.x) * per)
+      for (int col = lane * 8; col < cols; col += lanes * 8) store8(table, row, col, zeros, cols - col);
+  }
+  if (int(blockIdx.x) < nb) radix_upsweep<SRC, ITEMS>(in, kNoPlan, shift, mask, hist);
 }
 
 // Blocks (digit d, segment s): hist_scan[d][b] = sum of hist[d][b'] over b' < b, rowtot[d]
@@ -320,13 +345,14 @@ __global__ void __launch_bounds__(kSortThreads) radix_scan_kernel(DepthPlan dp, 
 // Gaussians).  The depth plan's last pass writes no keys; it looks every value (a
 // Gaussian id) up in val_rect and writes the Gaussian's tile rectangle and tile count
 // beside it.
-template <int SRC>
+template <int SRC, int ITEMS = kSortItems>
 __global__ void __launch_bounds__(kSortThreads) radix_downsweep_kernel(
     PassIn in, DepthPlan dp, int shift, uint32_t mask, int nb, const uint32_t* __restrict__ hist_scan,
     const uint32_t* __restrict__ rowtot, uint32_t* keys_out, uint32_t* vals_out, uint32_t* __restrict__ count_out,
     const uint2* __restrict__ val_rect, uint2* __restrict__ rect_out, uint32_t* __restrict__ counts_out) {
-  __shared__ uint32_t s_keys[kSortTile];
-  __shared__ uint32_t s_vals[kSortTile];
+  constexpr int kTileItems = kSortThreads * ITEMS;
+  __shared__ uint32_t s_keys[kTileItems];
+  __shared__ uint32_t s_vals[kTileItems];
   __shared__ uint16_t s_whist[kWaves][kRadix];   // per-wave digit counts, then starts (<= 4096)
   __shared__ uint16_t s_local[kRadix];           // block-local start of each digit
   __shared__ uint32_t s_global[kRadix];          // global start of (digit, this block)
@@ -362,7 +388,7 @@ __global__ void __launch_bounds__(kSortThreads) radix_downsweep_kernel(
     }
   }
   const uint32_t count = pass_count(in);
-  const uint32_t base = blockIdx.x * kSortTile;
+  const uint32_t base = blockIdx.x * uint32_t(kTileItems);
   if (base >= count) return;   // uniform per block
   __syncthreads();
   // Each wave ranks its own 1024 consecutive items, 64 per round, with a wave-private
@@ -370,7 +396,7 @@ __global__ void __launch_bounds__(kSortThreads) radix_downsweep_kernel(
   // before its round plus its rank in the round (a ballot per digit bit gives each lane its peers;
   // CDNA has no match-any).  Waves, rounds and lanes follow the items' order, so the
   // placement is stable.
-  constexpr int kWaveItems = kSortTile / kWaves;
+  constexpr int kWaveItems = kTileItems / kWaves;
   constexpr int kRounds = kWaveItems / 64;
   const uint64_t lt_mask = (uint64_t(1) << lane) - 1;
   const int nbits = __popc(mask);
@@ -437,9 +463,9 @@ __global__ void __launch_bounds__(kSortThreads) radix_downsweep_kernel(
   __syncthreads();
   // out in sorted order, sixteen places per thread (the last depth pass's rectangle
   // gathers issued together)
-  uint32_t okey[kSortItems], oval[kSortItems], dst[kSortItems];
+  uint32_t okey[ITEMS], oval[ITEMS], dst[ITEMS];
 #pragma unroll
-  for (int j = 0; j < kSortItems; ++j) {
+  for (int j = 0; j < ITEMS; ++j) {
     const uint32_t k = tid + j * kSortThreads;
     okey[j] = s_keys[k];
     oval[j] = s_vals[k];
@@ -447,11 +473,11 @@ __global__ void __launch_bounds__(kSortThreads) radix_downsweep_kernel(
     dst[j] = s_global[d] + (k - s_local[d]);
   }
   if (last) {
-    uint2 rc[kSortItems];
+    uint2 rc[ITEMS];
 #pragma unroll
-    for (int j = 0; j < kSortItems; ++j) rc[j] = val_rect[tid + j * kSortThreads < block_total ? oval[j] : 0u];
+    for (int j = 0; j < ITEMS; ++j) rc[j] = val_rect[tid + j * kSortThreads < block_total ? oval[j] : 0u];
 #pragma unroll
-    for (int j = 0; j < kSortItems; ++j) {
+    for (int j = 0; j < ITEMS; ++j) {
       if (tid + j * kSortThreads < block_total) {
         vals_out[dst[j]] = oval[j];
         rect_out[dst[j]] = rc[j];
@@ -460,7 +486,7 @@ __global__ void __launch_bounds__(kSortThreads) radix_downsweep_kernel(
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < kSortItems; ++j) {
+    for (int j = 0; j < ITEMS; ++j) {
       if (tid + j * kSortThreads < block_total) {
         keys_out[dst[j]] = okey[j];
         vals_out[dst[j]] = oval[j];
@@ -803,31 +829,84 @@ hipError_t launch_sort_pairs_u32(uint32_t* keys, uint32_t* vals, uint32_t count,
   return hipSuccess;
 }
 
-size_t sort_index_ws_bytes(int64_t n) { return sort_pairs_ws_bytes(n); }
+namespace {
+
+int index_blocks(int64_t n) {
+  return n <= kIndexMost ? int(div_up(n > 0 ? n : 1, kSortThreads * kIndexItems)) : blocks_for(n);
+}
+
+struct IndexWs {
+  uint32_t *keys, *vals;
+  RadixWs r;
+};
+
+size_t carve_index(void* ws, int64_t n, IndexWs* out) {
+  Carver c{static_cast<char*>(ws)};
+  IndexWs w;
+  w.keys = c.take(size_t(n) * 4);
+  w.vals = c.take(size_t(n) * 4);
+  // a workspace for more places serves fewer, which may be cut into more blocks
+  w.r = carve_radix(c, n > kIndexMost ? std::max(index_blocks(n), index_blocks(kIndexMost)) : index_blocks(n));
+  if (out) *out = w;
+  return c.off;
+}
+
+template <int SRC, int ITEMS>
+hipError_t index_pass(const PassIn& in, int nb, int shift, int bits, const RadixWs& w, uint32_t* keys_out,
+                      uint32_t* vals_out, const MatArg& table, int64_t rows, int cols, hipStream_t s) {
+  const uint32_t mask = (1u << bits) - 1u;
+  {
+    GSK_PROF("index_upsweep", s);
+    // eight stores of a thread and more in the table's blocks
+    const int64_t units = SRC == kFromKeys ? 0 : rows * ((cols + 7) / 8);
+    const int clear = int(std::min<int64_t>(2048, div_up(units, kSortThreads * 8)));
+    int lanes = 1;   // of a row of the table, 8 columns each
+    while (lanes < 64 && lanes * 8 < cols) lanes *= 2;
+    index_upsweep_kernel<SRC, ITEMS>
+        <<<std::max(nb, clear), kSortThreads, 0, s>>>(in, shift, mask, nb, w.hist, table, rows, cols, lanes);
+  }
+  {
+    GSK_PROF("radix_scan", s);
+    const int segs = std::max(1, int(div_up(div_up(nb, kHistGroup), kScanStepGroups)));
+    radix_scan_kernel<<<dim3(int(mask) + 1, segs), kSortThreads, 0, s>>>(kNoPlan, nb, w.hist, w.hist_scan, w.rowtot);
+  }
+  GSK_PROF("radix_downsweep", s);
+  radix_downsweep_kernel<SRC, ITEMS><<<nb, kSortThreads, 0, s>>>(in, kNoPlan, shift, mask, nb, w.hist_scan, w.rowtot, keys_out,
+                                                                 vals_out, nullptr, nullptr, nullptr, nullptr);
+  return hipGetLastError();
+}
+
+template <int SRC>
+hipError_t index_pass(const PassIn& in, int shift, int bits, const RadixWs& w, uint32_t* keys_out, uint32_t* vals_out,
+                      const MatArg& table, int64_t rows, int cols, hipStream_t s) {
+  const int nb = index_blocks(in.count);
+  return in.count <= kIndexMost ? index_pass<SRC, kIndexItems>(in, nb, shift, bits, w, keys_out, vals_out, table, rows, cols, s)
+                                : index_pass<SRC, kSortItems>(in, nb, shift, bits, w, keys_out, vals_out, table, rows, cols, s);
+}
+
+}  // namespace
+
+size_t sort_index_ws_bytes(int64_t n) { return carve_index(nullptr, n, nullptr); }
 
 hipError_t launch_sort_index(const void* index, bool wide, uint32_t count, uint32_t entries, uint32_t* keys, uint32_t* vals,
-                             void* ws, hipStream_t s) {
-  Carver c{static_cast<char*>(ws)};
-  uint32_t* alt_k = c.take(size_t(count) * 4);
-  uint32_t* alt_v = c.take(size_t(count) * 4);
-  const RadixWs r = carve_radix(c, blocks_for(count));
-  const int nb = blocks_for(count);
+                             const MatArg& table, int cols, void* ws, hipStream_t s) {
+  IndexWs w;
+  carve_index(ws, count, &w);
   const int all = std::max(1, bits_for(entries)), passes = (all + kDigitBits - 1) / kDigitBits;
   const int low = (all + passes - 1) / passes;   // as evenly as the tile sort's
   for (int pass = 0; pass < passes; ++pass) {
     const bool last = (passes - 1 - pass) % 2 == 0;   // passes that write keys and vals
-    uint32_t *ko = last ? keys : alt_k, *vo = last ? vals : alt_v;
+    uint32_t *ko = last ? keys : w.keys, *vo = last ? vals : w.vals;
     const int shift = low * pass, bits = std::min(low, all - shift);
-    PassIn in{last ? alt_k : keys, last ? alt_v : vals, nullptr, nullptr, 0u, count, nullptr};
+    PassIn in{last ? w.keys : keys, last ? w.vals : vals, nullptr, nullptr, 0u, count, nullptr};
     if (pass == 0) {
       in.keys = static_cast<const uint32_t*>(index);
       in.key_base = entries;
     }
-    const hipError_t e =
-        pass > 0 ? radix_pass<kFromKeys>(in, kNoPlan, nb, shift, bits, r, ko, vo, nullptr, nullptr, nullptr, nullptr, s)
-        : wide   ? radix_pass<kFromIndex64>(in, kNoPlan, nb, shift, bits, r, ko, vo, nullptr, nullptr, nullptr, nullptr, s)
-                 : radix_pass<kFromIndex>(in, kNoPlan, nb, shift, bits, r, ko, vo, nullptr, nullptr, nullptr, nullptr, s);
-    if (e != hipSuccess) return e;
+    const hipError_t e = pass > 0 ? index_pass<kFromKeys>(in, shift, bits, w.r, ko, vo, table, entries, cols, s)
+                         : wide   ? index_pass<kFromIndex64>(in, shift, bits, w.r, ko, vo, table, entries, cols, s)
+                                  : index_pass<kFromIndex>(in, shift, bits, w.r, ko, vo, table, entries, cols, s);
+    if (e != hipSuccess || count == 0) return e;   // without places there is only the table to clear
   }
   return hipSuccess;
 }
