@@ -278,7 +278,7 @@ size_t gs_workspace_bytes(int32_t which_call, int64_t n, uint32_t pairs, int32_t
     case GS_WS_CAMERA_GRAD: return gsk::camera_grad_ws_bytes(n < 0 ? 0 : n);
     case GS_WS_RELOCATE: return gsk::relocate_ws_bytes(n < 0 ? 0 : n);
     case GS_WS_RMSNORM_BWD: return n >= 0 && width_ok(W) ? gsk::rmsnorm_bwd_ws_bytes(n, W) : 0;
-    case GS_WS_LOOKUP_BWD: return n >= 0 && n < (int64_t(1) << 31) && width_ok(W) ? gsk::lookup_bwd_ws_bytes(n, W) : 0;
+    case GS_WS_LOOKUP_BWD: return n >= 0 && n < (int64_t(1) << 31) && width_ok(W) && H > 0 ? gsk::lookup_bwd_ws_bytes(n, W, H) : 0;
     case GS_WS_CLIP_GRADS: return gsk::clip_ws_bytes();
     case GS_WS_LINEAR_BWD: return n >= 0 && width_ok(W) && width_ok(H) ? gsk::linear_bwd_ws_bytes(n, W, H) : 0;
     default: return 0;
@@ -845,7 +845,7 @@ int32_t gs_lookup_bwd(const gs_matrix* dy, const void* index, int32_t index_byte
   int32_t st;
   if ((st = check_lookup(dtable, "dtable", dy, "dy", index, index_bytes, scale)) != GS_OK) return st;
   if (same_data(dy, dtable)) return fail(GS_ERR_INVALID_ARG, "the output is one of the inputs");
-  const size_t need = gsk::lookup_bwd_ws_bytes(dy->rows, int(dy->cols));
+  const size_t need = gsk::lookup_bwd_ws_bytes(dy->rows, int(dy->cols), dtable->rows);
   if (need > 0 && (!ws || ws_bytes < need)) return fail(GS_ERR_CAPACITY, "lookup_bwd workspace needs %zu bytes", need);
   const hipError_t e = gsk::launch_lookup_bwd(gsk::mat_arg(dy), index, index_bytes == 8, scale, gsk::mat_arg(dtable),
                                               dy->rows, dtable->rows, int(dy->cols), ws, as_stream(stream));

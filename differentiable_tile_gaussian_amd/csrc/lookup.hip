@@ -7,7 +7,8 @@
 // used.  The lanes of a slot add up its runs of equal entries in float32, and runs that reach into
 // the next slots of the block are joined through LDS.  What goes on in another block becomes a row of
 // partial sums, at most one at each end of a block, and a second kernel joins those: the block in
-// which a run begins adds the rows of the blocks that it reaches.
+// which a run begins adds the rows of the blocks that it reaches.  The first kernel also marks the entries
+// that have rows, and the second writes zeros to the others.
 #include "lookup.h"
 #include "profile.h"
 
@@ -73,6 +74,7 @@ struct SegArgs {
   int per_slot, per_block;  // places
   float* part;              // [2 blocks][cols]: of a block, the run that came from before, the run that goes on
   uint32_t* flags;          // [blocks]
+  uint8_t* marks;           // [entries]: whether it has rows
   int lanes;
 };
 
@@ -130,13 +132,17 @@ __global__ void __launch_bounds__(kThreads) segment_sums_kernel(SegArgs a) {
       for (int u = 0; u < kFlight; ++u) {
         const int64_t p = p0 + u < last ? p0 + u : last - 1;
         keys[u] = a.key[p];
-        places[u] = a.order[p];
+        places[u] = keys[u] < a.entries ? a.order[p] : 0;   // what has no entry is not fetched for nothing
       }
     };
     fetch(first);
     key = keys[0];
     bool from_before = key == before;    // the present run began in front of the slot
     block_head = group == 0 && from_before;
+    auto mark = [&]() {
+      if (leads && key < a.entries) a.marks[key] = 1;
+    };
+    if (!from_before) mark();
     for (int64_t p0 = first; p0 < last; p0 += kFlight) {
       Raw8 raw[kFlight];
       uint32_t now[kFlight];
@@ -158,6 +164,7 @@ __global__ void __launch_bounds__(kThreads) segment_sums_kernel(SegArgs a) {
           }
           from_before = false;
           key = now[u];
+          mark();
         }
         float v[8];
         raw8_to_float(raw[u], a.src.type, v);
@@ -205,14 +212,24 @@ __global__ void __launch_bounds__(kThreads) segment_sums_kernel(SegArgs a) {
   if (leads && state == kEnds && (group == groups - 1 || slot == a.slots - 1)) a.flags[blockIdx.x] = kEnds;
 }
 
-// The runs that reach over a block's end, from the blocks in which they begin.
+// The runs that reach over a block's end, from the blocks in which they begin; and, behind the
+// first `joins` blocks, the entries without rows.
 template <bool NARROW>
-__global__ void __launch_bounds__(kThreads) segment_joins_kernel(SegArgs a) {
+__global__ void __launch_bounds__(kThreads) segment_joins_kernel(SegArgs a, unsigned joins) {
   __shared__ float sums[kThreads * 8];
-  __shared__ int is_long_run[kThreads], beyond;
+  __shared__ int marked[kThreads], beyond;
   const int groups = kThreads / a.lanes, group = threadIdx.x / a.lanes;
   const int64_t block = int64_t(blockIdx.x) * groups + group;
   const Share s = share_of<NARROW>(a);
+  if (blockIdx.x >= joins) {
+    const int64_t first = int64_t(blockIdx.x - joins) * kThreads, mine = first + threadIdx.x;
+    marked[threadIdx.x] = a.count > 0 && mine < a.entries ? a.marks[mine] : a.count > 0;
+    __syncthreads();
+    const float zeros[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int e = group; e < kThreads && first + e < a.entries; e += groups)
+      if (!marked[e]) write_entry(a, s, uint32_t(first + e), zeros);
+    return;
+  }
   const MatArg part{reinterpret_cast<char*>(a.part), nullptr, a.cols, 0, GS_MAT_F32};
   auto add = [&](float sum[8], int64_t row) {
     float v[8];
@@ -242,12 +259,12 @@ __global__ void __launch_bounds__(kThreads) segment_joins_kernel(SegArgs a) {
     }
   }
   // the long ones, in the order of their blocks
-  is_long_run[threadIdx.x] = 0;
+  marked[threadIdx.x] = 0;
   __syncthreads();
-  if (is_long && (threadIdx.x & (a.lanes - 1)) == 0) is_long_run[group] = 1;
+  if (is_long && (threadIdx.x & (a.lanes - 1)) == 0) marked[group] = 1;
   __syncthreads();
   for (int g = 0; g < groups; ++g) {
-    if (!is_long_run[g]) continue;
+    if (!marked[g]) continue;
     const int64_t from = int64_t(blockIdx.x) * groups + g;
     // the block in which the run ends
     constexpr int kLook = 4;
@@ -306,12 +323,13 @@ int per_slot(int64_t rows, int lanes) {
 // The sorted indices, the sort's space, and the partial sums.
 struct BwdWs {
   uint32_t *key, *order, *flags;
+  uint8_t* marks;
   void* sort;
   float* part;
   size_t bytes;
 };
 
-BwdWs carve(void* ws, int64_t rows, int cols) {
+BwdWs carve(void* ws, int64_t rows, int cols, int64_t entries) {
   BwdWs w;
   char* p = static_cast<char*>(ws);
   size_t at = 0;
@@ -322,6 +340,7 @@ BwdWs carve(void* ws, int64_t rows, int cols) {
   };
   w.key = reinterpret_cast<uint32_t*>(take(size_t(rows) * 4));
   w.order = reinterpret_cast<uint32_t*>(take(size_t(rows) * 4));
+  w.marks = reinterpret_cast<uint8_t*>(take(size_t(entries)));
   w.sort = take(sort_index_ws_bytes(rows));
   // at least as many blocks as fewer rows take (512 where slots are longest for their number)
   const int lanes = lanes_for(cols), n = per_slot(rows, lanes);
@@ -348,28 +367,27 @@ hipError_t launch_lookup_fwd(const MatArg& table, const void* index, bool wide, 
   return hipGetLastError();
 }
 
-size_t lookup_bwd_ws_bytes(int64_t rows, int cols) { return carve(nullptr, rows, cols).bytes; }
+size_t lookup_bwd_ws_bytes(int64_t rows, int cols, int64_t entries) { return carve(nullptr, rows, cols, entries).bytes; }
 
 hipError_t launch_lookup_bwd(const MatArg& dy, const void* index, bool wide, float scale, const MatArg& dtable, int64_t rows,
                              int64_t entries, int cols, void* ws, hipStream_t s) {
   const int lanes = lanes_for(cols);
   const unsigned across = div_up(cols, lanes * 8);
-  const BwdWs w = carve(ws, rows, cols);
-  hipError_t e = launch_sort_index(index, wide, uint32_t(rows), uint32_t(entries), w.key, w.order, dtable, cols, w.sort, s);
-  if (e != hipSuccess || rows == 0) return e;
+  const BwdWs w = carve(ws, rows, cols, entries);
   const int n = per_slot(rows, lanes), per_block = n * (kThreads / lanes);
-  const SegArgs a{dy,   w.key, w.order, dtable,    scale,  uint32_t(entries), cols, rows, (rows + n - 1) / n, div_up(rows, per_block), n,
-                  per_block, w.part, w.flags, lanes};
-  {
+  const SegArgs a{dy,      w.key, w.order, dtable,  scale,  uint32_t(entries), cols, rows, (rows + n - 1) / n, div_up(rows, per_block), n, per_block,
+                  w.part, w.flags, w.marks, lanes};
+  if (rows > 0) {
+    const hipError_t e = launch_sort_index(index, wide, uint32_t(rows), uint32_t(entries), w.key, w.order, w.marks, w.sort, s);
+    if (e != hipSuccess) return e;
     GSK_PROF("lookup_sums", s);
     const auto kernel = cols < 8 ? &segment_sums_kernel<true> : &segment_sums_kernel<false>;
     kernel<<<dim3(unsigned(a.blocks), across), kThreads, 0, s>>>(a);
   }
-  if (a.blocks > 1) {
-    GSK_PROF("lookup_joins", s);
-    const auto kernel = cols < 8 ? &segment_joins_kernel<true> : &segment_joins_kernel<false>;
-    kernel<<<dim3(div_up(a.blocks, kThreads / lanes), across), kThreads, 0, s>>>(a);
-  }
+  GSK_PROF("lookup_joins", s);
+  const auto kernel = cols < 8 ? &segment_joins_kernel<true> : &segment_joins_kernel<false>;
+  const unsigned joins = a.blocks > 1 ? div_up(a.blocks, kThreads / lanes) : 0;
+  kernel<<<dim3(joins + div_up(entries, kThreads), across), kThreads, 0, s>>>(a, joins);
   return hipGetLastError();
 }
 

@@ -246,19 +246,14 @@ __global__ void __launch_bounds__(kSortThreads) radix_upsweep_kernel(PassIn in, 
   radix_upsweep<SRC, kSortItems>(in, dp, shift, mask, hist);
 }
 
-// An index sort's histograms (of nb blocks).  The first pass's blocks, and more where the table is
-// larger, also clear the rows of a table, whose writes take the memory that the histogram leaves idle.
+// An index sort's histograms.  The first pass also clears the entries' marks (16 bytes at a time).
 template <int SRC, int ITEMS>
-__global__ void __launch_bounds__(kSortThreads) index_upsweep_kernel(PassIn in, int shift, uint32_t mask, int nb,
-                                                                      uint32_t* __restrict__ hist, MatArg table,
-                                                                      int64_t rows, int cols, int lanes) {
-  if (SRC != kFromKeys) {
-    const float zeros[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    const int lane = threadIdx.x & (lanes - 1), per = kSortThreads / lanes;
-    for (int64_t row = int64_t(blockIdx.x) * per + threadIdx.x / lanes; row < rows; row += int64_t(gridDim.x) * per)
-      for (int col = lane * 8; col < cols; col += lanes * 8) store8(table, row, col, zeros, cols - col);
-  }
-  if (int(blockIdx.x) < nb) radix_upsweep<SRC, ITEMS>(in, kNoPlan, shift, mask, hist);
+__global__ void __launch_bounds__(kSortThreads) index_upsweep_kernel(PassIn in, int shift, uint32_t mask,
+                                                                      uint32_t* __restrict__ hist, uint4* marks, int64_t marks16) {
+  if (SRC != kFromKeys)
+    for (int64_t i = int64_t(blockIdx.x) * kSortThreads + threadIdx.x; i < marks16; i += int64_t(gridDim.x) * kSortThreads)
+      marks[i] = make_uint4(0u, 0u, 0u, 0u);
+  radix_upsweep<SRC, ITEMS>(in, kNoPlan, shift, mask, hist);
 }
 
 // Blocks (digit d, segment s): hist_scan[d][b] = sum of hist[d][b'] over b' < b, rowtot[d]
@@ -853,17 +848,11 @@ size_t carve_index(void* ws, int64_t n, IndexWs* out) {
 
 template <int SRC, int ITEMS>
 hipError_t index_pass(const PassIn& in, int nb, int shift, int bits, const RadixWs& w, uint32_t* keys_out,
-                      uint32_t* vals_out, const MatArg& table, int64_t rows, int cols, hipStream_t s) {
+                      uint32_t* vals_out, uint4* marks, int64_t marks16, hipStream_t s) {
   const uint32_t mask = (1u << bits) - 1u;
   {
     GSK_PROF("index_upsweep", s);
-    // eight stores of a thread and more in the table's blocks
-    const int64_t units = SRC == kFromKeys ? 0 : rows * ((cols + 7) / 8);
-    const int clear = int(std::min<int64_t>(2048, div_up(units, kSortThreads * 8)));
-    int lanes = 1;   // of a row of the table, 8 columns each
-    while (lanes < 64 && lanes * 8 < cols) lanes *= 2;
-    index_upsweep_kernel<SRC, ITEMS>
-        <<<std::max(nb, clear), kSortThreads, 0, s>>>(in, shift, mask, nb, w.hist, table, rows, cols, lanes);
+    index_upsweep_kernel<SRC, ITEMS><<<nb, kSortThreads, 0, s>>>(in, shift, mask, w.hist, marks, marks16);
   }
   {
     GSK_PROF("radix_scan", s);
@@ -878,10 +867,10 @@ hipError_t index_pass(const PassIn& in, int nb, int shift, int bits, const Radix
 
 template <int SRC>
 hipError_t index_pass(const PassIn& in, int shift, int bits, const RadixWs& w, uint32_t* keys_out, uint32_t* vals_out,
-                      const MatArg& table, int64_t rows, int cols, hipStream_t s) {
+                      uint4* marks, int64_t marks16, hipStream_t s) {
   const int nb = index_blocks(in.count);
-  return in.count <= kIndexMost ? index_pass<SRC, kIndexItems>(in, nb, shift, bits, w, keys_out, vals_out, table, rows, cols, s)
-                                : index_pass<SRC, kSortItems>(in, nb, shift, bits, w, keys_out, vals_out, table, rows, cols, s);
+  return in.count <= kIndexMost ? index_pass<SRC, kIndexItems>(in, nb, shift, bits, w, keys_out, vals_out, marks, marks16, s)
+                                : index_pass<SRC, kSortItems>(in, nb, shift, bits, w, keys_out, vals_out, marks, marks16, s);
 }
 
 }  // namespace
@@ -889,7 +878,9 @@ hipError_t index_pass(const PassIn& in, int shift, int bits, const RadixWs& w, u
 size_t sort_index_ws_bytes(int64_t n) { return carve_index(nullptr, n, nullptr); }
 
 hipError_t launch_sort_index(const void* index, bool wide, uint32_t count, uint32_t entries, uint32_t* keys, uint32_t* vals,
-                             const MatArg& table, int cols, void* ws, hipStream_t s) {
+                             uint8_t* marks, void* ws, hipStream_t s) {
+  uint4* m = reinterpret_cast<uint4*>(marks);
+  const int64_t m16 = (int64_t(entries) + 15) / 16;
   IndexWs w;
   carve_index(ws, count, &w);
   const int all = std::max(1, bits_for(entries)), passes = (all + kDigitBits - 1) / kDigitBits;
@@ -903,10 +894,10 @@ hipError_t launch_sort_index(const void* index, bool wide, uint32_t count, uint3
       in.keys = static_cast<const uint32_t*>(index);
       in.key_base = entries;
     }
-    const hipError_t e = pass > 0 ? index_pass<kFromKeys>(in, shift, bits, w.r, ko, vo, table, entries, cols, s)
-                         : wide   ? index_pass<kFromIndex64>(in, shift, bits, w.r, ko, vo, table, entries, cols, s)
-                                  : index_pass<kFromIndex>(in, shift, bits, w.r, ko, vo, table, entries, cols, s);
-    if (e != hipSuccess || count == 0) return e;   // without places there is only the table to clear
+    const hipError_t e = pass > 0 ? index_pass<kFromKeys>(in, shift, bits, w.r, ko, vo, m, m16, s)
+                         : wide   ? index_pass<kFromIndex64>(in, shift, bits, w.r, ko, vo, m, m16, s)
+                                  : index_pass<kFromIndex>(in, shift, bits, w.r, ko, vo, m, m16, s);
+    if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
