@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(MatArg table, const vo
     raw8_to_float(raw[u], table.type, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = at[u] < 0 ? 0.0f : v[i] * scale;
-    if (row < rows && c.skip < 8) store8(y, row, NARROW ? col : c.at, v, NARROW ? cols - col : 8);
+    if (row < rows && c.skip < 8) store8_once(y, row, NARROW ? col : c.at, v, NARROW ? cols - col : 8);
   }
 }
 
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) segment_sums_kernel(SegArgs a) {
       for (int u = 0; u < kFlight; ++u) {
         const int64_t p = p0 + u < last ? p0 + u : last - 1;
         keys[u] = a.key[p];
-        places[u] = keys[u] < a.entries ? a.order[p] : 0;   // what has no entry is not fetched for nothing
+        places[u] = a.order[p];
       }
     };
     fetch(first);
@@ -148,7 +148,8 @@ __global__ void __launch_bounds__(kThreads) segment_sums_kernel(SegArgs a) {
       uint32_t now[kFlight];
 #pragma unroll
       for (int u = 0; u < kFlight; ++u) {
-        raw[u] = load_share<NARROW>(a.src, places[u], s);
+        // the rows of no entry, all alike, are not fetched for nothing
+        raw[u] = load_share<NARROW>(a.src, keys[u] < a.entries ? places[u] : 0, s);
         now[u] = keys[u];
       }
       fetch(p0 + kFlight < last ? p0 + kFlight : p0);
