@@ -428,20 +428,15 @@ __device__ inline void store8(const MatArg& m, int64_t row, int col, const float
     store_bf16x8(m.p + (row * m.ld + col) * 2, v, n);
 }
 
-// The same for results that the kernel does not read again, past the caches where the columns are all
-// there: a table that it reads stays in them.
+// The same for results that the kernel does not read again: bfloat16, whose lanes' stores fill lines,
+// past the caches, so that a table that the kernel reads stays in them.
 __device__ inline void store8_once(const MatArg& m, int64_t row, int col, const float v[8], int n) {
   typedef u32x4 Any16 __attribute__((aligned(2)));
-  typedef f32x4 AnyFloats __attribute__((aligned(4)));
-  if (n < 8) {
+  if (n < 8 || m.type == GS_MAT_F32) {
     store8(m, row, col, v, n);
-  } else if (m.type == GS_MAT_F32) {
-    AnyFloats* p = reinterpret_cast<AnyFloats*>(reinterpret_cast<float*>(m.p) + row * m.ld + col);
-    __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, p);
-    __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, p + 1);
   } else {
-    Any16* p = reinterpret_cast<Any16*>(m.p + (row * m.ld + col) * 2);
-    __builtin_nontemporal_store(u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])}, p);
+    const u32x4 w{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+    __builtin_nontemporal_store(w, reinterpret_cast<Any16*>(m.p + (row * m.ld + col) * 2));
   }
 }
 
