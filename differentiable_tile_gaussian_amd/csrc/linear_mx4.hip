@@ -174,92 +174,119 @@ hipError_t go(const MatArg& x, const MatArg& w, const Epilogue& e, int64_t rows,
 
 // ------------------------------------------------------------- both operands in MX4, by tiles
 
-// Tiles of 128 columns by 32 QT rows, 64 x 16 QT for each of four waves, in steps of 128 k staged
-// through registers into two LDS buffers as in linear_tiles.hip.  LDS holds the operands as the
-// matrix cores take them: a fragment (16 rows, 128 k) is 1 KiB, 16 bytes a lane in the lanes'
-// order, which is also the order in which a wave loads it, so that writes and reads are
-// contiguous; and its scales, four bytes a row, of which a lane reads its own.  ALIGNED: rows
-// of scales are whole aligned words.
-constexpr int kTileThreads = 256;
+// Tiles of 128 columns by 32 QT rows, 64 x 16 QT for each of four waves, in steps of 128 k.  LDS holds
+// the operands as the matrix cores take them: a fragment (16 rows, 128 k) is 1 KiB, 16 bytes a lane
+// in the lanes' order, which is how a wave's load writes LDS without passing through registers.
+// kStages steps are in LDS or on their way, so that a step's loads have two others' time; one
+// barrier a step.  The scales of 16 steps are held beside them, four bytes a row and step, of which
+// a lane reads its own.
+constexpr int kTileThreads = 256, kStages = 4, kSegment = 16;
 
-template <int QT, bool ALIGNED>
-__global__ void __launch_bounds__(kTileThreads) tile_mx4_kernel(MatArg W, MatArg X, int np, int64_t nq, int nk, Epilogue e,
-                                                                 int ptiles, int tiles) {
-  constexpr int BP = 128, BQ = 32 * QT, kP = BP / 16, kQ = BQ / 16, kFrags = kP + kQ, kStep = kFrags * (1024 + 64), D = 2;
-  __shared__ __align__(16) uint8_t lds[2 * kStep];
+template <int QT>
+struct TileLds {
+  static constexpr int kP = 8, kQ = 2 * QT, kRows = 16 * (kP + kQ);
+  uint8_t stage[kStages][(kP + kQ) * 1024];
+  uint32_t scales[kSegment][kRows];
+};
+
+// A load of 16 bytes a lane from memory to LDS, at `to` (the same in all lanes) and 16 lane on.
+__device__ inline void load_to_lds(Buffer from, uint32_t off, uint8_t* to) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void*)to, 16, int(off), 0, 0, 0);
+}
+
+// Waits until at most N of the wave's loads are on their way and its LDS operations are done, and
+// for the other waves to have come as far.  (A fence would wait for all loads to LDS.)
+template <int N>
+__device__ inline void wait_loads_and_waves() {
+  static_assert(N < 64, "six bits");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x0070);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <int QT>
+__global__ void __launch_bounds__(kTileThreads, 2) tile_mx4_kernel(MatArg W, MatArg X, int np, int64_t nq, int nk, Epilogue e,
+                                                                    int ptiles, int tiles) {
+  using Lds = TileLds<QT>;
+  constexpr int BP = 128, BQ = 32 * QT, kP = Lds::kP, kQ = Lds::kQ, kLoads = (kP + kQ) / 4;
+  extern __shared__ __align__(16) uint8_t lds_bytes[];
+  Lds& lds = *reinterpret_cast<Lds*>(lds_bytes);
   const int tile = tile_of(blockIdx.x, tiles);
   if (tile >= tiles) return;
   const int p0 = tile % ptiles * BP;
   const int64_t q0 = int64_t(tile / ptiles) * BQ;
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, wp = wave % 2, wq = wave / 2, g = lane / 16, r = lane % 16;
+  const int lane = threadIdx.x % 64, g = lane / 16, r = lane % 16;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), wp = wave % 2, wq = wave / 2;
   const int blocks = (nk + 31) / 32, steps = (blocks + 3) / 4;
   const uint32_t wpitch = uint32_t(mx4_pitch(W)), xpitch = uint32_t(mx4_pitch(X));
-  const Buffer wb = buffer_at(W.p + int64_t(p0) * wpitch), ws = buffer_at(W.s + p0 * W.lds);
-  const Buffer xb = buffer_at(X.p + q0 * xpitch), xs = buffer_at(X.s + q0 * X.lds);
+  const Buffer wb = buffer_at(W.p + int64_t(p0) * wpitch), xb = buffer_at(X.p + q0 * xpitch);
   // a lane's four result tiles are 16 consecutive columns
   auto wrow = [](int f, int r) { return f / 4 * 64 + r / 4 * 16 + f % 4 * 4 + r % 4; };
-  uint32_t woff[kP / 4], xoff[kQ / 4];
+  uint32_t off[kLoads];
 #pragma unroll
-  for (int u = 0; u < kP / 4; ++u) {
-    const int row = wrow(wave + 4 * u, r);
-    woff[u] = p0 + row < np ? row * wpitch + g * 16 : kAbsent;
+  for (int u = 0; u < kLoads; ++u) {
+    const int f = wave + 4 * u, row = f < kP ? wrow(f, r) : (f - kP) * 16 + r;
+    const bool there = f < kP ? p0 + row < np : q0 + row < nq;
+    off[u] = there ? row * (f < kP ? wpitch : xpitch) + g * 16 : kAbsent;
   }
-#pragma unroll
-  for (int u = 0; u < kQ / 4; ++u) {
-    const int row = (wave + 4 * u) * 16 + r;
-    xoff[u] = q0 + row < nq ? row * xpitch + g * 16 : kAbsent;
-  }
-  // the thread's row of scales
-  const int sf = threadIdx.x / 16, srow = sf < kP ? wrow(sf, r) : (sf - kP) * 16 + r;
-  const bool is_w = sf < kP, has_scales = is_w ? p0 + srow < np : sf < kFrags && q0 + srow < nq;
-  const uint32_t soff = srow * uint32_t(is_w ? W.lds : X.lds);
-  u32x4 wr[D][kP / 4], xr[D][kQ / 4];
-  uint32_t sr[D];
-  auto fetch = [&](int d, int s) {
+  auto issue = [&](int s, int stage) {
     const bool in = s * 4 + g < blocks;
 #pragma unroll
-    for (int u = 0; u < kP / 4; ++u) wr[d][u] = buffer_load16(wb, in ? woff[u] + s * 64 : kAbsent);
+    for (int u = 0; u < kLoads; ++u)
+      load_to_lds(u < kP / 4 ? wb : xb, in ? off[u] + s * 64 : kAbsent, lds.stage[stage] + (wave + 4 * u) * 1024);
+  };
+  // The thread's row of scales, 16 bytes (four steps) at a time.  Absent ones are zero, and 2^-127 takes
+  // with it whatever LDS holds there.
+  const int sf = threadIdx.x / 16, srow = sf < kP ? wrow(sf, r) : (sf - kP) * 16 + r;
+  const bool has_scales = sf < kP ? p0 + srow < np : sf < kP + kQ && q0 + srow < nq;
+  const uint8_t* scale_row = sf < kP ? W.s + (has_scales ? p0 + srow : 0) * W.lds : X.s + (has_scales ? q0 + srow : 0) * X.lds;
+  u32x4 sr[kSegment / 4];
+  auto load_scales = [&](int s0) {
 #pragma unroll
-    for (int u = 0; u < kQ / 4; ++u) xr[d][u] = buffer_load16(xb, in ? xoff[u] + s * 64 : kAbsent);
-    // both matrices' descriptors are uniform, the choice is the wave's (a wave holds four fragments)
-    const Buffer from = __builtin_amdgcn_readfirstlane(is_w) ? ws : xs;
-    if constexpr (ALIGNED) {
-      sr[d] = buffer_load4(from, has_scales && s * 4 < blocks ? soff + s * 4 : kAbsent);
-    } else {
-      uint32_t b[4];
+    for (int j = 0; j < kSegment / 4; ++j) {
+      const int at = (s0 + j * 4) * 4, n = blocks - at;
+      sr[j] = u32x4{0, 0, 0, 0};
+      if (n >= 16) {
+        __builtin_memcpy(&sr[j], scale_row + at, 16);
+      } else if (n > 0) {
+        uint8_t byte[16];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) b[i] = buffer_load1(from, has_scales && s * 4 + i < blocks ? soff + s * 4 + i : kAbsent);
-      sr[d] = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
+        for (int i = 0; i < 16; ++i) byte[i] = scale_row[at + (i < n ? i : 0)];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sr[j][i / 4] |= (i < n ? uint32_t(byte[i]) : 0u) << (8 * (i % 4));
+      }
+      if (!has_scales) sr[j] = u32x4{0, 0, 0, 0};
     }
   };
-  auto stage = [&](int d, int s, uint8_t* at) {
-    if (nk % 32 && s == steps - 1) {   // x ends inside a block (what the weight holds behind it meets zeros)
+  auto put_scales = [&]() {
+    if (sf < kP + kQ) {
 #pragma unroll
-      for (int u = 0; u < kQ / 4; ++u) xr[d][u] = mx4_keep(xr[d][u], nk - (s * 4 + g) * 32);
+      for (int j = 0; j < kSegment; ++j) lds.scales[j][threadIdx.x] = sr[j / 4][j % 4];
     }
-#pragma unroll
-    for (int u = 0; u < kP / 4; ++u) *reinterpret_cast<u32x4*>(at + (wave + 4 * u) * 1024 + lane * 16) = wr[d][u];
-#pragma unroll
-    for (int u = 0; u < kQ / 4; ++u) *reinterpret_cast<u32x4*>(at + (kP + wave + 4 * u) * 1024 + lane * 16) = xr[d][u];
-    if (sf < kFrags) *reinterpret_cast<uint32_t*>(at + kFrags * 1024 + threadIdx.x * 4) = sr[d];
   };
   f32x4 acc[QT][4];
 #pragma unroll
   for (int i = 0; i < QT; ++i)
 #pragma unroll
     for (int t = 0; t < 4; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
-  fetch(0, 0);
-  stage(0, 0, lds);
+  load_scales(0);
 #pragma unroll
-  for (int d = 0; d < D; ++d) fetch(d, d + 1);
-  for (int s0 = 0; s0 < steps; s0 += D) {
+  for (int d = 0; d < kStages - 1; ++d) issue(d, d);
+  put_scales();
+  for (int s0 = 0; s0 < steps; s0 += kStages) {
+    if (s0 > 0 && s0 % kSegment == 0) {   // the next steps' scales, when all waves are done with the others
+      load_scales(s0);
+      step_barrier();
+      put_scales();
+    }
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
+    for (int d = 0; d < kStages; ++d) {
       const int s = s0 + d;
       if (s >= steps) break;
-      step_barrier();
-      const uint8_t* now = lds + (s & 1) * kStep;
-      const uint8_t *data = now + lane * 16, *scales = now + kFrags * 1024 + r * 4 + g;
+      wait_loads_and_waves<(kStages - 2) * kLoads>();
+      const uint8_t* data = lds.stage[d] + lane * 16;
+      const uint8_t* scales = reinterpret_cast<const uint8_t*>(lds.scales[s % kSegment]) + r * 4 + g;
       u32x4 wf[4], xf[QT];
       uint32_t wsc[4], xsc[QT];
 #pragma unroll
@@ -272,8 +299,11 @@ __global__ void __launch_bounds__(kTileThreads) tile_mx4_kernel(MatArg W, MatArg
         xf[i] = *reinterpret_cast<const u32x4*>(data + (kP + wq * QT + i) * 1024);
         xsc[i] = scales[(kP + wq * QT + i) * 64];
       }
-      stage(d, s + 1, lds + (~s & 1) * kStep);   // past the end: zeros, not read
-      fetch(d, s + 1 + D);
+      issue(s + kStages - 1, (d + kStages - 1) % kStages);   // always, so that the waits' count holds
+      if (nk % 32 && s == steps - 1) {   // x ends inside a block (what the weight holds behind it meets zeros)
+#pragma unroll
+        for (int i = 0; i < QT; ++i) xf[i] = mx4_keep(xf[i], nk - (s * 4 + g) * 32);
+      }
 #pragma unroll
       for (int i = 0; i < QT; ++i)
 #pragma unroll
@@ -292,12 +322,14 @@ __global__ void __launch_bounds__(kTileThreads) tile_mx4_kernel(MatArg W, MatArg
     for (int j = 0; j < 16; ++j) v[j] = acc[i][j / 4][j % 4] + bias[j];
     finish16<false, kNone, kAny>(e, row, col, v, row < nq ? n : 0);
   }
+  __builtin_amdgcn_s_waitcnt(0x0f70);   // a wave leaves no load to LDS behind
 }
 
 template <int QT>
 hipError_t go_tiles(const MatArg& x, const MatArg& w, const Epilogue& e, int64_t rows, int k, int n, hipStream_t s) {
-  auto words = [&](const MatArg& m) { return reinterpret_cast<uintptr_t>(m.s) % 4 == 0 && m.lds % 4 == 0; };
-  const auto kernel = (k + 31) / 32 % 4 == 0 && words(x) && words(w) ? &tile_mx4_kernel<QT, true> : &tile_mx4_kernel<QT, false>;
+  const auto kernel = &tile_mx4_kernel<QT>;
+  static LdsLimit limit;
+  if (const hipError_t no = limit.allow(kernel, sizeof(TileLds<QT>)); no != hipSuccess) return no;
   const int ptiles = int(div_up(n, 128));
   const int64_t most = (kMaxBlocks - 8) / ptiles * (32 * QT);   // rows of one launch
   for (int64_t first = 0; first < rows; first += most) {
@@ -306,7 +338,7 @@ hipError_t go_tiles(const MatArg& x, const MatArg& w, const Epilogue& e, int64_t
     part.r = rows_from(e.r, first);
     part.y = rows_from(e.y, first);
     const int tiles = int(ptiles * int64_t(div_up(count, 32 * QT)));
-    kernel<<<(tiles + 7) / 8 * 8, kTileThreads, 0, s>>>(w, mx4_rows_from(x, first), n, count, k, part, ptiles, tiles);
+    kernel<<<(tiles + 7) / 8 * 8, kTileThreads, sizeof(TileLds<QT>), s>>>(w, mx4_rows_from(x, first), n, count, k, part, ptiles, tiles);
   }
   return hipGetLastError();
 }

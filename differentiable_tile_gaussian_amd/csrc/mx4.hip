@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kThreads) mx4_unpack_kernel(MatArg q, MatArg x
     const int64_t row = row0 + int64_t(u) * per;
     float v[8];
     mx4_decode8(w[u], mx8_scale(byte[u]), v);
-    if (row < rows && col < cols) store8(x, row, col, v, NARROW || cols - col < 8 ? cols - col : 8);
+    if (row < rows && col < cols) store8_once(x, row, col, v, NARROW || cols - col < 8 ? cols - col : 8);
   }
 }
 
