@@ -102,6 +102,17 @@ __device__ inline void activate16(float v[16]) {
   for (int i = 0; i < 16; ++i) v[i] = activate(v[i], ACT);
 }
 
+// The bias of 16 columns, of which the first n exist (zeros behind them; nullable): one wait for all.
+__device__ inline void load_bias16(const float* bias, int col, int n, float (&v)[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] = 0.0f;
+  if (!bias || n <= 0) return;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] = bias[col + (j < n ? j : 0)];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] = j < n ? v[j] : 0.0f;
+}
+
 // v: x W^T (with the bias) for 16 columns of a row.  Z, Y: the types of z and y, or kAny,
 // or kNone for z.
 template <bool WHOLE, int Z, int Y>

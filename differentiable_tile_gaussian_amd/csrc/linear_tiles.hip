@@ -215,8 +215,7 @@ __global__ void __launch_bounds__(kThreads) tile_nt_kernel(MatArg P, MatArg Q, i
   }
   const int col = p0 + wp * 64 + g * 16, n = np - col < 16 ? np - col : 16;
   float bias[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) bias[i] = e.bias && i < n ? e.bias[col + i] : 0.0f;
+  load_bias16(e.bias, col, n, bias);
 #pragma unroll
   for (int i = 0; i < QT; ++i) {
     const int64_t r = q0 + (wq * QT + i) * 16 + r16;
