@@ -176,39 +176,42 @@ hipError_t go(const MatArg& x, const MatArg& w, const Epilogue& e, int64_t rows,
 
 // ------------------------------------------------------------- by tiles, x in MX4 or MX8
 
-// Tiles of 128 columns by 32 QT rows, 64 x 16 QT for each of four waves, in steps of 128 k.  LDS holds
-// the operands as they are in memory, in the order in which lanes take them: a fragment (16 rows,
-// 128 k) of MX4 is 1 KiB, 16 bytes a lane, one of MX8 two such halves, which is also how a wave's load
-// writes LDS without passing through registers.  x in MX8 and its weight are decoded to bfloat16
-// behind LDS, which moves a quarter to a half of the bytes that way.
+// Tiles of 128 columns by 32 QT rows, 64 x 16 QT for each of four waves, in steps of 256 k (x in MX4)
+// or 128 k (MX8): 128 bytes of a row, a line.  LDS holds the operands as they are in memory: a wave's
+// load takes a line of eight rows and writes 1 KiB of LDS without passing through registers, the 16-byte
+// pieces of a row permuted by its number so that a fragment's 16 rows are read from different
+// banks.  (A load of 64 bytes of sixteen rows takes twice the time, 40 cycles of the address unit.)  x
+// in MX8 and its weight are decoded to bfloat16 behind LDS, which moves a quarter to a half of
+// the bytes that way.
 //
 // A block takes one tile after another, and its loads run ahead of its products by kStages - 1 steps, into
-// the next tile too: what a tile costs beside its products is latency (with a block to a tile, 8
-// steps of which the loads and products take 7 us take 25).  One barrier a step.
+// the next tile too: what a tile costs beside its products is latency.  One barrier a step.
 //
-// Scales are four bytes a row and step, of which a lane reads its own.  ALIGNED: they are whole
-// aligned words and come with their step; otherwise through registers, kSegment steps at a time.
+// Scales are four bytes a row and 128 k, of which a lane reads its own; they come through registers (any
+// alignment), kParts of them at a time, into one of two places.
 constexpr int kTileThreads = 256;
 
-template <int XT, int QT_, bool ALIGNED_>
+template <int XT, int QT_>
 struct Tile {
-  static constexpr bool kX4 = XT == GS_MAT_MX4, ALIGNED = ALIGNED_;
-  static constexpr int QT = QT_, BP = 128, BQ = 32 * QT, kP = BP / 16, kQ = BQ / 16, kHalves = kX4 ? 1 : 2;
-  static constexpr int kUnits = kP + kQ * kHalves, kLoads = kUnits / 4, kRows = 256;
-  static constexpr int kStages = kX4 ? 4 : 3, kSegment = 4;
+  static constexpr bool kX4 = XT == GS_MAT_MX4;
+  static constexpr int QT = QT_, BP = 128, BQ = 32 * QT, kP = BP / 16, kQ = BQ / 16;
+  static constexpr int kSub = kX4 ? 2 : 1, kHalves = kX4 ? 1 : 2;   // 128 k parts of a step; 16-byte parts of a lane's 32 k
+  static constexpr int kStages = kX4 ? 2 : 3, kParts = kX4 ? 4 : 2;
+  static constexpr int kW = kP * kSub, kX = kQ * 2;   // KiB, and loads, of a step
+  static constexpr int kLoads = (kW + kX) / 4;
   struct Lds {
-    uint8_t stage[kStages][kUnits * 1024];
-    uint32_t scales[ALIGNED ? kStages : 2 * kSegment][kRows];   // 16 (kP + kQ) rows are used
+    uint8_t stage[kStages][(kW + kX) * 1024];
+    uint8_t scales[2][256][4 * kParts];   // 16 (kP + kQ) rows are used
     float bias[kStages][BP];   // of as many tiles as loads run ahead, where a tile is one step
   };
 };
 
-// A load of 16 bytes a lane from memory to LDS, at `to` (the same in all lanes) and 16 lane on.
-__device__ inline void load_to_lds(Buffer from, uint32_t off, uint8_t* to) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void*)to, 16, int(off), 0, 0, 0);
+// Loads to LDS of 16 or 4 bytes a lane, from off + more on, to `to` (the same in all lanes) and on.
+__device__ __forceinline__ void load16_to_lds(Buffer from, uint32_t off, int more, void* to) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void*)to, 16, int(off), more, 0, 0);
 }
-__device__ inline void load_words_to_lds(Buffer from, uint32_t off, void* to) {   // 4 bytes a lane
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void*)to, 4, int(off), 0, 0, 0);
+__device__ __forceinline__ void load4_to_lds(Buffer from, uint32_t off, int more, void* to) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void*)to, 4, int(off), more, 0, 0);
 }
 
 // Waits until at most N of the wave's loads are on their way and its LDS operations are done, and
@@ -226,17 +229,17 @@ __device__ inline void wait_loads_and_waves() {
 // columns.
 __device__ inline int weight_row(int f, int r) { return f / 4 * 64 + r / 4 * 16 + f % 4 * 4 + r % 4; }
 
-template <class T, int XT>
+template <class T>
 __global__ void __launch_bounds__(kTileThreads, 2) tile_mx4_kernel(MatArg W, MatArg X, int np, int64_t nq, int nk, Epilogue e,
                                                                     int ptiles, int tiles) {
-  constexpr int QT = T::QT, kP = T::kP, kQ = T::kQ, kH = T::kHalves, kLoads = T::kLoads, kStages = T::kStages, kSegment = T::kSegment;
-  constexpr bool kX4 = T::kX4, ALIGNED = T::ALIGNED;
-  constexpr int kAhead = (kStages - 2) * (kLoads + ALIGNED);   // loads on their way behind those of a step
+  constexpr int QT = T::QT, kP = T::kP, kQ = T::kQ, kH = T::kHalves, kSub = T::kSub, kStages = T::kStages, kParts = T::kParts;
+  constexpr bool kX4 = T::kX4;
+  constexpr int kAhead = (kStages - 2) * T::kLoads;   // loads on their way behind those of a step
   extern __shared__ __align__(16) uint8_t lds_bytes[];
   typename T::Lds& lds = *reinterpret_cast<typename T::Lds*>(lds_bytes);
   const int lane = threadIdx.x % 64, g = lane / 16, r = lane % 16;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), wp = wave % 2, wq = wave / 2;
-  const int blocks = (nk + 31) / 32, steps = (blocks + 3) / 4;
+  const int blocks = (nk + 31) / 32, parts = (blocks + 3) / 4, steps = (parts + kSub - 1) / kSub;
   const uint32_t wpitch = uint32_t(mx4_pitch(W)), xpitch = kX4 ? uint32_t(mx4_pitch(X)) : uint32_t(X.ld);
   // the block's tiles, by turns: tile_of gives an XCD neighbouring ones
   const int turns = (tiles + 7) / 8 * 8;
@@ -245,21 +248,13 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_mx4_kernel(MatArg W, Mat
     return turn;
   };
 
-  // ---- loads to LDS: unit wave + 4 u of step `step` of the tile of turn `ahead`, and the thread's word of
-  // scales (a wave's are all of W or all of x); with a tile's first step its bias
-  const int sf = threadIdx.x / 16, srow = sf < kP ? weight_row(sf, r) : (sf - kP) * 16 + r;
-  const bool of_w = wave < kP / 4;
+  // ---- loads to LDS, for step `step` of the tile of turn `ahead`: of a wave's kW / 4 and kX / 4 KiB; with a
+  // tile's first step its bias.  A line's lanes: row lane / 8 of eight, and of it piece lane % 8 ^ row.
+  const int row8 = lane / 8, piece = (lane % 8) ^ row8;
   int ahead = valid_from(blockIdx.x), step = 0, to = 0, bias_to = 0;
-  Buffer wb = buffer_at(nullptr), xb = buffer_at(nullptr), sb = buffer_at(nullptr);
-  uint32_t off[kLoads], soff = kAbsent, boff = kAbsent;
+  Buffer wb = buffer_at(nullptr), xb = buffer_at(nullptr);
+  uint32_t woff[T::kW / 4], xoff[T::kX / 4], boff = kAbsent;
   const Buffer bb = buffer_at(e.bias);
-  int most[kLoads];    // steps in which the lane's 16 bytes exist
-#pragma unroll
-  for (int u = 0; u < kLoads; ++u) {
-    const bool is_w = u < kP / 4;
-    const int f = wave + 4 * u, k0 = is_w ? g * 32 : g * 32 + (f - kP) % kH * 16, n = is_w || kX4 ? blocks * 32 : nk;
-    most[u] = (n - k0 + 127) / 128;
-  }
   auto point = [&]() {
     const bool there = ahead < turns;
     const int tile = there ? tile_of(ahead, tiles) : 0, p0 = tile % ptiles * T::BP;
@@ -267,35 +262,35 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_mx4_kernel(MatArg W, Mat
     wb = buffer_at(W.p + int64_t(p0) * wpitch);
     xb = buffer_at(X.p + q0 * xpitch);
 #pragma unroll
-    for (int u = 0; u < kLoads; ++u) {
-      const int f = wave + 4 * u;
-      if (u < kP / 4) {
-        const int row = weight_row(f, r);
-        off[u] = there && p0 + row < np ? row * wpitch + g * 16 : kAbsent;
-      } else {
-        const int row = (f - kP) / kH * 16 + r;
-        off[u] = there && q0 + row < nq ? row * xpitch + g * 16 * kH + (f - kP) % kH * 16 : kAbsent;
-      }
+    for (int j = 0; j < T::kW / 4; ++j) {
+      const int unit = wave * (T::kW / 4) + j;
+      const int row = kSub == 2 ? weight_row(unit / 2, unit % 2 * 8 + row8) : weight_row(unit, r);
+      woff[j] = there && p0 + row < np ? row * wpitch + (kSub == 2 ? piece : g) * 16 : kAbsent;
     }
-    if constexpr (ALIGNED) {
-      sb = buffer_at(of_w ? W.s + p0 * W.lds : X.s + q0 * X.lds);
-      const bool row = of_w ? p0 + srow < np : sf < kP + kQ && q0 + srow < nq;
-      soff = there && row ? srow * uint32_t(of_w ? W.lds : X.lds) : kAbsent;
+#pragma unroll
+    for (int j = 0; j < T::kX / 4; ++j) {
+      const int row = (wave * (T::kX / 4) + j) * 8 + row8;
+      xoff[j] = there && q0 + row < nq ? row * xpitch + piece * 16 : kAbsent;
     }
     const int c = p0 + int(threadIdx.x) % T::BP;
     boff = there && e.bias && c < np ? c * 4 : kAbsent;
   };
-  auto issue = [&]() {   // always, so that the waits' count holds
-#pragma unroll
-    for (int u = 0; u < kLoads; ++u) {
-      const uint32_t at = off[u] + step * (u < kP / 4 ? 64 : 64 * kH);
-      load_to_lds(u < kP / 4 ? wb : xb, step < most[u] ? at : kAbsent, lds.stage[to] + (wave + 4 * u) * 1024);
-    }
-    if constexpr (ALIGNED) load_words_to_lds(sb, step * 4 < blocks ? soff + step * 4 : kAbsent, lds.scales[to] + wave * 64);
+  // The same number of loads every time, so that the waits' count holds.
+  auto issue = [&]() {
     if (step == 0) {   // (one more on its way only makes the waits longer; the upper waves write the same)
-      load_words_to_lds(bb, boff, lds.bias[bias_to] + wave % 2 * 64);
+      load4_to_lds(bb, boff, 0, lds.bias[bias_to] + wave % 2 * 64);
       bias_to = bias_to + 1 < kStages ? bias_to + 1 : 0;
     }
+    uint8_t *wto = lds.stage[to] + wave * (T::kW / 4) * 1024, *xto = lds.stage[to] + (T::kW + wave * (T::kX / 4)) * 1024;
+    bool w_in = true, x_in = true;
+    if ((step + 1) * (128 * kSub) > nk) {   // the last step: pieces that exist
+      w_in = (step * kSub) * 4 + (kSub == 2 ? piece : g) < blocks;
+      x_in = kX4 ? w_in : step * 128 + piece * 16 < nk;
+    }
+#pragma unroll
+    for (int j = 0; j < T::kW / 4; ++j) load16_to_lds(wb, w_in ? woff[j] : kAbsent, step * 64 * kSub, wto + j * 1024);
+#pragma unroll
+    for (int j = 0; j < T::kX / 4; ++j) load16_to_lds(xb, x_in ? xoff[j] : kAbsent, step * 128, xto + j * 1024);
     to = to + 1 < kStages ? to + 1 : 0;
     if (++step == steps) {
       step = 0;
@@ -304,36 +299,33 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_mx4_kernel(MatArg W, Mat
     }
   };
 
-  // ---- scales of any alignment: the thread's row, 16 bytes (four steps) at a time.  Absent ones are zero.
-  u32x4 sr[kSegment / 4];
-  auto load_scales = [&](int turn, int s0) {
-    if (ALIGNED || turn >= turns) return;
+  // ---- scales: the thread's row, kParts words at a time.  Absent ones are zero.
+  const int sf = threadIdx.x / 16, srow = sf < kP ? weight_row(sf, r) : (sf - kP) * 16 + r;
+  uint32_t sr[kParts];
+  auto load_scales = [&](int turn, int part) {
+    if (turn >= turns) return;
     const int tile = tile_of(turn, tiles), p0 = tile % ptiles * T::BP;
     const int64_t q0 = int64_t(tile / ptiles) * T::BQ;
     const bool there = sf < kP ? p0 + srow < np : sf < kP + kQ && q0 + srow < nq;
     const uint8_t* row = sf < kP ? W.s + (there ? p0 + srow : 0) * W.lds : X.s + (there ? q0 + srow : 0) * X.lds;
+    const int at = part * 4, n = blocks - at;
+    if (n >= 4 * kParts) {
+      __builtin_memcpy(sr, row + at, 4 * kParts);
+    } else {
+      uint8_t byte[4 * kParts];
 #pragma unroll
-    for (int j = 0; j < kSegment / 4; ++j) {
-      const int at = (s0 + j * 4) * 4, n = blocks - at;
-      sr[j] = u32x4{0, 0, 0, 0};
-      if (n >= 16) {
-        __builtin_memcpy(&sr[j], row + at, 16);
-      } else if (n > 0) {
-        uint8_t byte[16];
+      for (int i = 0; i < 4 * kParts; ++i) byte[i] = row[at + (i < n ? i : 0)];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) byte[i] = row[at + (i < n ? i : 0)];
+      for (int j = 0; j < kParts; ++j) {
+        sr[j] = 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sr[j][i / 4] |= (i < n ? uint32_t(byte[i]) : 0u) << (8 * (i % 4));
+        for (int i = 0; i < 4; ++i) sr[j] |= (4 * j + i < n ? uint32_t(byte[4 * j + i]) : 0u) << (8 * i);
       }
-      if (!there) sr[j] = u32x4{0, 0, 0, 0};
     }
-  };
-  auto put_scales = [&](int half) {
-    if constexpr (!ALIGNED) {
 #pragma unroll
-      for (int j = 0; j < kSegment; ++j) lds.scales[half * kSegment + j][threadIdx.x] = sr[j / 4][j % 4];
-    }
+    for (int j = 0; j < kParts; ++j) sr[j] = there ? sr[j] : 0;
   };
+  auto put_scales = [&](int half) { __builtin_memcpy(__builtin_assume_aligned(lds.scales[half][threadIdx.x], 4 * kParts), sr, 4 * kParts); };
 
   int turn = ahead, now = 0, half = 0, bias_at = 0;
   bool stores = false;   // the epilogue in front of this step has made all its stores
@@ -351,13 +343,13 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_mx4_kernel(MatArg W, Mat
     for (int i = 0; i < QT; ++i)
 #pragma unroll
       for (int t = 0; t < 4; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
-    const int segment = ALIGNED ? steps : kSegment;
-    for (int s0 = 0; s0 < steps; s0 += segment) {
-      if (s0 + segment < steps)
-        load_scales(turn, s0 + segment);
+    constexpr int kSegment = kParts / kSub;   // steps
+    for (int s0 = 0; s0 < steps; s0 += kSegment) {
+      if (s0 + kSegment < steps)
+        load_scales(turn, (s0 + kSegment) * kSub);
       else
         load_scales(next, 0);
-      const int last = s0 + segment < steps ? s0 + segment : steps;
+      const int last = s0 + kSegment < steps ? s0 + kSegment : steps;
       for (int s = s0; s < last; ++s) {
         // the stores are younger than the loads that this step needs
         if (!stores)
@@ -367,57 +359,71 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_mx4_kernel(MatArg W, Mat
         else
           wait_loads_and_waves<kAhead + 2 * QT>();
         stores = false;
-        const uint8_t* data = lds.stage[now] + lane * 16;
-        const uint8_t* scales = reinterpret_cast<const uint8_t*>(lds.scales[ALIGNED ? now : half * kSegment + s - s0]) + r * 4 + g;
-        u32x4 wf[4], xf[QT][kH];
-        uint32_t wsc[4], xsc[QT];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          wf[t] = *reinterpret_cast<const u32x4*>(data + (wp * 4 + t) * 1024);
-          wsc[t] = scales[(wp * 4 + t) * 64];
-        }
-#pragma unroll
-        for (int i = 0; i < QT; ++i) {
-#pragma unroll
-          for (int h = 0; h < kH; ++h) xf[i][h] = *reinterpret_cast<const u32x4*>(data + (kP + (wq * QT + i) * kH + h) * 1024);
-          xsc[i] = scales[(kP + wq * QT + i) * 64];
-        }
         issue();
+        const uint8_t* wdata = lds.stage[now] + wp * (4 * kSub * 1024);
+        const uint8_t* xdata = lds.stage[now] + (T::kW + wq * (QT * 2)) * 1024 + r * 128;
+        const uint8_t* wscale = lds.scales[half][wp * 64 + r] + (s - s0) * kSub * 4 + g;
+        const uint8_t* xscale = lds.scales[half][kP * 16 + wq * (QT * 16) + r] + (s - s0) * kSub * 4 + g;
         now = now + 1 < kStages ? now + 1 : 0;
-        if (nk % 128 && s == steps - 1) {   // x ends inside the step (what W holds behind it meets zeros)
-          const int left = nk - (s * 4 + g) * 32;
+        u32x4 wf[kSub][4], xf[kSub][QT][kH];
+        uint32_t wsc[kSub][4], xsc[kSub][QT];
+#pragma unroll
+        for (int sub = 0; sub < kSub; ++sub) {
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const int at = kSub == 2 ? r * 128 + ((sub * 4 + g) ^ (r & 7)) * 16 : lane * 16;
+            wf[sub][t] = *reinterpret_cast<const u32x4*>(wdata + t * (kSub * 1024) + at);
+            wsc[sub][t] = wscale[sub * 4 + t * (64 * kParts)];
+          }
 #pragma unroll
           for (int i = 0; i < QT; ++i) {
-            if constexpr (kX4) {
-              xf[i][0] = mx4_keep(xf[i][0], left);
-            } else {
 #pragma unroll
-              for (int h = 0; h < kH; ++h) xf[i][h] = left > h * 16 ? xf[i][h] : u32x4{0, 0, 0, 0};
+            for (int h = 0; h < kH; ++h)
+              xf[sub][i][h] = *reinterpret_cast<const u32x4*>(xdata + i * 2048 + ((kX4 ? sub * 4 + g : g * 2 + h) ^ (r & 7)) * 16);
+            xsc[sub][i] = xscale[sub * 4 + i * (64 * kParts)];
+          }
+        }
+        if (nk % 128 && s == steps - 1) {   // x ends inside (what W holds behind its end meets zeros)
+#pragma unroll
+          for (int sub = 0; sub < kSub; ++sub) {
+            const int left = nk - ((s * kSub + sub) * 4 + g) * 32;
+#pragma unroll
+            for (int i = 0; i < QT; ++i) {
+              if constexpr (kX4) {
+                xf[sub][i][0] = mx4_keep(xf[sub][i][0], left);
+              } else {
+#pragma unroll
+                for (int h = 0; h < kH; ++h) xf[sub][i][h] = left > h * 16 ? xf[sub][i][h] : u32x4{0, 0, 0, 0};
+              }
             }
           }
         }
-        if constexpr (kX4) {
 #pragma unroll
-          for (int i = 0; i < QT; ++i)
-#pragma unroll
-            for (int t = 0; t < 4; ++t) acc[i][t] = product4(wf[t], wsc[t], xf[i][0], xsc[i], acc[i][t]);
-        } else {
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            bf16x8 wo[4], xo[QT];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) wo[t] = mx4_to_bf16x8(wf[t][h], mx8_scale(wsc[t]));
-#pragma unroll
-            for (int i = 0; i < QT; ++i) {
-              const float sc = mx8_scale(xsc[i]);
-              const u32x4 raw = xf[i][h / 2];
-              const u32x2 a = mx8_to_bf16x4(raw[h % 2 * 2], sc), b = mx8_to_bf16x4(raw[h % 2 * 2 + 1], sc);
-              xo[i] = __builtin_bit_cast(bf16x8, u32x4{a[0], a[1], b[0], b[1]});
-            }
+        for (int sub = 0; sub < kSub; ++sub) {
+          if (sub > 0 && s * kSub + sub >= parts) break;
+          if constexpr (kX4) {
 #pragma unroll
             for (int i = 0; i < QT; ++i)
 #pragma unroll
-              for (int t = 0; t < 4; ++t) acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wo[t], xo[i], acc[i][t], 0, 0, 0);
+              for (int t = 0; t < 4; ++t) acc[i][t] = product4(wf[sub][t], wsc[sub][t], xf[sub][i][0], xsc[sub][i], acc[i][t]);
+          } else {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              bf16x8 wo[4], xo[QT];
+#pragma unroll
+              for (int t = 0; t < 4; ++t) wo[t] = mx4_to_bf16x8(wf[sub][t][h], mx8_scale(wsc[sub][t]));
+#pragma unroll
+              for (int i = 0; i < QT; ++i) {
+                const float sc = mx8_scale(xsc[sub][i]);
+                const u32x4 raw = xf[sub][i][h / 2];
+                const u32x2 a = mx8_to_bf16x4(raw[h % 2 * 2], sc), b = mx8_to_bf16x4(raw[h % 2 * 2 + 1], sc);
+                xo[i] = __builtin_bit_cast(bf16x8, u32x4{a[0], a[1], b[0], b[1]});
+              }
+#pragma unroll
+              for (int i = 0; i < QT; ++i)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wo[t], xo[i], acc[i][t], 0, 0, 0);
+            }
           }
         }
       }
@@ -449,10 +455,10 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_mx4_kernel(MatArg W, Mat
   __builtin_amdgcn_s_waitcnt(0x0f70);   // a wave leaves no load to LDS behind
 }
 
-template <int XT, int QT, bool ALIGNED>
+template <int XT, int QT>
 hipError_t go_tiles(const MatArg& x, const MatArg& w, const Epilogue& e, int64_t rows, int k, int n, hipStream_t s) {
-  using T = Tile<XT, QT, ALIGNED>;
-  const auto kernel = &tile_mx4_kernel<T, XT>;
+  using T = Tile<XT, QT>;
+  const auto kernel = &tile_mx4_kernel<T>;
   static LdsLimit limit;
   if (const hipError_t no = limit.allow(kernel, sizeof(typename T::Lds)); no != hipSuccess) return no;
   const int ptiles = int(div_up(n, 128));
@@ -471,11 +477,8 @@ hipError_t go_tiles(const MatArg& x, const MatArg& w, const Epilogue& e, int64_t
 
 template <int XT>
 hipError_t by_tiles(const MatArg& x, const MatArg& w, const Epilogue& e, int64_t rows, int k, int n, hipStream_t s) {
-  auto words = [](const MatArg& m) { return reinterpret_cast<uintptr_t>(m.s) % 4 == 0 && m.lds % 4 == 0; };
-  const bool aligned = (k + 31) / 32 % 4 == 0 && words(x) && words(w);
-  const bool few = int64_t(div_up(n, 128)) * div_up(rows, 128) <= 256;
-  if (few) return aligned ? go_tiles<XT, 2, true>(x, w, e, rows, k, n, s) : go_tiles<XT, 2, false>(x, w, e, rows, k, n, s);
-  return aligned ? go_tiles<XT, 4, true>(x, w, e, rows, k, n, s) : go_tiles<XT, 4, false>(x, w, e, rows, k, n, s);
+  return int64_t(div_up(n, 128)) * div_up(rows, 128) <= 256 ? go_tiles<XT, 2>(x, w, e, rows, k, n, s)
+                                                           : go_tiles<XT, 4>(x, w, e, rows, k, n, s);
 }
 
 }  // namespace
