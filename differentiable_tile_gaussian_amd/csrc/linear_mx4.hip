@@ -7,6 +7,8 @@
 // are exact in bfloat16 and take four 16x16x32 products.  (The matrix cores' product of 8-bit
 // with 4-bit elements is twice as fast, but it drops the low bits of what it adds: 4.5e-5 of the
 // result, which an MX8 or float32 y would show.)
+#include <type_traits>
+
 #include "linear.h"
 #include "mx4.h"
 #include "profile.h"
@@ -75,13 +77,17 @@ struct BlockX {
   }
 };
 
-// Any size and type.  A block of four waves takes 64 columns by 16 QT rows, the waves sharing
-// the contraction; their sums are joined through LDS in order.
-constexpr int kWaves = 4;
+// ------------------------------------------------------------- few rows, and any size and type
+
+// A block takes 64 columns by 16 QT rows and its waves share the contraction, each loading its
+// operands into registers one step ahead; the waves' sums are joined through LDS in order.  Bounded by
+// latency: with few rows there is little to read but the weight.
+constexpr int waves_of(int qt) { return qt == 4 ? 4 : 8; }   // 64 KiB of sums at most
 
 template <int XT, int QT, bool NARROW>
-__global__ void __launch_bounds__(kWaves * 64) linear_mx4_kernel(MatArg W, MatArg X, int np, int64_t nq, int nk, Epilogue e) {
+__global__ void __launch_bounds__(waves_of(QT) * 64) linear_mx4_kernel(MatArg W, MatArg X, int np, int64_t nq, int nk, Epilogue e) {
   constexpr bool kX4 = XT == GS_MAT_MX4;
+  constexpr int kWaves = waves_of(QT);
   __shared__ f32x4 sums[kWaves * QT * 4 * 64];   // [wave][QT][tile][lane]
   const int lane = threadIdx.x % 64, g = lane / 16, r = lane % 16;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -90,33 +96,50 @@ __global__ void __launch_bounds__(kWaves * 64) linear_mx4_kernel(MatArg W, MatAr
   const uint32_t wp = uint32_t(mx4_pitch(W)), xp = kX4 ? uint32_t(mx4_pitch(X)) : 0u;
   const Buffer wb = buffer_at(W.p + int64_t(p0) * wp), ws = buffer_at(W.s + int64_t(p0) * W.lds);
   const Buffer xb = buffer_at(kX4 ? X.p + q0 * xp : nullptr), xs = buffer_at(kX4 ? X.s + q0 * X.lds : nullptr);
-  f32x4 acc[QT][4];
-#pragma unroll
-  for (int i = 0; i < QT; ++i)
-#pragma unroll
-    for (int t = 0; t < 4; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
   const int steps = (nk + 127) / 128;
-  for (int s = wave; s < steps; s += kWaves) {
+  Block4 w[4];
+  std::conditional_t<kX4, Block4, BlockX<XT, NARROW>> x[QT];
+  auto fetch = [&](int s) {   // past the end: the weight is absent
     const int block = s * 4 + g, left = nk - block * 32;
-    Block4 w[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const int row = r / 4 * 16 + t * 4 + r % 4;   // a lane's tiles: 16 consecutive columns
       w[t].load(wb, ws, row, wp, uint32_t(W.lds), p0 + row < np, block, left);
     }
-    if constexpr (kX4) {
-      Block4 x[QT];
 #pragma unroll
-      for (int i = 0; i < QT; ++i) {
-        x[i].load(xb, xs, i * 16 + r, xp, uint32_t(X.lds), q0 + i * 16 + r < nq, block, left);
-        x[i].keep(left);
-      }
+    for (int i = 0; i < QT; ++i) {
+      const int64_t row = q0 + i * 16 + r;
+      if constexpr (kX4)
+        x[i].load(xb, xs, i * 16 + r, xp, uint32_t(X.lds), row < nq, block, left);
+      else
+        x[i].load(X, row < nq ? row : nq - 1, block * 32, nk, row < nq);
+    }
+  };
+  fetch(wave);
+  float bias[16];
+  const int col = p0 + g * 16, n = np - col < 16 ? np - col : 16;
+  load_bias16(e.bias, col, wave < QT ? n : 0, bias);
+  f32x4 acc[QT][4];
+#pragma unroll
+  for (int i = 0; i < QT; ++i)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
+  for (int s = wave; s < steps; s += kWaves) {
+    const int left = nk - (s * 4 + g) * 32;
+    if constexpr (kX4) {
+      u32x4 wq[4], xq[QT];
+      uint32_t wsc[4], xsc[QT];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) wq[t] = w[t].q, wsc[t] = w[t].scale;
+#pragma unroll
+      for (int i = 0; i < QT; ++i) xq[i] = mx4_keep(x[i].q, left), xsc[i] = x[i].scale;
+      fetch(s + kWaves);
 #pragma unroll
       for (int i = 0; i < QT; ++i)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) acc[i][t] = product4(w[t].q, w[t].scale, x[i].q, x[i].scale, acc[i][t]);
+        for (int t = 0; t < 4; ++t) acc[i][t] = product4(wq[t], wsc[t], xq[i], xsc[i], acc[i][t]);
     } else {
-      bf16x8 wo[4][4];
+      bf16x8 wo[4][4], xo[QT][4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         w[t].keep(left);
@@ -124,17 +147,16 @@ __global__ void __launch_bounds__(kWaves * 64) linear_mx4_kernel(MatArg W, MatAr
       }
 #pragma unroll
       for (int i = 0; i < QT; ++i) {
-        const int64_t row = q0 + i * 16 + r;
-        BlockX<XT, NARROW> x;
-        x.load(X, row < nq ? row : nq - 1, block * 32, nk, row < nq);
-        x.settle();
-        bf16x8 xo[4];
-        x.operands(xo);
+        x[i].settle();
+        x[i].operands(xo[i]);
+      }
+      fetch(s + kWaves);
+#pragma unroll
+      for (int i = 0; i < QT; ++i)
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-          for (int h = 0; h < 4; ++h) acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wo[t][h], xo[h], acc[i][t], 0, 0, 0);
-      }
+          for (int h = 0; h < 4; ++h) acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wo[t][h], xo[i][h], acc[i][t], 0, 0, 0);
     }
   }
 #pragma unroll
@@ -144,34 +166,39 @@ __global__ void __launch_bounds__(kWaves * 64) linear_mx4_kernel(MatArg W, MatAr
   __syncthreads();
   if (wave >= QT) return;
   const int64_t row = q0 + wave * 16 + r;
-  const int col = p0 + g * 16, n = np - col < 16 ? np - col : 16;
   float v[16];
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     f32x4 total = sums[(wave * 4 + t) * 64 + lane];
+#pragma unroll
     for (int o = 1; o < kWaves; ++o) total += sums[((o * QT + wave) * 4 + t) * 64 + lane];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[4 * t + i] = total[i];
+    for (int i = 0; i < 4; ++i) v[4 * t + i] = total[i] + bias[4 * t + i];
   }
-  float bias[16];
-  load_bias16(e.bias, col, n, bias);
-#pragma unroll
-  for (int j = 0; j < 16; ++j) v[j] += bias[j];
   finish16<false, kNone, kAny>(e, row, col, v, row < nq ? n : 0);
 }
 
-template <int XT, bool NARROW>
+template <int XT, int QT, bool NARROW>
 hipError_t go(const MatArg& x, const MatArg& w, const Epilogue& e, int64_t rows, int k, int n, hipStream_t s) {
-  const int64_t most = kMaxBlocks * 64;   // rows of one launch
+  const int64_t most = kMaxBlocks / 2 * (16 * QT);   // rows of one launch
   for (int64_t first = 0; first < rows; first += most) {
     const int64_t count = rows - first < most ? rows - first : most;
     Epilogue part = e;
     part.r = rows_from(e.r, first);
     part.y = rows_from(e.y, first);
     const MatArg xp = XT == GS_MAT_MX4 ? mx4_rows_from(x, first) : rows_from(x, first);
-    linear_mx4_kernel<XT, 4, NARROW><<<dim3(div_up(count, 64), div_up(n, 64)), kWaves * 64, 0, s>>>(w, xp, n, count, k, part);
+    linear_mx4_kernel<XT, QT, NARROW>
+        <<<dim3(div_up(count, 16 * QT), div_up(n, 64)), waves_of(QT) * 64, 0, s>>>(w, xp, n, count, k, part);
   }
   return hipGetLastError();
+}
+
+// Rows of a block: 16 where there are no more, else the more the fewer blocks are left idle.
+template <int XT, bool NARROW>
+hipError_t by_rows(const MatArg& x, const MatArg& w, const Epilogue& e, int64_t rows, int k, int n, hipStream_t s) {
+  const int64_t across = div_up(n, 64);
+  if (rows <= 16 || across * div_up(rows, 32) < 128) return go<XT, 1, NARROW>(x, w, e, rows, k, n, s);
+  return across * div_up(rows, 64) < 128 ? go<XT, 2, NARROW>(x, w, e, rows, k, n, s) : go<XT, 4, NARROW>(x, w, e, rows, k, n, s);
 }
 
 // ------------------------------------------------------------- by tiles, x in MX4 or MX8
@@ -489,14 +516,17 @@ hipError_t launch_linear_mx4(const MatArg& x, const MatArg& w, const float* bias
   if (rows_fwd_takes(k, n) && rows > 16) return launch_rows_mx4(x, w, e, rows, k, n, s);
   GSK_PROF("linear_mx4", s);
   const int64_t tiles = int64_t(div_up(n, 128)) * div_up(rows, 128);
+  // up to 64 tiles leave most of the card idle (700 rows 4096 to 1024 from MX8, 48 tiles: 28 us, by
+  // tiles 31; 700 rows 1024 to 4096, 192 tiles, 16 us)
   if (tiles > 64) {
     if (x.type == GS_MAT_MX4) return by_tiles<GS_MAT_MX4>(x, w, e, rows, k, n, s);
     if (x.type == GS_MAT_MX8 && k % 16 == 0 && buffer_ok(x)) return by_tiles<GS_MAT_MX8>(x, w, e, rows, k, n, s);
     return launch_tile_nt(w, x, n, rows, k, e, s);
   }
-  if (x.type == GS_MAT_MX4) return go<GS_MAT_MX4, false>(x, w, e, rows, k, n, s);
-  if (x.type == GS_MAT_MX8) return k < 16 ? go<GS_MAT_MX8, true>(x, w, e, rows, k, n, s) : go<GS_MAT_MX8, false>(x, w, e, rows, k, n, s);
-  return k < 16 ? go<GS_MAT_BF16, true>(x, w, e, rows, k, n, s) : go<GS_MAT_BF16, false>(x, w, e, rows, k, n, s);
+  if (x.type == GS_MAT_MX4) return by_rows<GS_MAT_MX4, false>(x, w, e, rows, k, n, s);
+  if (x.type == GS_MAT_MX8)
+    return k < 16 ? by_rows<GS_MAT_MX8, true>(x, w, e, rows, k, n, s) : by_rows<GS_MAT_MX8, false>(x, w, e, rows, k, n, s);
+  return k < 16 ? by_rows<GS_MAT_BF16, true>(x, w, e, rows, k, n, s) : by_rows<GS_MAT_BF16, false>(x, w, e, rows, k, n, s);
 }
 
 }  // namespace gsk
