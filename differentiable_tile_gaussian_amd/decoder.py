@@ -1,7 +1,8 @@
 """A network that decodes a feature row per Gaussian into some of its parameters.
 
 Residual feed-forward blocks over the rows and a linear head, every operator a library call
-(gs_rmsnorm_*, gs_linear_*, gs_mx8_*); torch holds the buffers.  Per block, with h the residual
+(gs_rmsnorm_*, gs_linear_*, gs_mx8_*; gs_lookup_* for rows that Gaussians share, gs_clip_grads before an
+update, gs_mx4_* to serve the trained network); torch holds the buffers.  Per block, with h the residual
 stream and f the block's branch:
 
     h = h + f_previous;  a = norm(h);  u = silu(a W1^T + b1);  f = u W2^T + b2
@@ -108,6 +109,89 @@ class FeatureDecoder:
             gs.gs_rmsnorm_bwd(self.da, self.h8[i], p[f"norm.{i}"], self.rstd[i], self.dh, g[f"norm.{i}"], self.ws,
                               dres=self.dh)
         return self.dh
+
+
+class FeatureTable:
+    """Feature rows that Gaussians share (a codebook): forward(index) gives a decoder its rows, times
+    `scale`, and backward(dx) takes their gradient back to the table.  parameters and grads: "table",
+    [entries][width] float32.  A Gaussian whose index is outside the table has a row of zeros."""
+
+    def __init__(self, entries, width, scale=1.0, device="cuda", seed=0):
+        self.entries, self.width, self.scale, self.device = entries, width, scale, device
+        g = torch.Generator().manual_seed(seed)
+        self.parameters = {"table": torch.randn(entries, width, generator=g).to(device)}
+        self.grads = {"table": torch.zeros_like(self.parameters["table"])}
+        self.rows = -1
+
+    def forward(self, index):
+        """index [rows] (int32 or int64) -> [rows][width] bfloat16, overwritten by the next call."""
+        rows = index.shape[0]
+        if rows != self.rows:
+            self.rows = -1   # until both are there
+            self.x = torch.empty((rows, self.width), dtype=torch.bfloat16, device=self.device)
+            self.ws = gs.workspace(gs.GS_WS_LOOKUP_BWD, n=rows, W=self.width, H=self.entries, device=self.device)
+            self.rows = rows
+        self.index = index
+        gs.gs_lookup_fwd(self.parameters["table"], index, self.x, scale=self.scale)
+        return self.x
+
+    def backward(self, dx):
+        """dx [rows][width] (float32 or bfloat16): fills grads for the last forward's index."""
+        gs.gs_lookup_bwd(dx, self.index, self.grads["table"], self.ws, scale=self.scale)
+
+
+class ServedDecoder:
+    """A trained FeatureDecoder's forward pass with its weights in 4 bits (MX4), an eighth of their
+    float32 size.  Between its layers there are 8 bits (MX8), written by the norm and by the first
+    layer of a block as the next layer reads them; nothing is kept for a backward pass."""
+
+    def __init__(self, net):
+        self.net, self.rows = net, -1
+        self.w4 = {}
+        for name, w in net.parameters.items():
+            if w.dim() == 2:
+                self.w4[name] = gs.mx4_empty(*w.shape, w.device)
+                gs.gs_mx4_pack(w, self.w4[name])
+
+    def _reserve(self, rows):
+        if rows == self.rows:
+            return
+        self.rows = -1   # until all of them are there
+        n, dev = self.net, self.net.device
+        self.h, self.f = (torch.empty((rows, n.width), dtype=torch.bfloat16, device=dev) for _ in range(2))
+        self.a8, self.u8 = gs.mx8_empty(rows, n.width, dev), gs.mx8_empty(rows, n.hidden, dev)
+        self.y = torch.empty((rows, n.outputs), device=dev)
+        self.rows = rows
+
+    def forward(self, x, base=None):
+        """As FeatureDecoder.forward."""
+        self._reserve(x.shape[0])
+        n, p, w = self.net, self.net.parameters, self.w4
+        branch = None
+        for i in range(n.blocks):
+            gs.gs_rmsnorm_fwd(x if i == 0 else self.h, p[f"norm.{i}"], EPS, self.a8, residual=branch, h=self.h)
+            gs.gs_linear_fwd(self.a8, w[f"w1.{i}"], self.u8, bias=p[f"b1.{i}"], act="silu")
+            gs.gs_linear_fwd(self.u8, w[f"w2.{i}"], self.f, bias=p[f"b2.{i}"])
+            branch = self.f
+        gs.gs_rmsnorm_fwd(self.h if n.blocks else x, p["norm.head"], EPS, self.a8, residual=branch)
+        gs.gs_linear_fwd(self.a8, w["w3"], self.y, bias=p["b3"], residual=base)
+        return self.y
+
+
+class GradientClip:
+    """Clipping by the global norm of gradients in buffers that stay where they are (a decoder's
+    and a table's grads, with others): calling it scales all of them by min(1, max_norm / norm) and
+    returns the norm (device tensor of one value, overwritten by the next call)."""
+
+    def __init__(self, tensors, max_norm):
+        self.lists, self.max_norm = gs.Matrices(tensors), max_norm
+        device = self.lists.tensors[0].device if self.lists.tensors else "cuda"
+        self.norm = torch.zeros(1, device=device)
+        self.ws = gs.workspace(gs.GS_WS_CLIP_GRADS, device=device)
+
+    def __call__(self):
+        gs.gs_clip_grads(self.lists, self.max_norm, self.norm, self.ws)
+        return self.norm
 
 
 def planes_to_rows(blocked, n, first, count, out=None):

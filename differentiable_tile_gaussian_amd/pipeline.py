@@ -106,6 +106,7 @@ class Pipeline:
         self.t = 0
         self.pairs = 0
         self.projected_for = None   # set by a fused update that projected for the next step's camera
+        self.clip_ws = None         # clip()'s workspace
         self.dstats = None          # [n][2] density statistics, once enable_density_stats() is called
 
     def planar(self, blocked: torch.Tensor) -> torch.Tensor:
@@ -151,6 +152,17 @@ class Pipeline:
         gs.gs_render_bwd(self.params, self.deg, self.proj, self.vals, self.ranges, self.pairs, cam, self.T, self.nc,
                          self.dLdI, self.gscreen, self.grads, self.ws_render, cfg=self.cfg)
 
+    def clip(self, max_norm, others=()):
+        """Scales this step's parameter gradients, and `others` (tensors, of a network in front of
+        the rasteriser) with them, by min(1, max_norm / norm), norm being that of all of them
+        together.  Returns the norm (device tensor of one value, overwritten by the next call)."""
+        if self.clip_ws is None:
+            self.clip_ws = gs.workspace(gs.GS_WS_CLIP_GRADS, device=self.params.device)
+            self.grad_norm = torch.zeros(1, dtype=torch.float32, device=self.params.device)
+        gs.gs_clip_grads(gs.blocked_matrices(self.grads, self.n, self.deg) + list(others), max_norm, self.grad_norm,
+                         self.clip_ws)
+        return self.grad_norm
+
     def adam(self):
         self.t += 1
         gs.gs_adam_step(self.params, self.grads, self.m, self.v, self.n, self.deg, self.rates(self.t), self.betas[0],
@@ -175,13 +187,14 @@ class Pipeline:
         self.projected_for = next_cam
 
     def step(self, cam: gs.GsCamera, target: torch.Tensor, adam: bool = True, fused: bool = True,
-             next_cam: gs.GsCamera = None):
-        """One training step; with next_cam (fused Adam only) the update also projects
+             next_cam: gs.GsCamera = None, max_grad_norm: float = None):
+        """One training step; with max_grad_norm the gradients are clipped to that global norm
+        before the update, which then is not the fused one; with next_cam (fused Adam only) the update also projects
         the scene for the camera of the following step.  With density statistics enabled,
         the step's observations are added to them (from this step's projection and
         screen gradients, before any projection for the next camera replaces them)."""
         self.forward(cam)
-        if adam and fused:
+        if adam and fused and max_grad_norm is None:
             self.backward_adam(cam, target, next_cam)   # accumulates the statistics when projecting
             if self.dstats is not None and next_cam is None:
                 gs.gs_densify_accumulate(self.proj, self.gscreen, self.dstats)
@@ -189,14 +202,16 @@ class Pipeline:
         self.backward(cam, target)
         if self.dstats is not None:
             gs.gs_densify_accumulate(self.proj, self.gscreen, self.dstats)
+        if max_grad_norm is not None:
+            self.clip(max_grad_norm)
         if adam:
             self.adam()
         return self.loss
 
-    def step_views(self, cams, targets):
+    def step_views(self, cams, targets, max_grad_norm: float = None):
         """One training step over several views: each view is rendered and differentiated
         in turn, its parameter gradients added into one buffer with weight 1/B (the mean
-        over the B views), then one Adam update.  Returns the losses of the views
+        over the B views), clipped to max_grad_norm if given, then one Adam update.  Returns the losses of the views
         ([B][3]: total, L1, SSIM).  With density statistics enabled, every view's
         observations are added to them."""
         B = len(cams)
@@ -210,6 +225,8 @@ class Pipeline:
                                       cfg=self.cfg)
             if self.dstats is not None:
                 gs.gs_densify_accumulate(self.proj, self.gscreen, self.dstats)
+        if max_grad_norm is not None:
+            self.clip(max_grad_norm)
         self.adam()
         return losses
 
