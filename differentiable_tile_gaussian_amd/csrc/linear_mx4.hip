@@ -77,6 +77,20 @@ struct BlockX {
   }
 };
 
+// run(x, epilogue, rows) for parts of at most `most` rows, which a launch takes.
+template <class Run>
+hipError_t in_parts(const MatArg& x, const Epilogue& e, int64_t rows, int64_t most, Run run) {
+  for (int64_t first = 0; first < rows; first += most) {
+    const int64_t count = rows - first < most ? rows - first : most;
+    Epilogue part = e;
+    part.r = rows_from(e.r, first);
+    part.y = rows_from(e.y, first);
+    const hipError_t no = run(x.type == GS_MAT_MX4 ? mx4_rows_from(x, first) : rows_from(x, first), part, count);
+    if (no != hipSuccess) return no;
+  }
+  return hipSuccess;
+}
+
 // ------------------------------------------------------------- few rows, and any size and type
 
 // A block takes 64 columns by 16 QT rows and its waves share the contraction, each loading its
@@ -180,17 +194,11 @@ __global__ void __launch_bounds__(waves_of(QT) * 64) linear_mx4_kernel(MatArg W,
 
 template <int XT, int QT, bool NARROW>
 hipError_t go(const MatArg& x, const MatArg& w, const Epilogue& e, int64_t rows, int k, int n, hipStream_t s) {
-  const int64_t most = kMaxBlocks / 2 * (16 * QT);   // rows of one launch
-  for (int64_t first = 0; first < rows; first += most) {
-    const int64_t count = rows - first < most ? rows - first : most;
-    Epilogue part = e;
-    part.r = rows_from(e.r, first);
-    part.y = rows_from(e.y, first);
-    const MatArg xp = XT == GS_MAT_MX4 ? mx4_rows_from(x, first) : rows_from(x, first);
+  return in_parts(x, e, rows, kMaxBlocks / 2 * (16 * QT), [&](const MatArg& part, const Epilogue& to, int64_t count) {
     linear_mx4_kernel<XT, QT, NARROW>
-        <<<dim3(div_up(count, 16 * QT), div_up(n, 64)), waves_of(QT) * 64, 0, s>>>(w, xp, n, count, k, part);
-  }
-  return hipGetLastError();
+        <<<dim3(div_up(count, 16 * QT), div_up(n, 64)), waves_of(QT) * 64, 0, s>>>(w, part, n, count, k, to);
+    return hipGetLastError();
+  });
 }
 
 // Rows of a block: 16 where there are no more, else the more the fewer blocks are left idle.
@@ -474,6 +482,10 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_mx4_kernel(MatArg W, Mat
       float v[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) v[j] = acc[i][j / 4][j % 4] + bias[j];
+      if (n < 16) {   // absent columns are what LDS held, and a block in MX8 takes them for zero
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = j < n ? v[j] : 0.0f;
+      }
       finish16<false, kNone, kAny>(e, row, col, v, row < nq ? n : 0);
     }
     stores = p0 + T::BP <= np && q0 + T::BQ <= nq;
@@ -489,17 +501,11 @@ hipError_t go_tiles(const MatArg& x, const MatArg& w, const Epilogue& e, int64_t
   static LdsLimit limit;
   if (const hipError_t no = limit.allow(kernel, sizeof(typename T::Lds)); no != hipSuccess) return no;
   const int ptiles = int(div_up(n, 128));
-  const int64_t most = (kMaxBlocks - 8) / ptiles * T::BQ;   // rows of one launch
-  for (int64_t first = 0; first < rows; first += most) {
-    const int64_t count = rows - first < most ? rows - first : most;
-    Epilogue part = e;
-    part.r = rows_from(e.r, first);
-    part.y = rows_from(e.y, first);
+  return in_parts(x, e, rows, (kMaxBlocks - 8) / ptiles * T::BQ, [&](const MatArg& part, const Epilogue& to, int64_t count) {
     const int tiles = int(ptiles * int64_t(div_up(count, T::BQ))), turns = (tiles + 7) / 8 * 8;
-    kernel<<<turns < 512 ? turns : 512, kTileThreads, sizeof(typename T::Lds), s>>>(
-        w, XT == GS_MAT_MX4 ? mx4_rows_from(x, first) : rows_from(x, first), n, count, k, part, ptiles, tiles);
-  }
-  return hipGetLastError();
+    kernel<<<turns < 512 ? turns : 512, kTileThreads, sizeof(typename T::Lds), s>>>(w, part, n, count, k, to, ptiles, tiles);
+    return hipGetLastError();
+  });
 }
 
 template <int XT>
@@ -521,7 +527,8 @@ hipError_t launch_linear_mx4(const MatArg& x, const MatArg& w, const float* bias
   if (tiles > 64) {
     if (x.type == GS_MAT_MX4) return by_tiles<GS_MAT_MX4>(x, w, e, rows, k, n, s);
     if (x.type == GS_MAT_MX8 && k % 16 == 0 && buffer_ok(x)) return by_tiles<GS_MAT_MX8>(x, w, e, rows, k, n, s);
-    return launch_tile_nt(w, x, n, rows, k, e, s);
+    return in_parts(x, e, rows, (kMaxBlocks - 8) / div_up(n, 128) * 64,
+                    [&](const MatArg& part, const Epilogue& to, int64_t count) { return launch_tile_nt(w, part, n, count, k, to, s); });
   }
   if (x.type == GS_MAT_MX4) return by_rows<GS_MAT_MX4, false>(x, w, e, rows, k, n, s);
   if (x.type == GS_MAT_MX8)

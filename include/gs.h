@@ -454,7 +454,8 @@ int32_t gs_relocate(float* params, float* m, float* v, int64_t n, int32_t sh_deg
  * data may be NULL; sums over the rows are then zero.
  *
  * Outputs must not share memory with inputs or each other, except where a call says that one
- * may be the input itself.  No call uses atomics: the results are reproducible bit for bit.
+ * may be the input itself.  No result depends on the order of atomics: all are reproducible bit
+ * for bit.
  * Every call only enqueues. */
 typedef struct gs_matrix {
   void* data;

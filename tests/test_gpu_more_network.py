@@ -140,6 +140,55 @@ def test_linear_mx4_without_bias_and_large_values(gs):
             within(y, x64 @ w64.t(), (x64.abs() @ w64.abs().t()) * 162 * SUM, (ex, ew, xk))
 
 
+@pytest.mark.parametrize("rows,k,n", [(1200, 272, 1000), (3000, 1040, 700), (1100, 128, 1024), (4200, 512, 400)])
+@pytest.mark.parametrize("pad,offset", [(4, 0), (0, 4), (12, 8), (1, 0)])
+def test_linear_mx4_by_tiles_from_rows_of_any_alignment(gs, rows, k, n, pad, offset):
+    """Rows of x in MX8 that start at multiples of 4, 8 or 1 bytes, and scales of any pitch."""
+    g = rng("align4", rows, k, n)
+    (x, x64), (w, w64) = given(gs, normal(g, rows, k), "mx8", pad, offset), mx4_of(gs, normal(g, n, k, scale=k ** -0.5), pad % 3, behind=3)
+    y = output(gs, rows, n, "f32", pad, offset)
+    gs.gs_linear_fwd(x, w, y)
+    within(y, x64 @ w64.t(), (x64.abs() @ w64.abs().t()) * (k + 2) * SUM, "y")
+    assert untouched(y, rows, n)
+
+
+@pytest.mark.parametrize("xk", ["mx8", "mx4"])
+@pytest.mark.parametrize("rows,k,n", [(1200, 272, 1007), (300, 640, 33), (20, 96, 7), (4000, 128, 113)])
+def test_absent_columns_do_not_reach_a_block(gs, xk, rows, k, n):
+    """y in MX8 of zero weights is zero with the smallest scale, whatever was computed before."""
+    g = rng("absent4", rows, k, n)
+    x, _ = operand(gs, normal(g, rows, k) * 1e30, xk)
+    y = output(gs, rows, n, "mx8")
+    gs.gs_linear_fwd(x, mx4_of(gs, normal(g, n, k))[0], y)
+    gs.gs_linear_fwd(x, mx4_of(gs, torch.zeros(n, k))[0], y)
+    assert bool((y.scales.view(torch.uint8) == 1).all()) and bool(((y.q.view(torch.uint8) & 0x7f) == 0).all())
+
+
+def test_linear_mx4_tiles_take_turns(gs):
+    """More tiles than blocks, and tiles of a single step, of which the loads of several are under way
+    at once: every tile has its own bias, scales and rows."""
+    g = torch.Generator(device="cuda").manual_seed(11)
+    for k in (32, 128, 160, 256, 300, 544):
+        x, w = torch.randn(20_000, k, generator=g, device="cuda"), torch.randn(900, k, generator=g, device="cuda")
+        b = torch.randn(900, generator=g, device="cuda") * 10
+        w4, x4 = gs.mx4_empty(900, k), gs.mx4_empty(20_000, k)
+        gs.gs_mx4_pack(w, w4)
+        gs.gs_mx4_pack(x, x4)
+        x8 = gs.mx8_empty(20_000, k)
+        gs.gs_mx8_pack(x, x8)
+        wv = torch.empty_like(w)
+        gs.gs_mx4_unpack(w4, wv)
+        for q, unpack in ((x4, gs.gs_mx4_unpack), (x8, gs.gs_mx8_unpack)):
+            xv, y = torch.empty_like(x), torch.empty(20_000, 900, device="cuda")
+            unpack(q, xv)
+            gs.gs_linear_fwd(q, w4, y, bias=b)
+            want, mag = xv.double() @ wv.double().t() + b.double(), xv.double().abs() @ wv.double().abs().t() + b.double().abs()
+            assert bool(((y.double() - want).abs() <= mag * (k + 2) * SUM).all()), k
+            again = torch.empty_like(y)
+            gs.gs_linear_fwd(q, w4, again, bias=b)
+            assert torch.equal(again, y)
+
+
 # ------------------------------------------------------------------------------- lookup
 
 LOOKUP_SHAPES = [(1, 1, 1), (1, 7, 32), (5, 3, 7), (64, 10, 8), (65, 1, 64), (63, 200, 59), (1000, 64, 128), (4097, 33, 3),
