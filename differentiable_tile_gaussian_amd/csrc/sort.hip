@@ -256,6 +256,110 @@ __global__ void __launch_bounds__(kSortThreads) index_upsweep_kernel(PassIn in, 
   radix_upsweep<SRC, ITEMS>(in, kNoPlan, shift, mask, hist);
 }
 
+// Few places: all passes of an index sort in one block, in LDS.  Each of the 16 waves ranks its 256
+// consecutive places by ballots as the downsweep does; one launch in place of three a pass.  A whole
+// gradient of 4000 rows takes 23-26 us with it (64 to 65536 entries), one of 5000 rows, by the passes,
+// 32-41.  The other blocks clear the entries' marks.
+constexpr int kSmallThreads = 1024, kSmallWaves = kSmallThreads / 64, kSmallRounds = 4;
+constexpr uint32_t kSmallMost = kSmallThreads * kSmallRounds;
+constexpr int kSmallBits = 8;
+
+template <int SRC>
+__global__ void __launch_bounds__(kSmallThreads) index_small_kernel(PassIn in, int all, uint32_t* __restrict__ keys_out,
+                                                                     uint32_t* __restrict__ vals_out, uint4* marks, int64_t marks16) {
+  __shared__ uint32_t s_key[2][kSmallMost];
+  __shared__ uint16_t s_val[2][kSmallMost];
+  __shared__ uint16_t s_whist[kSmallWaves][1 << kSmallBits];   // a wave's digit counts, then starts (<= 4096)
+  __shared__ uint32_t s_wave[(1 << kSmallBits) / 64];
+  const int tid = threadIdx.x, lane = __lane_id(), wave = tid >> 6;
+  if (blockIdx.x > 0) {
+    const int64_t first = int64_t(blockIdx.x - 1) * kSmallMost;
+#pragma unroll
+    for (int r = 0; r < kSmallRounds; ++r) {
+      const int64_t i = first + r * kSmallThreads + tid;
+      if (i < marks16) marks[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    return;
+  }
+  const uint32_t first = wave * (64u * kSmallRounds) + lane;
+#pragma unroll
+  for (int r = 0; r < kSmallRounds; ++r) {
+    uint32_t key, val;
+    load_item<SRC>(in, min(first + r * 64u, in.count - 1), key, val);
+    s_key[0][first + r * 64u] = key;
+    s_val[0][first + r * 64u] = uint16_t(val);
+  }
+  const uint64_t lt_mask = (uint64_t(1) << lane) - 1;
+  int now = 0;
+  for (int shift = 0; shift < all; shift += kSmallBits, now ^= 1) {
+    const int nbits = min(kSmallBits, all - shift);
+    const uint32_t mask = (1u << nbits) - 1u;
+    for (int i = tid; i < kSmallWaves << kSmallBits; i += kSmallThreads) (&s_whist[0][0])[i] = 0;
+    __syncthreads();
+    uint32_t key[kSmallRounds], rk[kSmallRounds];
+#pragma unroll
+    for (int r = 0; r < kSmallRounds; ++r) key[r] = s_key[now][first + r * 64u];
+#pragma unroll
+    for (int r = 0; r < kSmallRounds; ++r) {
+      const bool valid = first + r * 64u < in.count;
+      const uint32_t d = (key[r] >> shift) & mask;
+      uint64_t peers = __ballot(valid);
+      for (int b = 0; b < nbits; ++b) {
+        const bool bit = (d >> b) & 1u;
+        const uint64_t m = __ballot(bit);
+        peers &= bit ? m : ~m;
+      }
+      const uint32_t before = valid ? uint32_t(s_whist[wave][d]) : 0u;
+      const uint32_t rank = __popcll(peers & lt_mask);
+      // (one wave's LDS operations are performed in order)
+      if (valid && rank == 0) s_whist[wave][d] = uint16_t(before + uint32_t(__popcll(peers)));
+      rk[r] = before + rank;
+    }
+    __syncthreads();
+    // a digit's start: the smaller digits' places, and for a wave those of the earlier waves
+    uint32_t count = 0, scan = 0;
+    if (tid < 1 << kSmallBits) {
+#pragma unroll
+      for (int w = 0; w < kSmallWaves; ++w) count += s_whist[w][tid];
+      scan = count;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t a = __shfl_up(scan, d, 64);
+        if (lane >= d) scan += a;
+      }
+      if (lane == 63) s_wave[wave] = scan;
+    }
+    __syncthreads();
+    if (tid < 1 << kSmallBits) {
+      uint32_t at = scan - count;
+      for (int w = 0; w < wave; ++w) at += s_wave[w];
+#pragma unroll
+      for (int w = 0; w < kSmallWaves; ++w) {
+        const uint32_t c = s_whist[w][tid];
+        s_whist[w][tid] = uint16_t(at);
+        at += c;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kSmallRounds; ++r) {
+      if (first + r * 64u >= in.count) continue;
+      const uint32_t to = s_whist[wave][(key[r] >> shift) & mask] + rk[r];
+      s_key[now ^ 1][to] = key[r];
+      s_val[now ^ 1][to] = s_val[now][first + r * 64u];
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int r = 0; r < kSmallRounds; ++r) {
+    const uint32_t i = first + r * 64u;
+    if (i < in.count) {
+      keys_out[i] = s_key[now][i];
+      vals_out[i] = s_val[now][i];
+    }
+  }
+}
+
 // Blocks (digit d, segment s): hist_scan[d][b] = sum of hist[d][b'] over b' < b, rowtot[d]
 // the row sum.  A row is cut into segments of kScanStepGroups groups (2048 blocks), one block
 // each: the block sums the row's complete groups before its segment, then takes the segment
@@ -884,6 +988,13 @@ hipError_t launch_sort_index(const void* index, bool wide, uint32_t count, uint3
   IndexWs w;
   carve_index(ws, count, &w);
   const int all = std::max(1, bits_for(entries)), passes = (all + kDigitBits - 1) / kDigitBits;
+  if (count <= kSmallMost) {
+    GSK_PROF("index_small", s);
+    const PassIn in{static_cast<const uint32_t*>(index), nullptr, nullptr, nullptr, entries, count, nullptr};
+    const auto kernel = wide ? &index_small_kernel<kFromIndex64> : &index_small_kernel<kFromIndex>;
+    kernel<<<1 + div_up(m16, kSmallMost), kSmallThreads, 0, s>>>(in, all, keys, vals, m, m16);
+    return hipGetLastError();
+  }
   const int low = (all + passes - 1) / passes;   // as evenly as the tile sort's
   for (int pass = 0; pass < passes; ++pass) {
     const bool last = (passes - 1 - pass) % 2 == 0;   // passes that write keys and vals

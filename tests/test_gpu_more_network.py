@@ -245,6 +245,21 @@ def test_lookup_gradient(gs, rows, entries, cols, dk, tk, how, dtype, pad, offse
     assert torch.equal(again, out)                                     # the same bits
 
 
+@pytest.mark.parametrize("rows", [2, 255, 256, 257, 4095, 4096, 4097])
+@pytest.mark.parametrize("entries", [1, 2, 255, 256, 65_535, 70_000])
+def test_lookup_gradient_sorted_in_one_block(gs, rows, entries):
+    """Around the most places that are sorted in one block: small whole numbers have one sum, exactly."""
+    g = rng("lookupsmall", rows, entries)
+    index = torch.randint(-1, entries + 1, (rows,), generator=g)
+    dy = torch.randint(-8, 9, (rows, 8), generator=g).float()        # sums exact in float32
+    out = torch.empty(entries, 8, device="cuda")
+    ws = gs.workspace(gs.GS_WS_LOOKUP_BWD, n=rows, W=8, H=entries).fill_(0xff)
+    for dtype in (torch.int32, torch.int64):
+        gs.gs_lookup_bwd(dy.cuda(), index.to(dtype).cuda(), out.fill_(7.0), ws)
+        used = (index >= 0) & (index < entries)
+        assert torch.equal(out.cpu(), torch.zeros(entries, 8).index_add(0, index[used], dy[used]))
+
+
 def test_lookup_keeps_bad_values_to_their_entries(gs):
     """Rows of no entry may hold anything; a NaN reaches its own entry alone."""
     g = rng("badlookup")
