@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kSortThreads) index_upsweep_kernel(PassIn in, 
 // Few places: all passes of an index sort in one block, in LDS.  Each of the 16 waves ranks its 256
 // consecutive places by ballots as the downsweep does; one launch in place of three a pass.  A whole
 // gradient of 4000 rows takes 23-26 us with it (64 to 65536 entries), one of 5000 rows, by the passes,
-// 32-41.  The other blocks clear the entries' marks.
+// 29-41.  The other blocks clear the entries' marks.
 constexpr int kSmallThreads = 1024, kSmallWaves = kSmallThreads / 64, kSmallRounds = 4;
 constexpr uint32_t kSmallMost = kSmallThreads * kSmallRounds;
 constexpr int kSmallBits = 8;
@@ -444,7 +444,12 @@ __global__ void __launch_bounds__(kSortThreads) radix_scan_kernel(DepthPlan dp, 
 // Gaussians).  The depth plan's last pass writes no keys; it looks every value (a
 // Gaussian id) up in val_rect and writes the Gaussian's tile rectangle and tile count
 // beside it.
-template <int SRC, int ITEMS = kSortItems>
+//
+// COUNTS: hist_scan holds the upsweep's own counts of at most kHistGroup blocks, rowtot is not used, and
+// each block adds what it needs of them: 512 bytes a digit, from the cache, in place of a launch
+// between (a gradient of 100,003 rows to 4096 entries, digits of 7 and 6 bits: 43 to 39 us; to 65536, 9 and
+// 8 bits, 48 either way).
+template <int SRC, int ITEMS = kSortItems, bool COUNTS = false>
 __global__ void __launch_bounds__(kSortThreads) radix_downsweep_kernel(
     PassIn in, DepthPlan dp, int shift, uint32_t mask, int nb, const uint32_t* __restrict__ hist_scan,
     const uint32_t* __restrict__ rowtot, uint32_t* keys_out, uint32_t* vals_out, uint32_t* __restrict__ count_out,
@@ -470,11 +475,59 @@ __global__ void __launch_bounds__(kSortThreads) radix_downsweep_kernel(
   const int d0 = 2 * tid;   // this thread's two digits
   // the digit bases: exclusive prefix of the row totals, plus the earlier blocks' counts
   // of the digit (block 0 also stores the number of items)
+  if constexpr (COUNTS) {
+    // eight lanes a digit, 16 counts each
+    constexpr int kDigits = kSortThreads / 8, kLoads = kHistGroup / 8 / 4;
+    static_assert(kTileItems >= kRadix && kHistGroup == 128, "places of 16, by eights");
+    constexpr int kTurn = 4;   // digits of a thread loaded together
+    const int part = tid % 8;
+    for (int first = tid / 8; first <= int(mask) + tid / 8; first += kTurn * kDigits) {
+      uint4 c[kTurn][kLoads];
+#pragma unroll
+      for (int u = 0; u < kTurn; ++u) {
+        const int d = min(first + u * kDigits, int(mask));
+        const uint4* row = reinterpret_cast<const uint4*>(hist_scan + size_t(d) * kHistGroup) + part;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) c[u][j] = row[j * 8];
+      }
+#pragma unroll
+      for (int u = 0; u < kTurn; ++u) {
+        const int d = first + u * kDigits;
+        uint32_t before = 0u, total = 0u;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+          const uint32_t each[4] = {c[u][j].x, c[u][j].y, c[u][j].z, c[u][j].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t place = (j * 8 + part) * 4 + i, b = place % 16 * 8 + place / 16;   // hist_at
+            total += b < uint32_t(nb) ? each[i] : 0u;
+            before += b < blockIdx.x ? each[i] : 0u;
+          }
+        }
+#pragma unroll
+        for (int step = 1; step < 8; step <<= 1) {
+          before += __shfl_xor(before, step, 64);
+          total += __shfl_xor(total, step, 64);
+        }
+        if (part == 0 && d <= int(mask)) {
+          s_keys[d] = before;
+          s_vals[d] = total;
+        }
+      }
+    }
+    __syncthreads();
+  }
   {
     // digits above mask have no rows (and no items)
     const bool u0 = uint32_t(d0) <= mask, u1 = uint32_t(d0 + 1) <= mask;
-    const uint32_t g0 = u0 ? hist_scan[hist_at(d0, blockIdx.x)] : 0u, g1 = u1 ? hist_scan[hist_at(d0 + 1, blockIdx.x)] : 0u;
-    const uint32_t r0 = u0 ? rowtot[d0] : 0u, r1 = u1 ? rowtot[d0 + 1] : 0u;
+    uint32_t g0, g1, r0, r1;
+    if constexpr (COUNTS) {
+      g0 = u0 ? s_keys[d0] : 0u, g1 = u1 ? s_keys[d0 + 1] : 0u;
+      r0 = u0 ? s_vals[d0] : 0u, r1 = u1 ? s_vals[d0 + 1] : 0u;
+    } else {
+      g0 = u0 ? hist_scan[hist_at(d0, blockIdx.x)] : 0u, g1 = u1 ? hist_scan[hist_at(d0 + 1, blockIdx.x)] : 0u;
+      r0 = u0 ? rowtot[d0] : 0u, r1 = u1 ? rowtot[d0 + 1] : 0u;
+    }
     uint32_t all_total, unused;
     const uint32_t pre = block_scan2(r0 + r1, 0u, s_scan, all_total, unused).x;
     if (count_out && blockIdx.x == 0 && tid == 0) *count_out = all_total;
@@ -957,6 +1010,12 @@ hipError_t index_pass(const PassIn& in, int nb, int shift, int bits, const Radix
   {
     GSK_PROF("index_upsweep", s);
     index_upsweep_kernel<SRC, ITEMS><<<nb, kSortThreads, 0, s>>>(in, shift, mask, w.hist, marks, marks16);
+  }
+  if (ITEMS == kIndexItems && nb <= kHistGroup) {
+    GSK_PROF("radix_downsweep", s);
+    radix_downsweep_kernel<SRC, kIndexItems, true><<<nb, kSortThreads, 0, s>>>(in, kNoPlan, shift, mask, nb, w.hist, nullptr, keys_out,
+                                                                              vals_out, nullptr, nullptr, nullptr, nullptr);
+    return hipGetLastError();
   }
   {
     GSK_PROF("radix_scan", s);

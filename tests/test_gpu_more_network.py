@@ -245,10 +245,11 @@ def test_lookup_gradient(gs, rows, entries, cols, dk, tk, how, dtype, pad, offse
     assert torch.equal(again, out)                                     # the same bits
 
 
-@pytest.mark.parametrize("rows", [2, 255, 256, 257, 4095, 4096, 4097])
+@pytest.mark.parametrize("rows", [2, 255, 256, 257, 4095, 4096, 4097, 131_072, 131_073])
 @pytest.mark.parametrize("entries", [1, 2, 255, 256, 65_535, 70_000])
-def test_lookup_gradient_sorted_in_one_block(gs, rows, entries):
-    """Around the most places that are sorted in one block: small whole numbers have one sum, exactly."""
+def test_lookup_gradient_sorted_in_few_launches(gs, rows, entries):
+    """Around the most places that are sorted in one block, and in two launches a pass: small whole numbers
+    have one sum, exactly."""
     g = rng("lookupsmall", rows, entries)
     index = torch.randint(-1, entries + 1, (rows,), generator=g)
     dy = torch.randint(-8, 9, (rows, 8), generator=g).float()        # sums exact in float32
