@@ -6,6 +6,8 @@
 // a mean over an image are small), and the vector units do float64 at float32's rate.  In the second every
 // block adds those sums itself, in the same order, instead of waiting for a kernel between.
 // Matrices are cut into pieces of 16384 elements; a matrix whose rows are adjacent is one row.
+// 708 MB of gradients (3M Gaussians and a decoder): 127 us for the norm (5.6 TB/s), 269 to clip
+// them (5.3); the gradients of a small network, 1 MB: 6.5 and 6.2 us, latency.
 #include "clip.h"
 #include "matrix.h"
 #include "profile.h"

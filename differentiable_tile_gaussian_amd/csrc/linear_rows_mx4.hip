@@ -1,5 +1,7 @@
 // Linear layers of narrow width over many rows with the weight in MX4: linear_rows.hip's kernels,
 // the weight decoded once a block on its way to LDS.  x is decoded in registers; y may be MX8.
+// Bounded by HBM: 1,000,003 rows 128 to 128 with silu from and to MX8 take 70 us (3.8 TB/s over
+// 264 MB), from MX8 to bfloat16 107, from MX4 to bfloat16 87.
 #include "linear_rows.h"
 
 namespace gsk {

