@@ -6,8 +6,9 @@
 // a mean over an image are small), and the vector units do float64 at float32's rate.  In the second every
 // block adds those sums itself, in the same order, instead of waiting for a kernel between.
 // Matrices are cut into pieces of 16384 elements; a matrix whose rows are adjacent is one row.
-// 708 MB of gradients (3M Gaussians and a decoder): 127 us for the norm (5.6 TB/s), 269 to clip
-// them (5.3); the gradients of a small network, 1 MB: 6.5 and 6.2 us, latency.
+// 708 MB of gradients (3M Gaussians and a decoder): 126 us for the norm (5.6 TB/s), 270 to clip
+// them (5.3); the gradients of a small network, 1 MB: 5.3 and 4.9 us, latency (6.5 and 6.2 where a block finds
+// its part by a loop over them).
 #include "clip.h"
 #include "matrix.h"
 #include "profile.h"
@@ -41,8 +42,10 @@ struct Piece {
 };
 
 __device__ __forceinline__ Piece piece_of(const List& l, int64_t piece) {
-  int i = 0;
-  while (i + 1 < l.count && piece >= l.piece[i + 1]) ++i;
+  // the parts behind the first that begin at or before it, counted by the lanes
+  const int lane = __lane_id();
+  const int64_t begin = l.piece[lane < kParts ? lane : kParts];
+  const int i = __popcll(__ballot(lane > 0 && lane < l.count && piece >= begin));
   Piece x;
   x.p = l.part[i];
   const int64_t a_row = (x.p.cols + 7) / 8, first = (piece - l.piece[i]) * kPiece;
