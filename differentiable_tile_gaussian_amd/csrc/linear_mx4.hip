@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(waves_of(QT) * 64) linear_mx4_kernel(MatArg W,
       u32x4 wq[4], xq[QT];
       uint32_t wsc[4], xsc[QT];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) wq[t] = w[t].q, wsc[t] = w[t].scale;
+      for (int t = 0; t < 4; ++t) wq[t] = mx4_keep(w[t].q, left), wsc[t] = w[t].scale;
 #pragma unroll
       for (int i = 0; i < QT; ++i) xq[i] = mx4_keep(x[i].q, left), xsc[i] = x[i].scale;
       fetch(s + kWaves);
@@ -426,10 +426,12 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_mx4_kernel(MatArg W, Mat
             xsc[sub][i] = xscale[sub * 4 + i * (64 * kParts)];
           }
         }
-        if (nk % 128 && s == steps - 1) {   // x ends inside (what W holds behind its end meets zeros)
+        if (nk % 128 && s == steps - 1) {   // the rows end inside (with zeros alone in x, an infinity behind W's end would count)
 #pragma unroll
           for (int sub = 0; sub < kSub; ++sub) {
             const int left = nk - ((s * kSub + sub) * 4 + g) * 32;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) wf[sub][t] = mx4_keep(wf[sub][t], left);
 #pragma unroll
             for (int i = 0; i < QT; ++i) {
               if constexpr (kX4) {

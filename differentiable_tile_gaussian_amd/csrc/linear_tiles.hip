@@ -74,6 +74,10 @@ struct Unit<GS_MAT_MX4> {
     a = buffer_load8(data, off);
     scale = buffer_load1(scales, soff);
   }
+  __device__ void keep(int n) {
+    a[0] = mx4_keep8(a[0], n);
+    a[1] = mx4_keep8(a[1], n - 8);
+  }
   __device__ void operands(u32x4& p, u32x4& q) const {
     const float s = mx8_scale(scale);
     p = __builtin_bit_cast(u32x4, mx4_to_bf16x8(a[0], s));
@@ -84,7 +88,7 @@ struct Unit<GS_MAT_MX4> {
 // ------------------------------------------------- contraction contiguous in both operands
 
 // out(q, p) = sum_k Q(q, k) P(p, k) for the rows q of Q (bfloat16 or MX8) and p of P
-// (bfloat16, or MX4, whose blocks are whole: what they hold behind nk meets zeros of Q).  kWhole: nk is a multiple of 16 and both are in buffers' reach.  An LDS row is 64 k, 128 bytes, whose 16-byte pieces are
+// (bfloat16, or MX4).  kWhole: nk is a multiple of 16 and both are in buffers' reach.  An LDS row is 64 k, 128 bytes, whose 16-byte pieces are
 // permuted by the row's number so that a fragment read's 16 rows fall into different banks;
 // P's rows are stored so that a lane's four result tiles are 16 consecutive columns.
 template <int PTYPE, int QTYPE, int QT, int D, Reach HOW>
@@ -155,12 +159,13 @@ __global__ void __launch_bounds__(kThreads) tile_nt_kernel(MatArg P, MatArg Q, i
     *reinterpret_cast<u32x4*>(at + r * 128 + ((piece * 2) ^ s) * 16) = a;
     *reinterpret_cast<u32x4*>(at + r * 128 + ((piece * 2 + 1) ^ s) * 16) = b;
   };
-  auto stage = [&](int d, uint8_t* at) {
+  auto stage = [&](int d, uint8_t* at, int k0) {
     u32x4 a, b;
 #pragma unroll
     for (int u = 0; u < BP / 64; ++u) {
       const int r = u * 64 + row;
       if constexpr (!WHOLE && !kP4) pr[d][u].settle();
+      if constexpr (!WHOLE && kP4) pr[d][u].keep(nk - k0 - piece * 16);
       pr[d][u].operands(a, b);
       put(at, (r & ~63) | ((r & 12) << 2) | ((r & 48) >> 2) | (r & 3), a, b);
     }
@@ -181,7 +186,7 @@ __global__ void __launch_bounds__(kThreads) tile_nt_kernel(MatArg P, MatArg Q, i
   const int frag0 = r16 * 128 + (g ^ sw) * 16, frag1 = r16 * 128 + ((g + 4) ^ sw) * 16;
   // loads of D steps are in flight: step s + 1 + d in set (s + d) % D
   fetch(0, 0);
-  stage(0, lds);
+  stage(0, lds, 0);
 #pragma unroll
   for (int d = 0; d < D; ++d) fetch(d, (d + 1) * 64);
   const int steps = (nk + 63) / 64;
@@ -201,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) tile_nt_kernel(MatArg P, MatArg Q, i
 #pragma unroll
         for (int i = 0; i < QT; ++i) qf[kk][i] = *reinterpret_cast<const bf16x8*>(at + (BP + (wq * QT + i) * 16) * 128);
       }
-      stage(d, lds + (~s & 1) * kStep);   // past the end: zeros, not read
+      stage(d, lds + (~s & 1) * kStep, (s + 1) * 64);   // past the end: zeros, not read
       fetch(d, (s + 1 + D) * 64);
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk)

@@ -164,6 +164,28 @@ def test_absent_columns_do_not_reach_a_block(gs, xk, rows, k, n):
     assert bool((y.scales.view(torch.uint8) == 1).all()) and bool(((y.q.view(torch.uint8) & 0x7f) == 0).all())
 
 
+@pytest.mark.parametrize("xk", ["bf16", "mx8", "mx4"])
+@pytest.mark.parametrize("rows,k,n", [(1, 5, 40), (5, 300, 40), (300, 270, 130), (100, 40, 48), (90, 48, 64), (90, 37, 35),
+                                      (1200, 400, 1000), (1200, 392, 1000), (1200, 389, 1000), (4000, 333, 300)])
+def test_linear_mx4_takes_nothing_from_behind_a_row(gs, xk, rows, k, n):
+    """The last block's columns that exist are zeros, those behind them are codes that its scale makes
+    infinite in bfloat16: y is what the blocks in front of it give."""
+    print("behind4", xk, rows, k, n, flush=True)
+    g = rng("behind4", xk, rows, k, n)
+    x, x64 = operand(gs, normal(g, rows, k), xk)
+    wv, last = normal(g, n, k), k // 32 * 32
+    wv[:, last:] = 0
+    w, w64 = mx4_of(gs, wv)
+    w.q[:, (k + 1) // 2:] = 0xff
+    if k % 2:
+        w.q[:, k // 2] = 0xf0
+    w.scales.view(torch.uint8)[:, -1] = 254
+    y = torch.empty(rows, n, device="cuda")
+    gs.gs_linear_fwd(x, w, y)
+    want, mag = x64 @ w64.t(), x64.abs() @ w64.abs().t()
+    assert bool(((y.cpu().double() - want).abs() <= mag * (k + 2) * SUM).all())
+
+
 def test_linear_mx4_tiles_take_turns(gs):
     """More tiles than blocks, and tiles of a single step, of which the loads of several are under way
     at once: every tile has its own bias, scales and rows."""
