@@ -143,15 +143,27 @@ class FeatureTable:
 class ServedDecoder:
     """A trained FeatureDecoder's forward pass with its weights in 4 bits (MX4), an eighth of their
     float32 size.  Between its layers there are 8 bits (MX8), written by the norm and by the first
-    layer of a block as the next layer reads them; nothing is kept for a backward pass."""
+    layer of a block as the next layer reads them; nothing is kept for a backward pass.  It serves the
+    network as it was when this was made: weights, biases and norms are copies, which refresh()
+    renews after further training."""
 
     def __init__(self, net):
         self.net, self.rows = net, -1
-        self.w4 = {}
-        for name, w in net.parameters.items():
-            if w.dim() == 2:
-                self.w4[name] = gs.mx4_empty(*w.shape, w.device)
-                gs.gs_mx4_pack(w, self.w4[name])
+        self.w4, self.vectors = {}, {}
+        for name, v in net.parameters.items():
+            if v.dim() == 2:
+                self.w4[name] = gs.mx4_empty(*v.shape, v.device)
+            else:
+                self.vectors[name] = torch.empty_like(v)
+        self.refresh()
+
+    def refresh(self):
+        """Takes the network's present parameters, into the buffers that are there."""
+        for name, v in self.net.parameters.items():
+            if v.dim() == 2:
+                gs.gs_mx4_pack(v, self.w4[name])
+            else:
+                self.vectors[name].copy_(v.detach())
 
     def _reserve(self, rows):
         if rows == self.rows:
@@ -166,7 +178,7 @@ class ServedDecoder:
     def forward(self, x, base=None):
         """As FeatureDecoder.forward."""
         self._reserve(x.shape[0])
-        n, p, w = self.net, self.net.parameters, self.w4
+        n, p, w = self.net, self.vectors, self.w4
         branch = None
         for i in range(n.blocks):
             gs.gs_rmsnorm_fwd(x if i == 0 else self.h, p[f"norm.{i}"], EPS, self.a8, residual=branch, h=self.h)
