@@ -113,6 +113,11 @@ __device__ inline void load_bias16(const float* bias, int col, int n, float (&v)
   for (int j = 0; j < 16; ++j) v[j] = j < n ? v[j] : 0.0f;
 }
 
+// The store instructions of store16 where all 16 columns exist: float32 four of 16 bytes, bfloat16 two,
+// MX8 one and its scales'.  A kernel whose waits count memory operations relies on no fewer being made; more only
+// make them longer.
+constexpr int stores16(int type) { return type == GS_MAT_F32 ? 4 : 2; }
+
 // v: x W^T (with the bias) for 16 columns of a row.  Z, Y: the types of z and y, or kAny,
 // or kNone for z.
 template <bool WHOLE, int Z, int Y>

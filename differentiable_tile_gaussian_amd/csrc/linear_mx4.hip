@@ -372,6 +372,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_mx4_kernel(MatArg W, Mat
 
   int turn = ahead, now = 0, half = 0, bias_at = 0;
   bool stores = false;   // the epilogue in front of this step has made all its stores
+  static_assert(stores16(GS_MAT_MX8) == stores16(GS_MAT_BF16), "one wait for both");
   const bool f32 = e.y.type == GS_MAT_F32;
   load_scales(turn, 0);
   point();
@@ -394,13 +395,13 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_mx4_kernel(MatArg W, Mat
         load_scales(next, 0);
       const int last = s0 + kSegment < steps ? s0 + kSegment : steps;
       for (int s = s0; s < last; ++s) {
-        // the stores are younger than the loads that this step needs
+        // the stores are younger than the loads that this step needs; memory operations end in order
         if (!stores)
           wait_loads_and_waves<kAhead>();
         else if (f32)
-          wait_loads_and_waves<kAhead + 4 * QT>();
+          wait_loads_and_waves<kAhead + stores16(GS_MAT_F32) * QT>();
         else
-          wait_loads_and_waves<kAhead + 2 * QT>();
+          wait_loads_and_waves<kAhead + stores16(GS_MAT_BF16) * QT>();
         stores = false;
         issue();
         const uint8_t* wdata = lds.stage[now] + wp * (4 * kSub * 1024);
