@@ -141,35 +141,6 @@ __device__ inline void finish16(const Epilogue& e, int64_t row, int col, float v
 
 // ------------------------------------------------------------- tile kernels
 
-// Ends a step: LDS writes done, all waves there; loads from memory stay in flight.
-__device__ inline void step_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
-// The order in which a step's instructions are issued: a few operand reads, then four matrix
-// instructions at a time with what the next ones need in between: an operand read or two, an
-// LDS write of the step to come, a load from memory.  (Left to itself the compiler puts the
-// writes first, and every wave waits for them in front of its first operand.)
-template <int READS, int WRITES, int LOADS, int GROUPS, int I = 0>
-__device__ inline void interleave() {
-  constexpr int kFirst = READS / 4, kRest = READS - kFirst, kOver = GROUPS - 2;
-  if constexpr (I == 0) __builtin_amdgcn_sched_group_barrier(0x100, kFirst, 0);
-  if constexpr (I < GROUPS) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
-    if constexpr (I < kOver) {
-      constexpr int reads = (I + 1) * kRest / kOver - I * kRest / kOver;
-      if constexpr (reads > 0) __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);
-    }
-    constexpr int writes = (I + 1) * WRITES / GROUPS - I * WRITES / GROUPS;
-    if constexpr (writes > 0) __builtin_amdgcn_sched_group_barrier(0x200, writes, 0);
-    constexpr int loads = (I + 1) * LOADS / GROUPS - I * LOADS / GROUPS;
-    if constexpr (loads > 0) __builtin_amdgcn_sched_group_barrier(0x020, loads, 0);
-    interleave<READS, WRITES, LOADS, GROUPS, I + 1>();
-  }
-}
-
 // Which tile a block takes: consecutive blocks go to different XCDs, each with its own L2, so
 // an XCD is given neighbouring tiles (the P tiles of one Q tile after another).
 __device__ inline int tile_of(int block, int tiles) {

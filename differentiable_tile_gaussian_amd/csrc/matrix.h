@@ -286,9 +286,6 @@ __device__ inline Buffer buffer_at(const void* p) {
 __device__ inline u32x4 buffer_load16(Buffer b, uint32_t off) {
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, int(off), 0, 0));
 }
-__device__ inline uint32_t buffer_load4(Buffer b, uint32_t off) {
-  return uint32_t(__builtin_amdgcn_raw_buffer_load_b32(b, int(off), 0, 0));
-}
 __device__ inline u32x2 buffer_load8(Buffer b, uint32_t off) {
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(b, int(off), 0, 0));
 }
