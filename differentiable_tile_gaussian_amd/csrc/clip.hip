@@ -8,7 +8,9 @@
 // Matrices are cut into pieces of 16384 elements; a matrix whose rows are adjacent is one row.
 // 708 MB of gradients (3M Gaussians and a decoder): 126 us for the norm (5.6 TB/s), 270 to clip
 // them (5.3); the gradients of a small network, 1 MB: 5.3 and 4.9 us, latency (6.5 and 6.2 where a block finds
-// its part by a loop over them).
+// its part by a loop over them).  A launch takes 32 matrices, and the norm's launches share its 2048 sums
+// evenly, so that long lists leave it few blocks at a time: 708 MB in 320 matrices 408 us for the norm,
+// in 1024 598 (1.2 TB/s).
 #include "clip.h"
 #include "matrix.h"
 #include "profile.h"

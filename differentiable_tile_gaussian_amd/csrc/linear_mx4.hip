@@ -229,9 +229,11 @@ hipError_t by_rows(const MatArg& x, const MatArg& w, const Epilogue& e, int64_t 
 // alignment), kParts of them at a time, into one of two places.
 //
 // 8160 rows 4096 to 1024 from MX8: 63 us (1090 TFLOP/s, the rate of the library's plain bfloat16
-// product of these sizes); bounded by the matrix cores with the decodes beside them.  8160 rows 1024 to
-// 4096 from MX4 with gelu: 46 us (1.5 PFLOP/s), of which gelu takes 9 and the stores 6; without both
-// and the loads 26 would be left, the steps' latency with two blocks a compute unit.
+// product of these sizes); by the counters (in a short run, at 77 us) the matrix cores are busy in 40 % of the cycles
+// and vector instructions, the decodes and theirs, issue in 39.  The weight of that form is still loaded 64 bytes of
+// a row at a time.  8160 rows 1024 to 4096 from MX4 with gelu: 46 us (1.5 PFLOP/s), of which gelu takes 9 and the
+// stores 6; without both and the loads 26 would be left, the steps' latency with two blocks a compute unit.  (In
+// a short run, at 54 us: matrix cores 13 % of the cycles, vector issue 41, 22 instructions a wave and result.)
 constexpr int kTileThreads = 256;
 
 template <int XT, int QT_>

@@ -1,7 +1,10 @@
 // Linear layers of narrow width over many rows with the weight in MX4: linear_rows.hip's kernels,
 // the weight decoded once a block on its way to LDS.  x is decoded in registers; y may be MX8.
-// Bounded by HBM: 1,000,003 rows 128 to 128 with silu from and to MX8 take 70 us (3.8 TB/s over
-// 264 MB), from MX8 to bfloat16 107, from MX4 to bfloat16 87.
+// 1,000,003 rows 128 to 128 with silu from and to MX8 take 70-72 us (3.7 TB/s over 264 MB, by the counters all that
+// moves), without it 57 (4.6; a copy of the same matrices 47): HBM beside the vector units, which issue
+// in 62 % of the cycles (10 instructions a wave and result) with the matrix cores busy in 19 %.  From MX8
+// to bfloat16 86-88 us without and with it (4.5 TB/s: HBM), from MX4 85, from bfloat16 102 (5.0), 48 columns
+// of float32 with a residual 119 (4.3).
 #include "linear_rows.h"
 
 namespace gsk {

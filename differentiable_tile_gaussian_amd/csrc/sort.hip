@@ -26,8 +26,8 @@
 //             XCD-aware order, below; rows for the pass's 2^bits digits only)
 //   scan      per digit, exclusive prefix along its row and the row total, a row taken in
 //             segments of 2048 blocks, one scan block each (the carry summed directly)
-//   downsweep the digit bases from the row totals; each wave ranks its 1024
-//             consecutive items against a wave-private digit histogram (64-lane ballots:
+//   downsweep the digit bases from the row totals; each wave ranks its 1024 (in index
+//             sorts of up to 4M places 256) consecutive items against a wave-private digit histogram (64-lane ballots:
 //             no match-any on CDNA, one ballot per digit bit gives each lane its peer
 //             mask), one barrier turns the four histograms into run starts, then a local
 //             reorder through LDS and a coalesced scatter.
@@ -49,7 +49,8 @@ constexpr int kWaves = kSortThreads / 64;
 constexpr int kSortItems = 16;
 constexpr int kSortTile = kSortThreads * kSortItems;   // 4096 items per block
 // Index sorts of up to 4M places take 1024 a block: they are short of blocks, not of histogram
-// (1M places in two passes: 4096 a block 60 us).
+// (1M places in two passes: 4096 a block 60 us).  A gradient of 4,194,304 rows of 48 takes 360 us
+// with it, of one row more, 4096 a block, 332.
 constexpr int kIndexItems = 4;
 constexpr int64_t kIndexMost = int64_t(1) << 22;
 constexpr int kDigitBits = 9;
@@ -543,7 +544,7 @@ __global__ void __launch_bounds__(kSortThreads) radix_downsweep_kernel(
   const uint32_t base = blockIdx.x * uint32_t(kTileItems);
   if (base >= count) return;   // uniform per block
   __syncthreads();
-  // Each wave ranks its own 1024 consecutive items, 64 per round, with a wave-private
+  // Each wave ranks its own kWaveItems consecutive items, 64 per round, with a wave-private
   // digit histogram: an item's rank among equal digits of its wave is the histogram
   // before its round plus its rank in the round (a ballot per digit bit gives each lane its peers;
   // CDNA has no match-any).  Waves, rounds and lanes follow the items' order, so the
@@ -613,7 +614,7 @@ __global__ void __launch_bounds__(kSortThreads) radix_downsweep_kernel(
     }
   }
   __syncthreads();
-  // out in sorted order, sixteen places per thread (the last depth pass's rectangle
+  // out in sorted order, ITEMS places per thread (the last depth pass's rectangle
   // gathers issued together)
   uint32_t okey[ITEMS], oval[ITEMS], dst[ITEMS];
 #pragma unroll
